@@ -447,6 +447,75 @@ dash_status dash_inverse_sqrt_ndb(const float* A, const float* s, int64_t N, int
 /* u_p = X_p g_p for p < P (X [P, B, B], g_pieces and u_pieces [P, B]; u must not alias g). */
 dash_status dash_apply_vec(const float* X, const float* g_pieces, int64_t P, int32_t B, float* u_pieces, void* stream);
 
+/* ---- Microscaled storage, and the products that read it ----
+ *
+ * The optimizer's largest tensors in fewer bits: a layer's input kept for the backward pass, the
+ * gradient tiles, the roots kept between root updates ([PT] Resultados Experimentais: DASH's roots and
+ * products run in lower precision; the pages name no format).  A row of a matrix is cut into groups
+ * of 32 consecutive elements (the last one padded with zeros) that share a power of two 2^e:
+ *   scale byte  e + 127; 255 for a group that held an Inf or a NaN (its codes are 0 and it reads back
+ *               as NaN);
+ *   element     DASH_MX_E2M1: 4 bits (sign, 2 exponent bits, 1 mantissa bit: 0 .5 1 1.5 2 3 4 6), two
+ *               to a byte, the even one in the low half; DASH_MX_E4M3: 8 bits (sign, 4, 3; largest 448).
+ * e is the least integer >= -127 with max|x| <= m 2^e, m the format's largest value, so nothing
+ * saturates; x 2^-e is rounded to the nearest element value, ties to the even code.
+ * A matrix of `rows` x `cols` is rows * ceil(cols / 32) * 32 (E4M3) or 16 (E2M1) bytes of codes, 16-byte
+ * aligned, and rows * ceil(cols / 32) scale bytes, both row-major; a stack of matrices follows one
+ * after the other. */
+typedef enum { DASH_MX_E2M1 = 0, DASH_MX_E4M3 = 1 } dash_mx_fmt;
+
+/* Quantise N matrices of rows x cols, row-major with row pitch ld >= cols, matrix n at src + n rows ld
+ * (elements of `type`: DASH_FP32, DASH_FP16 or DASH_BF16, aligned to their size; any ld).
+ *   codes, scales:     the rows in groups along cols, or both NULL;
+ *   codes_t, scales_t: the columns in groups along rows, i.e. the transpose (cols x rows) of each
+ *                      matrix quantised by rows, or both NULL; at least one pair is given.  Both pairs
+ *                      together read src once.
+ *   diag: NULL, or (rows == cols, else DASH_ERR_SHAPE) [N, rows] receives the diagonals in fp32 and
+ *         their codes are 0: a root's diagonal, far above the rest of its row, then neither sets its
+ *         group's scale nor loses its own precision. */
+dash_status dash_mx_quantize(const void* src, dash_prec type, int64_t N, int64_t rows, int64_t cols, int64_t ld,
+                             dash_mx_fmt fmt, void* codes, void* scales, void* codes_t, void* scales_t, float* diag,
+                             void* stream);
+
+/* The values of N microscaled matrices: dst (element type `type`, row pitch ld >= cols, matrix n at dst +
+ * n rows ld; columns from cols to ld are not written) = element times 2^e, plus diag[n][r] on the
+ * diagonal when diag is given (rows == cols), rounded to `type` once (exact in fp32 and, but for
+ * bfloat16's subnormals, in bf16 when diag is NULL). */
+dash_status dash_mx_dequantize(const void* codes, const void* scales, const float* diag, int64_t N, int64_t rows,
+                               int64_t cols, dash_mx_fmt fmt, dash_prec type, int64_t ld, void* dst, void* stream);
+
+/* dash_update_stats from microscaled gradient tiles Q ([TG] body: L and R from gradient products):
+ *   L_t <- beta L_t + (1 - beta) Q_t Q_t^T,   R_t <- beta R_t + (1 - beta) Q'_t^T Q'_t,
+ * Q_t the values of codes/scales (the rows of the NG tiles of B x B, groups along a row) and Q'_t^T those
+ * of codes_t/scales_t (their columns): both pairs as dash_mx_quantize writes them.  Products exact,
+ * sums in fp32.  A, beta and the rest as dash_update_stats; a NaN group makes the rows and columns of
+ * A that it enters NaN.  (Here and below, element values under 2^-126 may lose their low bits.) */
+dash_status dash_update_stats_mx(const void* codes, const void* scales, const void* codes_t, const void* scales_t,
+                                 int64_t NG, int32_t B, dash_mx_fmt fmt, float beta, float* A, void* stream);
+
+/* dash_apply with microscaled roots: U_t = (XL_t G_t) XR_t^T for t < NG, where XL_t and XR_t are the values
+ * of the row codes XL / XR [NG, B, B] plus, when given, their fp32 diagonals XL_diag / XR_diag [NG, B].
+ * (The roots are symmetric; the right one is read by rows, as stored, so that it enters transposed:
+ * the groups' rounding makes the two differ.)  G_stack, U_stack fp32, results to fp32 accuracy in the
+ * given root values.  ws: dash_workspace_size(DASH_OP_APPLY, NG, B, ...), as dash_apply. */
+dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL_diag, const void* XR,
+                          const void* XR_scales, const float* XR_diag, const float* G_stack, int64_t NG, int32_t B,
+                          dash_mx_fmt fmt, float* U_stack, void* ws, size_t ws_bytes, void* stream);
+
+/* A linear layer's weight gradient from its microscaled input, as gradient tiles: for the input's T
+ * tokens, W = dY^T Q with dY [T, out] (`type`, aligned to its element, any row pitch ldy >= out; rows
+ * that start on 16 bytes load fastest) the gradient of the layer's output and Q [T, in] the values of codes/scales (the input quantised by rows
+ * in the forward pass), written as dash_stack would stack an out x in weight: ceil(out/B) x ceil(in/B)
+ * tiles, the part of an edge tile outside the weight zero.  accumulate = 1 adds to the tiles that
+ * G_stack holds (earlier micro-batches; the padding keeps what it holds), 0 overwrites them.  dY
+ * enters exactly in every type, sums are fp32, and equal calls give equal bits.  T = 0 (dY, codes and
+ * scales may be NULL): an empty sum.
+ * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned. */
+dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, const void* codes, const void* scales,
+                               dash_mx_fmt fmt, int64_t T, int64_t out, int64_t in, int32_t B, int32_t accumulate,
+                               float* G_stack, void* ws, size_t ws_bytes, void* stream);
+dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, dash_prec type, size_t* bytes);
+
 /* Workspace bytes for an operation.  k_or_degree: the number of start vectors for
  * DASH_OP_SCALE (power iteration; Frobenius needs 0), ignored otherwise.  DASH_OP_STATS: 0, or
  * with DASH_FP32_SPLIT16 the bound per tile that dash_update_stats_ws keeps (N = tiles).

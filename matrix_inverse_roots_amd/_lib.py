@@ -17,6 +17,7 @@ DASH_FP32, DASH_FP16, DASH_BF16, DASH_FP32_SPLIT, DASH_FP32_SPLIT16 = 0, 1, 2, 3
 DASH_SCALE_FROBENIUS, DASH_SCALE_POWER = 0, 1
 (DASH_OP_SCALE, DASH_OP_NDB, DASH_OP_CN, DASH_OP_CHEB, DASH_OP_APPLY, DASH_OP_STATS, DASH_OP_EVD,
  DASH_OP_ROUTED) = range(8)
+DASH_MX_E2M1, DASH_MX_E4M3 = 0, 1
 
 
 class DashError(RuntimeError):
@@ -82,6 +83,12 @@ def library() -> ctypes.CDLL:
             "dash_update_stats_vec": (st, [vp, i64, i32, f32, vp, vp]),
             "dash_inverse_sqrt_ndb": (st, [vp, vp, i64, i32, i32, st, vp, vp, vp, vp, sz, vp]),
             "dash_apply_vec": (st, [vp, vp, i64, i32, vp, vp]),
+            "dash_mx_quantize": (st, [vp, st, i64, i64, i64, i64, st, vp, vp, vp, vp, vp, vp]),
+            "dash_mx_dequantize": (st, [vp, vp, vp, i64, i64, i64, st, st, i64, vp, vp]),
+            "dash_update_stats_mx": (st, [vp, vp, vp, vp, i64, i32, st, f32, vp, vp]),
+            "dash_apply_mx": (st, [vp, vp, vp, vp, vp, vp, vp, i64, i32, st, vp, vp, sz, vp]),
+            "dash_grad_stack_mx": (st, [vp, st, i64, vp, vp, st, i64, i64, i64, i32, i32, vp, vp, sz, vp]),
+            "dash_grad_stack_mx_workspace": (st, [i64, i64, i64, st, ctypes.POINTER(sz)]),
             "dash_workspace_size": (st, [st, i64, i32, st, i32, ctypes.POINTER(sz)]),
             "dash_solver_products": (i64, [st, i32, i32]),
             "dash_flops": (f64, [st, i64, i32, st, i32, i32]),
@@ -124,7 +131,7 @@ class _Args:
         return True
 
     def ptr(self, t, name, dtype="float32", numel=0):
-        """Pointer of tensor argument `name` of `dtype` ('float32', 'int32' or None for any) holding
+        """Pointer of tensor argument `name` of `dtype` ('float32', 'int32', 'uint8' or None for any) holding
         at least `numel` elements."""
         if t is None:
             return None
@@ -133,7 +140,7 @@ class _Args:
         if self._tensor(t, name):
             import torch
 
-            want = {"float32": torch.float32, "int32": torch.int32}.get(dtype)
+            want = {"float32": torch.float32, "int32": torch.int32, "uint8": torch.uint8}.get(dtype)
             if want is not None and t.dtype != want:
                 raise ValueError("%s: %s must be %s, got %s" % (self.call, name, dtype, t.dtype))
             if not t.is_contiguous():
@@ -167,6 +174,33 @@ class _Args:
             arr[i].ld = t.stride(0)
         return arr
 
+    def rows(self, t, name, N, rows, cols, type, ld):
+        """(pointer, dash_prec type, row pitch) of N row-major matrices of rows x cols, one after the
+        other: a tensor [rows, cols] (N = 1) or [N, rows, cols] of float32, float16 or bfloat16 with unit
+        column stride and matrices rows * pitch apart, or a raw pointer with type and ld given."""
+        if t is None or isinstance(t, int) or not self._tensor(t, name):
+            p = t if t is None or isinstance(t, int) else t.data_ptr()
+            return p, DASH_FP32 if type is None else type, cols if ld is None else ld
+        have = _prec_of(t.dtype)
+        if have is None or type not in (None, have):
+            raise ValueError("%s: %s must be float32, float16 or bfloat16, got %s" % (self.call, name, t.dtype))
+        if tuple(t.shape) not in (((rows, cols), (1, rows, cols)) if N == 1 else ((N, rows, cols),)):
+            raise ValueError("%s: %s must be [%d, %d, %d], got %s" % (self.call, name, N, rows, cols, tuple(t.shape)))
+        if t.numel() == 0:
+            return t.data_ptr(), have, cols
+        pitch = t.stride(-2) if rows > 1 else max(cols, t.stride(-2) if N == 1 else t.stride(0))
+        if (cols > 1 and t.stride(-1) != 1) or pitch < cols or (N > 1 and t.stride(0) != rows * pitch):
+            raise ValueError("%s: %s must be row-major with unit column stride" % (self.call, name))
+        if ld not in (None, pitch):
+            raise ValueError("%s: %s has a row pitch of %d, not %d" % (self.call, name, pitch, ld))
+        return t.data_ptr(), have, pitch
+
+    def codes(self, codes, scales, name, N, rows, cols, fmt):
+        """Pointers of the codes and scale bytes of N microscaled matrices of rows x cols."""
+        n = N * rows * -(-cols // 32)
+        return (self.ptr(codes, name, "uint8", n * (32 if fmt == DASH_MX_E4M3 else 16)),
+                self.ptr(scales, name + "_scales" if name else "scales", "uint8", n))
+
     def vecs(self, ts, name):
         """dash_vec descriptors of contiguous 1-D fp32 GPU vectors."""
         arr = (DashVec * len(ts))()
@@ -197,6 +231,13 @@ def _nbytes(t):
     if t is None or isinstance(t, int):
         return 0
     return t.numel() * t.element_size()
+
+
+def _prec_of(dtype):
+    """The dash_prec of a torch element type (None for others)."""
+    import torch
+
+    return {torch.float32: DASH_FP32, torch.float16: DASH_FP16, torch.bfloat16: DASH_BF16}.get(dtype)
 
 
 def _tiles(shapes, B):
@@ -528,3 +569,87 @@ def dash_apply_vec(X, g_pieces, P: int, B: int, u_pieces, stream=None):
     _check("dash_apply_vec",
            library().dash_apply_vec(a.ptr(X, "X", numel=P * B * B), a.ptr(g_pieces, "g_pieces", numel=P * B), P, B,
                                     a.ptr(u_pieces, "u_pieces", numel=P * B), a.stream(stream)))
+
+
+def mx_buffers(N: int, rows: int, cols: int, fmt: int, device="cuda"):
+    """(codes, scales): uint8 tensors [N, rows, bytes of a row] and [N, rows, groups] for N microscaled
+    matrices of rows x cols."""
+    import torch
+
+    g = -(-cols // 32)
+    return (torch.empty((N, rows, g * (32 if fmt == DASH_MX_E4M3 else 16)), dtype=torch.uint8, device=device),
+            torch.empty((N, rows, g), dtype=torch.uint8, device=device))
+
+
+def dash_mx_quantize(src, N: int, rows: int, cols: int, fmt: int, codes=None, scales=None, codes_t=None, scales_t=None,
+                     diag=None, type=None, ld=None, stream=None):
+    """src: a tensor [N, rows, cols] (or [rows, cols]); its element type and row pitch are taken from it
+    (a raw pointer takes type and ld)."""
+    a = _Args("dash_mx_quantize")
+    p, prec, pitch = a.rows(src, "src", N, rows, cols, type, ld)
+    c = a.codes(codes, scales, "codes", N, rows, cols, fmt)
+    ct = a.codes(codes_t, scales_t, "codes_t", N, cols, rows, fmt)
+    _check("dash_mx_quantize",
+           library().dash_mx_quantize(p, prec, N, rows, cols, pitch, fmt, *c, *ct, a.ptr(diag, "diag", numel=N * rows),
+                                      a.stream(stream)))
+
+
+def dash_mx_dequantize(codes, scales, N: int, rows: int, cols: int, fmt: int, dst, diag=None, type=None, ld=None,
+                       stream=None):
+    """dst: a tensor [N, rows, cols] (or [rows, cols]) of the wanted element type."""
+    a = _Args("dash_mx_dequantize")
+    c = a.codes(codes, scales, "codes", N, rows, cols, fmt)
+    p, prec, pitch = a.rows(dst, "dst", N, rows, cols, type, ld)
+    _check("dash_mx_dequantize",
+           library().dash_mx_dequantize(*c, a.ptr(diag, "diag", numel=N * rows), N, rows, cols, fmt, prec, pitch, p,
+                                        a.stream(stream)))
+
+
+def dash_update_stats_mx(codes, scales, codes_t, scales_t, NG: int, B: int, fmt: int, beta: float, A, stream=None):
+    a = _Args("dash_update_stats_mx")
+    c = a.codes(codes, scales, "codes", NG, B, B, fmt)
+    ct = a.codes(codes_t, scales_t, "codes_t", NG, B, B, fmt)
+    _check("dash_update_stats_mx",
+           library().dash_update_stats_mx(*c, *ct, NG, B, fmt, beta, a.ptr(A, "A", numel=2 * NG * B * B),
+                                          a.stream(stream)))
+
+
+def dash_apply_mx(XL, XL_scales, XR, XR_scales, G_stack, NG: int, B: int, fmt: int, U_stack, XL_diag=None, XR_diag=None,
+                  ws=None, stream=None):
+    a = _Args("dash_apply_mx")
+    n = NG * B * B
+    cl = a.codes(XL, XL_scales, "XL", NG, B, B, fmt)
+    cr = a.codes(XR, XR_scales, "XR", NG, B, B, fmt)
+    _check("dash_apply_mx",
+           library().dash_apply_mx(*cl, a.ptr(XL_diag, "XL_diag", numel=NG * B), *cr,
+                                   a.ptr(XR_diag, "XR_diag", numel=NG * B), a.ptr(G_stack, "G_stack", numel=n), NG, B,
+                                   fmt, a.ptr(U_stack, "U_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream)))
+
+
+def dash_grad_stack_mx_workspace(T: int, out_features: int, in_features: int, type: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("dash_grad_stack_mx_workspace",
+           library().dash_grad_stack_mx_workspace(T, out_features, in_features, type, ctypes.byref(out)))
+    return out.value
+
+
+def grad_stack_mx_workspace(T: int, out_features: int, in_features: int, dtype, device="cuda"):
+    """A byte tensor of the size dash_grad_stack_mx_workspace reports for dY of torch type `dtype` (None
+    when no workspace is needed)."""
+    import torch
+
+    n = dash_grad_stack_mx_workspace(T, out_features, in_features, _prec_of(dtype))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def dash_grad_stack_mx(dY, codes, scales, fmt: int, T: int, out_features: int, in_features: int, B: int, G_stack,
+                       accumulate: bool = False, type=None, ldy=None, ws=None, stream=None):
+    """dY: a tensor [T, out_features]; its element type and row pitch are taken from it (a raw pointer
+    takes type and ldy)."""
+    a = _Args("dash_grad_stack_mx")
+    p, prec, pitch = a.rows(dY, "dY", 1, T, out_features, type, ldy)
+    c = a.codes(codes, scales, "codes", 1, T, in_features, fmt)
+    n = _tiles([(out_features, in_features)], B) * B * B
+    _check("dash_grad_stack_mx",
+           library().dash_grad_stack_mx(p, prec, pitch, *c, fmt, T, out_features, in_features, B, int(bool(accumulate)),
+                                        a.ptr(G_stack, "G_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream)))

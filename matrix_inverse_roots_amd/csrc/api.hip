@@ -75,6 +75,28 @@ dash_status stats_args_check(const float* G_stack, int64_t NG, int32_t B, float 
   if (!valid_B(B)) return DASH_ERR_SHAPE;
   return DASH_OK;
 }
+// microscaled operands
+bool valid_fmt(dash_mx_fmt f) { return f == DASH_MX_E2M1 || f == DASH_MX_E4M3; }
+bool plain_type(dash_prec t) { return t == DASH_FP32 || t == DASH_FP16 || t == DASH_BF16; }
+bool mx_codes_ok(const void* codes, const void* scales) { return codes && scales && aligned(codes, 16); }
+// sides of at most 2^31 - 1, and 2^44 elements in all (32 times the memory of one GPU, in bytes): no
+// offset or count overflows 64 bits
+constexpr int64_t MX_MAX_SIDE = 0x7fffffff;
+constexpr double MX_MAX_ELEMENTS = 17592186044416.0;
+dash_status mx_shape_check(dash_prec type, int64_t N, int64_t rows, int64_t cols, int64_t ld, dash_mx_fmt fmt) {
+  if (!valid_fmt(fmt) || !plain_type(type) || !valid_N(N)) return DASH_ERR_INVALID_ARG;
+  if (rows < 1 || cols < 1 || rows > MX_MAX_SIDE || cols > MX_MAX_SIDE || ld < cols || ld > MX_MAX_SIDE)
+    return DASH_ERR_SHAPE;
+  return (double)N * (double)rows * (double)ld > MX_MAX_ELEMENTS ? DASH_ERR_SHAPE : DASH_OK;
+}
+dash_status grad_shape_check(int64_t T, int64_t out, int64_t in, int64_t ldy, dash_prec type) {
+  if (!plain_type(type)) return DASH_ERR_INVALID_ARG;
+  if (T < 0 || out < 1 || in < 1 || T > MX_MAX_SIDE || out > MX_MAX_SIDE || in > MX_MAX_SIDE || ldy < out ||
+      ldy > MX_MAX_SIDE)
+    return DASH_ERR_SHAPE;
+  const double most = (double)(T > out ? T : out) * (double)(ldy > in ? ldy : in);
+  return most > MX_MAX_ELEMENTS ? DASH_ERR_SHAPE : DASH_OK;
+}
 // apply: the intermediate stack T = XL G, and for two-piece binary16 products the bounds of XL, G
 // and XR per block and T's per-wave maxima
 size_t ws_apply(int64_t N, int B) {
@@ -1685,6 +1707,92 @@ dash_status dash_inverse_sqrt_ndb(const float* A, const float* s, int64_t N, int
   const dash_status r = ndb_call(c, A, false, true, iters, 0, true, X, nullptr);
   if (r != DASH_OK) return r;
   if (monitor) TRY(launch_monitor_finish(monitor, N * iters, B, st));
+  return DASH_OK;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Microscaled storage and the products that read it
+// ------------------------------------------------------------------------------------------------
+
+dash_status dash_mx_quantize(const void* src, dash_prec type, int64_t N, int64_t rows, int64_t cols, int64_t ld,
+                             dash_mx_fmt fmt, void* codes, void* scales, void* codes_t, void* scales_t, float* diag,
+                             void* stream) {
+  const dash_status st = mx_shape_check(type, N, rows, cols, ld, fmt);
+  if (st != DASH_OK) return st;
+  if (!src || !aligned(src, type == DASH_FP32 ? 4 : 2) || src == codes || src == codes_t) return DASH_ERR_INVALID_ARG;
+  if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return DASH_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(codes_t, 16) || (codes && codes == codes_t)) return DASH_ERR_INVALID_ARG;
+  if (diag && !aligned(diag, 4)) return DASH_ERR_INVALID_ARG;
+  if (diag && rows != cols) return DASH_ERR_SHAPE;
+  TRY(launch_mx_quantize(src, type, N, rows, cols, ld, fmt, codes, scales, codes_t, scales_t, diag, as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_mx_dequantize(const void* codes, const void* scales, const float* diag, int64_t N, int64_t rows,
+                               int64_t cols, dash_mx_fmt fmt, dash_prec type, int64_t ld, void* dst, void* stream) {
+  const dash_status st = mx_shape_check(type, N, rows, cols, ld, fmt);
+  if (st != DASH_OK) return st;
+  if (!mx_codes_ok(codes, scales) || !dst || !aligned(dst, type == DASH_FP32 ? 4 : 2) || dst == codes || dst == scales)
+    return DASH_ERR_INVALID_ARG;
+  if (diag && (!aligned(diag, 4) || diag == dst)) return DASH_ERR_INVALID_ARG;
+  if (diag && rows != cols) return DASH_ERR_SHAPE;
+  TRY(launch_mx_dequantize(codes, scales, diag, N, rows, cols, fmt, type, ld, dst, as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_update_stats_mx(const void* codes, const void* scales, const void* codes_t, const void* scales_t,
+                                 int64_t NG, int32_t B, dash_mx_fmt fmt, float beta, float* A, void* stream) {
+  if (!mx_codes_ok(codes, scales) || !mx_codes_ok(codes_t, scales_t) || !valid_fmt(fmt)) return DASH_ERR_INVALID_ARG;
+  if (A == codes || A == codes_t || A == scales || A == scales_t) return DASH_ERR_INVALID_ARG;
+  const dash_status chk = stats_args_check(A, NG, B, beta, A);
+  if (chk != DASH_OK) return chk;
+  TRY(launch_mx_stats(mx_codes(codes, scales, B, B, fmt), mx_codes(codes_t, scales_t, B, B, fmt), NG, B, fmt, beta, A,
+                      as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL_diag, const void* XR,
+                          const void* XR_scales, const float* XR_diag, const float* G_stack, int64_t NG, int32_t B,
+                          dash_mx_fmt fmt, float* U_stack, void* ws, size_t ws_bytes, void* stream) {
+  if (!mx_codes_ok(XL, XL_scales) || !mx_codes_ok(XR, XR_scales) || !valid_fmt(fmt)) return DASH_ERR_INVALID_ARG;
+  if (!G_stack || !U_stack || !aligned(G_stack, 16) || !aligned(U_stack, 16) || !valid_N(NG))
+    return DASH_ERR_INVALID_ARG;
+  if (U_stack == G_stack || U_stack == XL || U_stack == XR || U_stack == XL_diag || U_stack == XR_diag)
+    return DASH_ERR_INVALID_ARG;
+  if ((XL_diag && !aligned(XL_diag, 4)) || (XR_diag && !aligned(XR_diag, 4)))
+    return DASH_ERR_INVALID_ARG;
+  if (!valid_B(B)) return DASH_ERR_SHAPE;
+  if (!ws || !aligned(ws, 256) || ws_bytes < ws_apply(NG, B)) return DASH_ERR_WORKSPACE;
+  Carver cv{(char*)ws, ws_bytes};
+  float* T = (float*)cv.take(stack_bytes(NG, B, DASH_FP32));
+  hipStream_t st = as_stream(stream);
+  TRY(launch_mx_apply(mx_codes(XL, XL_scales, B, B, fmt), XL_diag, G_stack, NG, B, fmt, true, T, st));
+  TRY(launch_mx_apply(mx_codes(XR, XR_scales, B, B, fmt), XR_diag, T, NG, B, fmt, false, U_stack, st));
+  return DASH_OK;
+}
+
+dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, dash_prec type, size_t* bytes) {
+  if (!bytes) return DASH_ERR_INVALID_ARG;
+  const dash_status st = grad_shape_check(T, out, in, out, type);
+  if (st != DASH_OK) return st;
+  *bytes = mx_grad_workspace_bytes(T, out, in);
+  return DASH_OK;
+}
+
+dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, const void* codes, const void* scales,
+                               dash_mx_fmt fmt, int64_t T, int64_t out, int64_t in, int32_t B, int32_t accumulate,
+                               float* G_stack, void* ws, size_t ws_bytes, void* stream) {
+  const dash_status st = grad_shape_check(T, out, in, ldy, type);
+  if (st != DASH_OK) return st;
+  if (!valid_fmt(fmt) || accumulate < 0 || accumulate > 1) return DASH_ERR_INVALID_ARG;
+  if (T > 0 && (!dY || !aligned(dY, type == DASH_FP32 ? 4 : 2) || !mx_codes_ok(codes, scales)))
+    return DASH_ERR_INVALID_ARG;
+  if (!G_stack || !aligned(G_stack, 16) || G_stack == dY || G_stack == codes) return DASH_ERR_INVALID_ARG;
+  if (!valid_B(B)) return DASH_ERR_SHAPE;
+  const size_t need = mx_grad_workspace_bytes(T, out, in);
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return DASH_ERR_WORKSPACE;
+  TRY(launch_mx_grad(dY, type, ldy, mx_codes(codes, scales, T, in, fmt), fmt, T, out, in, B, accumulate != 0, G_stack, ws,
+                     as_stream(stream)));
   return DASH_OK;
 }
 

@@ -284,6 +284,55 @@ hipError_t launch_vec_copy(float* v, int64_t len, float* pieces, int B, bool to_
 hipError_t launch_vec_stats(const float* g, int64_t P, int B, float beta, float* L, hipStream_t stream);
 hipError_t launch_vec_apply(const float* X, const float* g, int64_t P, int B, float* u, hipStream_t stream);
 
+// Microscaled matrices (mx.hip): rows of codes (E4M3 a byte, E2M1 half a byte, padded to whole groups
+// of MX_GROUP) and one scale byte per group.  A stack of matrices is one list of rows.
+constexpr int MX_GROUP = 32;
+struct MxCodes {
+  const uint8_t* codes = nullptr;
+  const uint8_t* scales = nullptr;
+  int64_t rows = 0;        // rows per matrix
+  int64_t row_bytes = 0;   // bytes of a row's codes
+  int64_t row_groups = 0;  // groups (scale bytes) of a row
+};
+inline int64_t mx_row_groups(int64_t cols) { return (cols + MX_GROUP - 1) / MX_GROUP; }
+inline int64_t mx_row_bytes(int64_t cols, dash_mx_fmt fmt) {
+  return mx_row_groups(cols) * (fmt == DASH_MX_E4M3 ? MX_GROUP : MX_GROUP / 2);
+}
+inline MxCodes mx_codes(const void* codes, const void* scales, int64_t rows, int64_t cols, dash_mx_fmt fmt) {
+  MxCodes q;
+  q.codes = (const uint8_t*)codes;
+  q.scales = (const uint8_t*)scales;
+  q.rows = rows;
+  q.row_bytes = mx_row_bytes(cols, fmt);
+  q.row_groups = mx_row_groups(cols);
+  return q;
+}
+// A floating operand: matrix b at p + b stride, rows ld apart, `cols` columns (in elements); vec: every
+// row starts on 16 bytes
+struct MxFloats {
+  const void* p = nullptr;
+  int64_t ld = 0, stride = 0, cols = 0;
+  bool vec = true;
+};
+// Codes and scales of the rows (codes, scales) and/or the columns (codes_t, scales_t) of N matrices, one
+// after the other with row pitch ld.  diag (square matrices): receives the diagonals, whose codes are 0.
+hipError_t launch_mx_quantize(const void* src, dash_prec type, int64_t N, int64_t rows, int64_t cols, int64_t ld,
+                              dash_mx_fmt fmt, void* codes, void* scales, void* codes_t, void* scales_t, float* diag,
+                              hipStream_t stream);
+hipError_t launch_mx_dequantize(const void* codes, const void* scales, const float* diag, int64_t N, int64_t rows,
+                                int64_t cols, dash_mx_fmt fmt, dash_prec type, int64_t ld, void* dst,
+                                hipStream_t stream);
+// Products with microscaled operands (mx_gemm.hip): A = [L; R] <- beta A + (1 - beta) [Q Q^T; Q' Q'^T] from
+// the codes of G's rows and columns; out = Q X (left) or X Q^T, with the root's fp32 diagonal; gradient
+// tiles dY^T Q in launch_tile_copy's order (ws: mx_grad_workspace_bytes).
+hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG, int B, dash_mx_fmt fmt, float beta,
+                           float* A, hipStream_t stream);
+hipError_t launch_mx_apply(const MxCodes& q, const float* diag, const float* X, int64_t NG, int B, dash_mx_fmt fmt,
+                           bool left, float* out, hipStream_t stream);
+size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in);
+hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
+                          int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // dash_scale's argument checks short of the workspace (DASH_OK or the status dash_scale returns).

@@ -55,48 +55,6 @@ namespace {
 template <int V>
 using IC = std::integral_constant<int, V>;
 
-// x = p0 + p1 + p2 for the 8 elements lo[0..3], hi[0..3]
-__device__ __forceinline__ void split3(const f32x4& lo, const f32x4& hi, bf16x8& p0, bf16x8& p1, bf16x8& p2) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float x = q < 4 ? lo[q] : hi[q - 4];
-    const __bf16 a0 = (__bf16)x;
-    const float r1 = x - (float)a0;
-    const __bf16 a1 = (__bf16)r1;
-    p0[q] = a0;
-    p1[q] = a1;
-    p2[q] = (__bf16)(r1 - (float)a1);
-  }
-}
-
-// power-of-two exponent e with 2^13 <= 2^e m < 2^14 (m = 0, inf or NaN: 0)
-__device__ __forceinline__ int top_exp(float m) {
-  int e;
-  frexpf(m, &e);  // m = f 2^e, f in [0.5, 1)
-  return (m > 0.f && isfinite(m)) ? 14 - e : 0;
-}
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// H2 pieces of the 8 elements lo[0..3], hi[0..3] of 2^e x: x0 = f16(x'), x1 = f16(x' - x0).  The
-// difference is formed by one mixed-precision fma of x0 (binary16 source) with -1; m1 holds -1 where
-// the compiler cannot see it, so that it keeps the fma instead of a conversion and a subtraction.
-__device__ __forceinline__ void split2(const f32x4& lo, const f32x4& hi, int e, float m1, f16x8& p0, f16x8& p1) {
-#pragma unroll
-  for (int q = 0; q < 8; q += 2) {
-    const float a = ldexpf(q < 4 ? lo[q] : hi[q - 4], e);
-    const float b = ldexpf(q < 4 ? lo[q + 1] : hi[q - 3], e);
-    const f16x2 h = __builtin_convertvector(f32x2{a, b}, f16x2);
-    const f32x2 r = {__builtin_fmaf((float)h[0], m1, a), __builtin_fmaf((float)h[1], m1, b)};
-    const f16x2 l = __builtin_convertvector(r, f16x2);
-    p0[q] = h[0];
-    p0[q + 1] = h[1];
-    p1[q] = l[0];
-    p1[q + 1] = l[1];
-  }
-}
-
 // LDS rows are 16 bfloat16 (two 16-byte chunks); a row swaps its chunks when bit 2 xor bit 3 of its
 // index is set, so that the 16-byte reads of 16 consecutive rows (one chunk each, the lanes the LDS
 // serves together) fall on 16 distinct 16-byte slots of its 64 banks

@@ -1,0 +1,747 @@
+// mx_gemm.hip -- batched products with microscaled operands: the Shampoo statistics from
+// microscaled gradient tiles, the preconditioned update with microscaled roots, and gradient tiles
+// from a layer's microscaled input.
+//
+// A microscaled element is c 2^(s - 127) with c an E2M1 or E4M3 value (at most 4 significant bits)
+// and s its group's scale byte.  bfloat16 has 8 significant bits and fp32's exponent range, so every
+// element is a bfloat16 number exactly (elements below 2^-126 lose their lowest bits to bfloat16's
+// subnormals), scale included, and the 32x32x16 bfloat16 MFMA forms products of two elements exactly
+// and sums them in fp32.  (The scaled 8-bit MFMA, at twice the rate, drops bits below the largest
+// addend of its 64: sums of 4096 positive E4M3 products came out 7e-5 low, a hundred times fp32's own
+// error, so it is not used.)  A floating operand beside a microscaled one is cut into bfloat16
+// pieces that add up to it exactly (one for bfloat16, two for binary16, three for fp32), and each
+// piece multiplies the one microscaled piece: exact products again, accumulated in fp32.
+//
+// One kernel frame: an output tile of TILE x TILE, 2 TILE threads, k-slices of 32 (one scale group
+// along k), a register ring of two slices and an LDS double buffer of bfloat16 planes, one per
+// piece.  An operand whose k is contiguous in memory sits in LDS as [row][32 k], one whose k is the
+// slow axis as [k][TILE], read back k-major by the transposing LDS load.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "gemm_common.hpp"
+
+namespace dash {
+namespace gemm {
+namespace {
+
+template <int V>
+using IC = std::integral_constant<int, V>;
+
+constexpr int BK = 32;  // k-slice: one scale group
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------------------------------------
+// Elements
+// ------------------------------------------------------------------------------------------------
+
+// The scale as the conversion instructions take it: only the exponent field of the fp32 operand
+// counts, so a scale byte in that field is the scale (255 makes the results NaN).
+__device__ __forceinline__ float scale_of(unsigned byte) { return __builtin_bit_cast(float, byte << 23); }
+
+// 8 consecutive elements to bfloat16, from 8 bytes (E4M3) or 4 bytes (E2M1)
+template <int F>
+struct Elem;
+template <>
+struct Elem<DASH_MX_E4M3> {
+  typedef u32x2 raw8;
+  static constexpr int BITS = 8;
+  static __device__ __forceinline__ bf16x8 decode(raw8 r, float s) {
+    bf16x8 v;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[w], s, false);
+      const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[w], s, true);
+      v[4 * w] = a[0];
+      v[4 * w + 1] = a[1];
+      v[4 * w + 2] = b[0];
+      v[4 * w + 3] = b[1];
+    }
+    return v;
+  }
+};
+template <>
+struct Elem<DASH_MX_E2M1> {
+  typedef unsigned raw8;
+  static constexpr int BITS = 4;
+  static __device__ __forceinline__ bf16x8 decode(raw8 r, float s) {
+    bf16x8 v;
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 3);
+    v[0] = a[0];
+    v[1] = a[1];
+    v[2] = b[0];
+    v[3] = b[1];
+    v[4] = c[0];
+    v[5] = c[1];
+    v[6] = d[0];
+    v[7] = d[1];
+    return v;
+  }
+};
+
+// x = p[0] + p[1] + ... for 8 elements: each piece the nearest bfloat16 to what is left, every
+// difference exact in fp32 (see split3).  Two pieces hold binary16's 11 significant bits.
+template <int P>
+__device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&p)[P]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float left = x[q];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const __bf16 a = (__bf16)left;
+      p[i][q] = a;
+      left -= (float)a;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// LDS planes: TILE x 32 bfloat16
+// ------------------------------------------------------------------------------------------------
+
+// [row][32 k]: rows of four 16-byte chunks; the chunk index is xored with bits 2-3 of the row, so
+// the 16-byte reads of 16 consecutive rows fall on 16 distinct slots of the 64 banks
+__device__ __forceinline__ int kc_at(int row, int chunk) { return row * BK + 8 * (chunk ^ ((row >> 2) & 3)); }
+
+// [k][TILE]: the 64-byte block of 32 columns is xored with k % 4 (with 64 columns, two blocks to a row
+// of half the banks, with bit 1 of k), so the four rows that one transposing load reads fall on distinct
+// banks
+template <int TILE>
+__device__ __forceinline__ int ks_at(int k, int col) {
+  const int turn = TILE == 64 ? (k >> 1) & 1 : k & 3;
+  return k * TILE + ((((col >> 5) ^ turn) << 5) | (col & 31));
+}
+
+// The MFMA operand of rows (columns) base .. base + 31, k = 16 ks .. 16 ks + 15: lane l holds row
+// l % 32, k = 8 (l / 32) .. + 7.
+template <int TILE, bool KS>
+__device__ __forceinline__ bf16x8 fragment(const __bf16* plane, int base, int ks, int lane) {
+  if constexpr (!KS) {
+    return *(const bf16x8*)&plane[kc_at(base + (lane & 31), 2 * ks + (lane >> 5))];
+  } else {
+    // transposing load: in each group of 16 lanes, lane 4 r + c points at four columns of row r; lane i
+    // receives column i of the group's four rows
+    const int k = 16 * ks + 8 * (lane >> 5) + ((lane & 15) >> 2);
+    const int col = base + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&plane[ks_at<TILE>(k, col)]);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&plane[ks_at<TILE>(k + 4, col)]);
+    const bf16x4 a = __builtin_bit_cast(bf16x4, lo), b = __builtin_bit_cast(bf16x4, hi);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Operand loaders.  init: the thread's place in the tile whose first row (column) is r0; load: slice
+// kt into ring slot `slot`; store: a slot into LDS planes.
+// ------------------------------------------------------------------------------------------------
+
+// Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
+template <int F, int TILE>
+struct CodesK {
+  static constexpr int PIECES = 1;
+  static constexpr bool KS = false;
+  typedef typename Elem<F>::raw8 raw8;
+  const uint8_t *c, *s;
+  raw8 r[2][2];
+  unsigned sc[2];
+  int row, half;
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int64_t, int64_t, int tid) {
+    row = tid >> 1;
+    half = tid & 1;
+    const int64_t at = b * q.rows + r0 + row;
+    c = q.codes + at * q.row_bytes + half * (2 * Elem<F>::BITS);
+    s = q.scales + at * q.row_groups;
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void load(int64_t kt) {
+    const raw8* p = (const raw8*)(c + kt * (BK * Elem<F>::BITS / 8));
+    r[SLOT][0] = p[0];
+    r[SLOT][1] = p[1];
+    sc[SLOT] = s[kt];
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void store(__bf16* planes) const {
+    const float f = scale_of(sc[SLOT]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *(bf16x8*)&planes[kc_at(row, 2 * half + i)] = Elem<F>::decode(r[SLOT][i], f);
+  }
+};
+
+// Microscaled, k the slow axis (rows of the stored matrix are k): thread t holds 8 columns of the
+// slice's rows, twice.  Columns beyond the stored row and rows beyond K are zero.
+template <int F, int TILE>
+struct CodesCol {
+  static constexpr int PIECES = 1;
+  static constexpr bool KS = true;
+  typedef typename Elem<F>::raw8 raw8;
+  const uint8_t *c[2], *s[2];
+  raw8 r[2][2];
+  unsigned sc[2][2];
+  int64_t step_c, step_s, left[2];  // rows from this thread's first one to the last
+  int k[2], col;
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t, int64_t c0, int64_t k0, int64_t k1, int tid) {
+    col = 8 * (tid % (TILE / 8));
+    step_c = BK * q.row_bytes;
+    step_s = BK * q.row_groups;
+    const bool in = c0 + col < q.row_groups * 32;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k[i] = tid / (TILE / 8) + 16 * i;
+      c[i] = q.codes + (k0 + k[i]) * q.row_bytes + (c0 + col) * Elem<F>::BITS / 8;
+      s[i] = q.scales + (k0 + k[i]) * q.row_groups + ((c0 + col) >> 5);
+      left[i] = in ? k1 - k0 - k[i] : 0;
+    }
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void load(int64_t kt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[SLOT][i] = raw8{};
+      sc[SLOT][i] = 0;
+      if (kt * BK < left[i]) {
+        r[SLOT][i] = *(const raw8*)(c[i] + kt * step_c);
+        sc[SLOT][i] = s[i][kt * step_s];
+      }
+    }
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void store(__bf16* planes) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *(bf16x8*)&planes[ks_at<TILE>(k[i], col)] = Elem<F>::decode(r[SLOT][i], scale_of(sc[SLOT][i]));
+  }
+};
+
+// fp32, k contiguous, three pieces: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
+template <int TILE>
+struct FloatK {
+  static constexpr int PIECES = 3;
+  static constexpr bool KS = false;
+  const float* p;
+  f32x4 r[2][4];
+  int row, half;
+  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int64_t, int64_t, int tid) {
+    row = tid >> 1;
+    half = tid & 1;
+    p = (const float*)x.p + b * x.stride + (r0 + row) * x.ld + 16 * half;
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void load(int64_t kt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[SLOT][i] = *(const f32x4*)(p + kt * BK + 4 * i);
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void store(__bf16* planes) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float x[8] = {r[SLOT][2 * i][0],     r[SLOT][2 * i][1],     r[SLOT][2 * i][2],     r[SLOT][2 * i][3],
+                          r[SLOT][2 * i + 1][0], r[SLOT][2 * i + 1][1], r[SLOT][2 * i + 1][2], r[SLOT][2 * i + 1][3]};
+      bf16x8 v[3];
+      pieces<3>(x, v);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) *(bf16x8*)&planes[q * TILE * BK + kc_at(row, 2 * half + i)] = v[q];
+    }
+  }
+};
+
+// fp32, bfloat16 or binary16, k the slow axis: thread t holds 8 columns of two of the slice's rows.
+// Columns and rows beyond the matrix are zero; only elements of the matrix are read.
+template <typename T>
+struct Pieces {
+  static constexpr int N = std::is_same<T, float>::value ? 3 : std::is_same<T, _Float16>::value ? 2 : 1;
+};
+template <typename T, int TILE>
+struct FloatCol {
+  static constexpr int PIECES = Pieces<T>::N;
+  static constexpr bool KS = true;
+  typedef T v8 __attribute__((ext_vector_type(8), aligned(16)));
+  const T* p[2];
+  v8 r[2][2];
+  int64_t step, left[2];
+  int k[2], col, wide;  // wide: elements of the thread's 8 columns that exist
+  bool vec;             // all 8, in a row that starts on 16 bytes
+  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t c0, int64_t k0, int64_t k1, int tid) {
+    col = 8 * (tid % (TILE / 8));
+    step = BK * x.ld;
+    const int64_t in = x.cols - c0 - col;
+    wide = in >= 8 ? 8 : in > 0 ? (int)in : 0;
+    vec = x.vec && wide == 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k[i] = tid / (TILE / 8) + 16 * i;
+      p[i] = (const T*)x.p + b * x.stride + (k0 + k[i]) * x.ld + c0 + col;
+      left[i] = wide ? k1 - k0 - k[i] : 0;
+    }
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void load(int64_t kt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[SLOT][i] = v8{};
+      if (kt * BK < left[i]) {
+        const T* at = p[i] + kt * step;
+        if (vec) {
+          r[SLOT][i] = *(const v8*)at;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (q < wide) r[SLOT][i][q] = at[q];
+        }
+      }
+    }
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void store(__bf16* planes) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      bf16x8 v[PIECES];
+      if constexpr (PIECES == 1) {
+        v[0] = __builtin_bit_cast(bf16x8, r[SLOT][i]);
+      } else {
+        float x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = (float)r[SLOT][i][q];
+        pieces<PIECES>(x, v);
+      }
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) *(bf16x8*)&planes[q * TILE * BK + ks_at<TILE>(k[i], col)] = v[q];
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// The product of one tile: acc = sum over slices of A's rows times B's columns
+// ------------------------------------------------------------------------------------------------
+
+// Waves of a tile: 256 -> 2 x 4 waves of 128 x 64, 128 -> 2 x 2 of 64 x 64, 64 -> 2 x 1 of 32 x 64
+template <int TILE>
+struct Shape;
+template <>
+struct Shape<256> {
+  static constexpr int WN = 4, MTM = 4, MTN = 2;
+};
+template <>
+struct Shape<128> {
+  static constexpr int WN = 2, MTM = 2, MTN = 2;
+};
+template <>
+struct Shape<64> {
+  static constexpr int WN = 1, MTM = 1, MTN = 2;
+};
+
+template <int TILE, typename LA, typename LB>
+__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, __bf16* stage0, __bf16* stage1, int wm,
+                                         int wn, int lane, f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
+  constexpr int PLANE = TILE * BK;
+  constexpr int PA = LA::PIECES, PB = LB::PIECES;
+#pragma unroll
+  for (int mt = 0; mt < MTM; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < MTN; ++nt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[mt][nt][r] = 0.f;
+  if (slices <= 0) return;
+
+  auto compute = [&](const __bf16* st) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) {
+        bf16x8 bv[MTN];
+#pragma unroll
+        for (int nt = 0; nt < MTN; ++nt)
+          bv[nt] = fragment<TILE, LB::KS>(st + (PA + pb) * PLANE, (wn * MTN + nt) * 32, ks, lane);
+#pragma unroll
+        for (int pa = 0; pa < PA; ++pa)
+#pragma unroll
+          for (int mt = 0; mt < MTM; ++mt) {
+            const bf16x8 av = fragment<TILE, LA::KS>(st + pa * PLANE, (wm * MTM + mt) * 32, ks, lane);
+#pragma unroll
+            for (int nt = 0; nt < MTN; ++nt) acc[mt][nt] = Half<__bf16>::mfma(av, bv[nt], acc[mt][nt]);
+          }
+      }
+  };
+  // slice kt is multiplied from one stage while slice kt + 1 moves from registers to the other and
+  // the loads of slice kt + 2 are under way
+  auto step = [&](auto slot_c, int64_t kt) {
+    constexpr int slot = decltype(slot_c)::value;
+    __bf16* now = slot ? stage1 : stage0;
+    __bf16* next = slot ? stage0 : stage1;
+    if (kt + 2 < slices) {
+      la.template load<slot>(kt + 2);
+      lb.template load<slot>(kt + 2);
+    }
+    if (kt + 1 < slices) {
+      la.template store<1 - slot>(next);
+      lb.template store<1 - slot>(next + PA * PLANE);
+    }
+    compute(now);
+    __syncthreads();
+  };
+  la.template load<0>(0);
+  lb.template load<0>(0);
+  if (slices > 1) {
+    la.template load<1>(1);
+    lb.template load<1>(1);
+  }
+  la.template store<0>(stage0);
+  lb.template store<0>(stage0 + PA * PLANE);
+  __syncthreads();
+  for (int64_t kt = 0; kt < slices; kt += 2) {
+    step(IC<0>{}, kt);
+    if (kt + 1 < slices) step(IC<1>{}, kt + 1);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Statistics: L <- beta L + (1 - beta) Q Q^T from row codes, R from column codes (two problems)
+// ------------------------------------------------------------------------------------------------
+
+struct StatsArgs {
+  GemmArgs g;
+  MxCodes q[2];
+};
+
+template <int F, int TILE>
+__global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
+  constexpr int STAGE = 2 * TILE * BK;
+  __shared__ __attribute__((aligned(16))) __bf16 stage0[STAGE];
+  __shared__ __attribute__((aligned(16))) __bf16 stage1[STAGE];
+  const TileCoord tc = decode_tile(a.g, true);
+  const MxCodes q = tc.prob ? a.q[1] : a.q[0];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
+  CodesK<F, TILE> la, lb;
+  la.init(q, tc.b, tc.ti * TILE, 0, 0, tid);
+  lb.init(q, tc.b, tc.tj * TILE, 0, 0, tid);
+  f32x16 acc[MTM][MTN];
+  multiply<TILE>(la, lb, a.g.B / BK, stage0, stage1, wm, wn, lane, acc);
+  constexpr int WAVES = TILE / 32;
+  constexpr int PER = WAVES / 2 * MLDS_FLOATS * 4;
+  static_assert(PER <= STAGE * 2, "LDS for the mirror");
+  float* mlds = (float*)(wave < WAVES / 2 ? (void*)stage0 : (void*)stage1) + (wave % (WAVES / 2)) * MLDS_FLOATS;
+  epilogue_split<MTM, MTN, MTM * 32, MTN * 32, true, false, TILE, false, false>(
+      a.g, tc, tc.prob ? a.g.p1 : a.g.p0, acc, wm, wn, lane, nullptr, mlds);
+}
+
+template <int F, int TILE>
+hipError_t launch_stats(StatsArgs& a, hipStream_t stream) {
+  a.g.tdim = a.g.B / TILE;
+  a.g.tiles = a.g.tdim * (a.g.tdim + 1) / 2;
+  const int64_t grid = 2 * a.g.N * a.g.tiles;
+  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((mx_stats_kernel<F, TILE>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------------
+// Update: T = XL G and U = T XR^T, each with the root's diagonal added in fp32
+// ------------------------------------------------------------------------------------------------
+
+struct ApplyArgs {
+  GemmArgs g;  // N, B and the tile map only
+  MxCodes q;
+  MxFloats x;
+  const float* diag;  // [N, B] or null: + diag[i] x[i][j] (LEFT) or + x[i][j] diag[j]
+  float* out;
+};
+
+// LEFT: out = Q X (Q's rows, X's columns); else out = X Q^T (X's rows, Q's rows as columns)
+template <int F, int TILE, bool LEFT>
+__global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
+  constexpr int STAGE = 4 * TILE * BK;
+  __shared__ __attribute__((aligned(16))) __bf16 stage0[STAGE];
+  __shared__ __attribute__((aligned(16))) __bf16 stage1[STAGE];
+  const TileCoord tc = decode_tile(a.g, false);
+  const int B = a.g.B;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
+  f32x16 acc[MTM][MTN];
+  if constexpr (LEFT) {
+    CodesK<F, TILE> la;
+    FloatCol<float, TILE> lb;
+    la.init(a.q, tc.b, tc.ti * TILE, 0, 0, tid);
+    lb.init(a.x, tc.b, tc.tj * TILE, 0, B, tid);
+    multiply<TILE>(la, lb, B / BK, stage0, stage1, wm, wn, lane, acc);
+  } else {
+    FloatK<TILE> la;
+    CodesK<F, TILE> lb;
+    la.init(a.x, tc.b, tc.ti * TILE, 0, 0, tid);
+    lb.init(a.q, tc.b, tc.tj * TILE, 0, 0, tid);
+    multiply<TILE>(la, lb, B / BK, stage0, stage1, wm, wn, lane, acc);
+  }
+  const int64_t off = tc.b * (int64_t)B * B;
+  const float* x = (const float*)a.x.p + off;
+  const float* dg = a.diag ? a.diag + tc.b * B : nullptr;
+  float* out = a.out + off;
+#pragma unroll
+  for (int mt = 0; mt < MTM; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < MTN; ++nt) {
+      const int i0 = tc.ti * TILE + (wm * MTM + mt) * 32 + 4 * (lane >> 5);
+      const int j = tc.tj * TILE + (wn * MTN + nt) * 32 + (lane & 31);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int i = i0 + 8 * (r >> 2) + (r & 3);
+        const int64_t at = (int64_t)i * B + j;
+        float v = acc[mt][nt][r];
+        if (dg) v += x[at] * dg[LEFT ? i : j];
+        out[at] = v;
+      }
+    }
+}
+
+template <int F, int TILE, bool LEFT>
+hipError_t launch_apply_one(ApplyArgs& a, hipStream_t stream) {
+  a.g.tdim = a.g.B / TILE;
+  a.g.tiles = a.g.tdim * a.g.tdim;
+  const int64_t grid = a.g.N * a.g.tiles;
+  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, LEFT>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------------
+// Gradient tiles: G = dY^T Q, dY [T, out], Q [T, in], in the order of launch_tile_copy
+// ------------------------------------------------------------------------------------------------
+
+struct GradArgs {
+  MxFloats dy;      // ld, cols = out
+  MxCodes q;        // rows = T
+  int64_t T, out, in;
+  int B;            // tiles of the stack
+  int64_t tr, tc;   // tile rows and columns of the stack
+  int64_t gm, gn;   // kernel tiles along out and in
+  int splits;       // of the token axis
+  int64_t chunk;    // tokens per split, a multiple of BK
+  int accumulate;
+  float* G;
+  float* part;      // [splits, gm TILE, gn TILE] when splits > 1
+};
+
+template <typename T, int F, int TILE>
+__global__ __launch_bounds__(2 * TILE) void mx_grad_kernel(GradArgs a) {
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
+  constexpr int STAGE = (Pieces<T>::N + 1) * TILE * BK;
+  __shared__ __attribute__((aligned(16))) __bf16 stage0[STAGE];
+  __shared__ __attribute__((aligned(16))) __bf16 stage1[STAGE];
+  const int64_t lid = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t tiles = a.gm * a.gn;
+  const int split = (int)(lid / tiles);
+  const int64_t rem = lid - split * tiles;
+  const int64_t ti = rem / a.gn, tj = rem - ti * a.gn;
+  const int64_t i0 = ti * TILE, j0 = tj * TILE;
+  const int64_t k0 = split * a.chunk, k1 = k0 + a.chunk < a.T ? k0 + a.chunk : a.T;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
+  f32x16 acc[MTM][MTN];
+  FloatCol<T, TILE> la;
+  CodesCol<F, TILE> lb;
+  la.init(a.dy, 0, i0, k0, k1, tid);
+  lb.init(a.q, 0, j0, k0, k1, tid);
+  // a tile of padding alone has no products
+  const int64_t slices = i0 < a.out && j0 < a.in ? (k1 - k0 + BK - 1) / BK : 0;
+  multiply<TILE>(la, lb, slices, stage0, stage1, wm, wn, lane, acc);
+#pragma unroll
+  for (int mt = 0; mt < MTM; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < MTN; ++nt) {
+      // a 32 x 32 sub-block lies in one tile of the stack (B is a multiple of 64)
+      const int64_t is = i0 + (wm * MTM + mt) * 32, js = j0 + (wn * MTN + nt) * 32;
+      if (is >= a.tr * a.B || js >= a.tc * a.B) continue;
+      const int64_t j = js + (lane & 31);
+      float* base;
+      int64_t ld;
+      if (a.splits > 1) {
+        ld = a.gn * TILE;
+        base = a.part + (split * a.gm * TILE + is) * ld + j;
+      } else {
+        ld = a.B;
+        const int64_t t = is / a.B * a.tc + js / a.B;
+        base = a.G + (t * a.B + is % a.B) * a.B + j % a.B;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int dr = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        float v = is + dr < a.out && j < a.in ? acc[mt][nt][r] : 0.f;
+        float* at = base + dr * ld;
+        if (a.splits == 1 && a.accumulate) v += *at;
+        *at = v;
+      }
+    }
+}
+
+// The splits' partial sums added in order, into the stack's tiles; one thread per 4 columns.
+__global__ __launch_bounds__(256) void mx_grad_join_kernel(GradArgs a, int64_t pm, int64_t pn) {
+  const int64_t quads = a.tc * a.B / 4;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= a.tr * a.B * quads) return;
+  const int64_t i = e / quads, j = 4 * (e - i * quads);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (i < a.out && j < a.in)
+    for (int s = 0; s < a.splits; ++s) v += *(const f32x4*)(a.part + (s * pm + i) * pn + j);
+  const int64_t t = i / a.B * a.tc + j / a.B;
+  f32x4* at = (f32x4*)(a.G + (t * a.B + i % a.B) * a.B + j % a.B);
+  *at = a.accumulate ? *at + v : v;
+}
+
+constexpr int GRAD_CHUNK_MIN = 512;  // tokens a split has at least
+
+// The launch's shape: kernel tile, tiles, and splits of the token axis so that few tiles still fill
+// the 256 compute units.
+struct GradShape {
+  int tile;
+  int64_t gm, gn, chunk;
+  int splits;
+};
+GradShape grad_shape(int64_t T, int64_t out, int64_t in) {
+  GradShape g;
+  g.tile = out <= 64 || in <= 64 ? 64 : out <= 128 || in <= 128 ? 128 : 256;
+  g.gm = (out + g.tile - 1) / g.tile;
+  g.gn = (in + g.tile - 1) / g.tile;
+  const int64_t tiles = g.gm * g.gn;
+  int64_t s = 256 / tiles;
+  if (s > T / GRAD_CHUNK_MIN) s = T / GRAD_CHUNK_MIN;
+  if (s < 1) s = 1;
+  g.chunk = ((T + s - 1) / s + BK - 1) / BK * BK;
+  g.splits = g.chunk ? (int)((T + g.chunk - 1) / g.chunk) : 1;
+  if (g.splits < 1) g.splits = 1;
+  return g;
+}
+
+template <typename T, int F, int TILE>
+hipError_t launch_grad_one(GradArgs& a, const GradShape& g, hipStream_t stream) {
+  // one split: the launch also writes the padding of the stack's edge tiles
+  if (g.splits == 1) {
+    a.gm = (a.tr * a.B + TILE - 1) / TILE;
+    a.gn = (a.tc * a.B + TILE - 1) / TILE;
+  } else {
+    a.gm = g.gm;
+    a.gn = g.gn;
+  }
+  const int64_t grid = a.gm * a.gn * g.splits;
+  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((mx_grad_kernel<T, F, TILE>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || g.splits == 1) return e;
+  const int64_t joins = (a.tr * a.B * (a.tc * a.B / 4) + 255) / 256;
+  if (joins > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(mx_grad_join_kernel, dim3((unsigned)joins), dim3(256), 0, stream, a, g.gm * TILE, g.gn * TILE);
+  return hipGetLastError();
+}
+
+template <typename T, int F>
+hipError_t launch_grad_tile(GradArgs& a, const GradShape& g, hipStream_t stream) {
+  if (g.tile == 256) return launch_grad_one<T, F, 256>(a, g, stream);
+  if (g.tile == 128) return launch_grad_one<T, F, 128>(a, g, stream);
+  return launch_grad_one<T, F, 64>(a, g, stream);
+}
+
+template <typename T>
+hipError_t launch_grad_fmt(GradArgs& a, const GradShape& g, dash_mx_fmt fmt, hipStream_t stream) {
+  return fmt == DASH_MX_E4M3 ? launch_grad_tile<T, DASH_MX_E4M3>(a, g, stream)
+                             : launch_grad_tile<T, DASH_MX_E2M1>(a, g, stream);
+}
+
+}  // namespace
+}  // namespace gemm
+
+using namespace gemm;
+
+hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG, int B, dash_mx_fmt fmt, float beta,
+                           float* A, hipStream_t stream) {
+  StatsArgs a;
+  a.g.N = NG;
+  a.g.B = B;
+  a.g.nprob = 2;
+  a.g.epi.alpha = 1.f - beta;
+  a.g.epi.delta = beta;
+  a.g.p0.D = A;
+  a.g.p0.E = A;
+  a.g.p1.D = A + NG * (int64_t)B * B;
+  a.g.p1.E = A + NG * (int64_t)B * B;
+  a.q[0] = rows;
+  a.q[1] = cols;
+  if (fmt == DASH_MX_E4M3)
+    return B % 256 == 0   ? launch_stats<DASH_MX_E4M3, 256>(a, stream)
+           : B % 128 == 0 ? launch_stats<DASH_MX_E4M3, 128>(a, stream)
+                          : launch_stats<DASH_MX_E4M3, 64>(a, stream);
+  return B % 256 == 0   ? launch_stats<DASH_MX_E2M1, 256>(a, stream)
+         : B % 128 == 0 ? launch_stats<DASH_MX_E2M1, 128>(a, stream)
+                        : launch_stats<DASH_MX_E2M1, 64>(a, stream);
+}
+
+template <int F>
+static hipError_t apply_tile(ApplyArgs& a, bool left, hipStream_t stream) {
+  const int B = a.g.B;
+  if (left)
+    return B % 256 == 0   ? launch_apply_one<F, 256, true>(a, stream)
+           : B % 128 == 0 ? launch_apply_one<F, 128, true>(a, stream)
+                          : launch_apply_one<F, 64, true>(a, stream);
+  return B % 256 == 0   ? launch_apply_one<F, 256, false>(a, stream)
+         : B % 128 == 0 ? launch_apply_one<F, 128, false>(a, stream)
+                        : launch_apply_one<F, 64, false>(a, stream);
+}
+
+hipError_t launch_mx_apply(const MxCodes& q, const float* diag, const float* X, int64_t NG, int B, dash_mx_fmt fmt,
+                           bool left, float* out, hipStream_t stream) {
+  ApplyArgs a;
+  a.g.N = NG;
+  a.g.B = B;
+  a.g.nprob = 1;
+  a.q = q;
+  a.x.p = X;
+  a.x.ld = B;
+  a.x.stride = (int64_t)B * B;
+  a.x.cols = B;
+  a.diag = diag;
+  a.out = out;
+  return fmt == DASH_MX_E4M3 ? apply_tile<DASH_MX_E4M3>(a, left, stream) : apply_tile<DASH_MX_E2M1>(a, left, stream);
+}
+
+size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in) {
+  const GradShape g = grad_shape(T, out, in);
+  return g.splits > 1 ? (size_t)g.splits * g.gm * g.gn * g.tile * g.tile * sizeof(float) : 0;
+}
+
+hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
+                          int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream) {
+  const GradShape g = grad_shape(T, out, in);
+  GradArgs a;
+  a.dy.p = dY;
+  a.dy.ld = ldy;
+  a.dy.stride = 0;
+  a.dy.cols = out;
+  a.dy.vec = ((uintptr_t)dY & 15) == 0 && (T <= 1 || ldy * (type == DASH_FP32 ? 4 : 2) % 16 == 0);
+  a.q = q;
+  a.T = T;
+  a.out = out;
+  a.in = in;
+  a.B = B;
+  a.tr = (out + B - 1) / B;
+  a.tc = (in + B - 1) / B;
+  a.splits = g.splits;
+  a.chunk = g.chunk;
+  a.accumulate = accumulate;
+  a.G = G;
+  a.part = (float*)ws;
+  if (type == DASH_FP32) return launch_grad_fmt<float>(a, g, fmt, stream);
+  if (type == DASH_BF16) return launch_grad_fmt<__bf16>(a, g, fmt, stream);
+  return launch_grad_fmt<_Float16>(a, g, fmt, stream);
+}
+
+}  // namespace dash
