@@ -507,7 +507,8 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
  * that start on 16 bytes load fastest) the gradient of the layer's output and Q [T, in] the values of codes/scales (the input quantised by rows
  * in the forward pass), written as dash_stack would stack an out x in weight: ceil(out/B) x ceil(in/B)
  * tiles, the part of an edge tile outside the weight zero.  accumulate = 1 adds to the tiles that
- * G_stack holds (earlier micro-batches; the padding keeps what it holds), 0 overwrites them.  dY
+ * G_stack holds (earlier micro-batches; the padding keeps what it holds), 0 overwrites them.  in, ldy at
+ * most 2^26.  dY
  * enters exactly in every type, sums are fp32, and equal calls give equal bits.  T = 0 (dY, codes and
  * scales may be NULL): an empty sum.
  * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned. */

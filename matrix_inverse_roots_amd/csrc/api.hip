@@ -91,8 +91,9 @@ dash_status mx_shape_check(dash_prec type, int64_t N, int64_t rows, int64_t cols
 }
 dash_status grad_shape_check(int64_t T, int64_t out, int64_t in, int64_t ldy, dash_prec type) {
   if (!plain_type(type)) return DASH_ERR_INVALID_ARG;
-  if (T < 0 || out < 1 || in < 1 || T > MX_MAX_SIDE || out > MX_MAX_SIDE || in > MX_MAX_SIDE || ldy < out ||
-      ldy > MX_MAX_SIDE)
+  // (rows of at most 2^26 elements: 16 of them are within a 32-bit byte offset)
+  constexpr int64_t most_row = (int64_t)1 << 26;
+  if (T < 0 || out < 1 || in < 1 || T > MX_MAX_SIDE || in > most_row || ldy < out || ldy > most_row)
     return DASH_ERR_SHAPE;
   const double most = (double)(T > out ? T : out) * (double)(ldy > in ? ldy : in);
   return most > MX_MAX_ELEMENTS ? DASH_ERR_SHAPE : DASH_OK;

@@ -142,32 +142,39 @@ __device__ __forceinline__ bf16x8 fragment(const __bf16* plane, int base, int ks
 
 // ------------------------------------------------------------------------------------------------
 // Operand loaders.  init: the thread's place in the tile whose first row (column) is r0; load: slice
-// kt into ring slot `slot`; store: a slot into LDS planes.
+// kt into ring slot SLOT (CHECK: with the matrix's edges minded; the others are whole); store: a slot
+// into LDS planes.  An address is a wave-uniform base that moves with kt plus a 32-bit lane offset.
 // ------------------------------------------------------------------------------------------------
 
+// D: slices in the register ring, 4 where an operand is 16 bits wide or less and 2 beside fp32 (four
+// slices of it spill)
 // Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
-template <int F, int TILE>
+template <int F, int TILE, int D>
 struct CodesK {
+  static constexpr int DEPTH = D;
   static constexpr int PIECES = 1;
   static constexpr bool KS = false;
   typedef typename Elem<F>::raw8 raw8;
   const uint8_t *c, *s;
-  raw8 r[2][2];
-  unsigned sc[2];
+  unsigned off_c, off_s;
+  raw8 r[DEPTH][2];
+  unsigned sc[DEPTH];
   int row, half;
-  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int64_t, int64_t, int tid) {
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int tid) {
     row = tid >> 1;
     half = tid & 1;
-    const int64_t at = b * q.rows + r0 + row;
-    c = q.codes + at * q.row_bytes + half * (2 * Elem<F>::BITS);
+    const int64_t at = b * q.rows + r0;
+    c = q.codes + at * q.row_bytes;
     s = q.scales + at * q.row_groups;
+    off_c = (unsigned)row * (unsigned)q.row_bytes + half * (2 * Elem<F>::BITS);
+    off_s = (unsigned)row * (unsigned)q.row_groups;
   }
-  template <int SLOT>
+  template <int SLOT, bool CHECK>
   __device__ __forceinline__ void load(int64_t kt) {
-    const raw8* p = (const raw8*)(c + kt * (BK * Elem<F>::BITS / 8));
+    const raw8* p = (const raw8*)(c + kt * (BK * Elem<F>::BITS / 8) + off_c);
     r[SLOT][0] = p[0];
     r[SLOT][1] = p[1];
-    sc[SLOT] = s[kt];
+    sc[SLOT] = (s + kt)[off_s];
   }
   template <int SLOT>
   __device__ __forceinline__ void store(__bf16* planes) const {
@@ -178,68 +185,73 @@ struct CodesK {
   }
 };
 
-// Microscaled, k the slow axis (rows of the stored matrix are k): thread t holds 8 columns of the
-// slice's rows, twice.  Columns beyond the stored row and rows beyond K are zero.
-template <int F, int TILE>
+// Microscaled, k the slow axis (rows of the stored matrix are k): thread t holds 8 columns of two of the
+// slice's rows, 16 apart.  Columns beyond the stored row and rows beyond K are zero.
+template <int F, int TILE, int D>
 struct CodesCol {
+  static constexpr int DEPTH = D;
   static constexpr int PIECES = 1;
   static constexpr bool KS = true;
   typedef typename Elem<F>::raw8 raw8;
-  const uint8_t *c[2], *s[2];
-  raw8 r[2][2];
-  unsigned sc[2][2];
-  int64_t step_c, step_s, left[2];  // rows from this thread's first one to the last
-  int k[2], col;
-  __device__ __forceinline__ void init(const MxCodes& q, int64_t, int64_t c0, int64_t k0, int64_t k1, int tid) {
+  const uint8_t *c, *s;
+  unsigned off_c, off_s;
+  raw8 r[DEPTH][2];
+  unsigned sc[DEPTH][2];
+  int64_t row_c, row_s, left;  // left: rows from this thread's first one to the last
+  int k, col;
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t c0, int64_t k0, int64_t k1, int tid) {
     col = 8 * (tid % (TILE / 8));
-    step_c = BK * q.row_bytes;
-    step_s = BK * q.row_groups;
-    const bool in = c0 + col < q.row_groups * 32;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      k[i] = tid / (TILE / 8) + 16 * i;
-      c[i] = q.codes + (k0 + k[i]) * q.row_bytes + (c0 + col) * Elem<F>::BITS / 8;
-      s[i] = q.scales + (k0 + k[i]) * q.row_groups + ((c0 + col) >> 5);
-      left[i] = in ? k1 - k0 - k[i] : 0;
-    }
+    k = tid / (TILE / 8);
+    row_c = q.row_bytes;
+    row_s = q.row_groups;
+    c = q.codes + k0 * row_c + c0 * Elem<F>::BITS / 8;
+    s = q.scales + k0 * row_s + c0 / 32;
+    off_c = (unsigned)k * (unsigned)row_c + col * Elem<F>::BITS / 8;
+    off_s = (unsigned)k * (unsigned)row_s + col / 32;
+    left = c0 + col < row_s * 32 ? k1 - k0 - k : 0;
   }
-  template <int SLOT>
+  template <int SLOT, bool CHECK>
   __device__ __forceinline__ void load(int64_t kt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      r[SLOT][i] = raw8{};
-      sc[SLOT][i] = 0;
-      if (kt * BK < left[i]) {
-        r[SLOT][i] = *(const raw8*)(c[i] + kt * step_c);
-        sc[SLOT][i] = s[i][kt * step_s];
+      const int64_t at = kt * BK + 16 * i;
+      if (CHECK) {
+        r[SLOT][i] = raw8{};
+        sc[SLOT][i] = 0;
+        if (at >= left) continue;
       }
+      r[SLOT][i] = *(const raw8*)(c + at * row_c + off_c);
+      sc[SLOT][i] = (s + at * row_s)[off_s];
     }
   }
   template <int SLOT>
   __device__ __forceinline__ void store(__bf16* planes) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *(bf16x8*)&planes[ks_at<TILE>(k[i], col)] = Elem<F>::decode(r[SLOT][i], scale_of(sc[SLOT][i]));
+      *(bf16x8*)&planes[ks_at<TILE>(k + 16 * i, col)] = Elem<F>::decode(r[SLOT][i], scale_of(sc[SLOT][i]));
   }
 };
 
 // fp32, k contiguous, three pieces: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
-template <int TILE>
+template <int TILE, int D>
 struct FloatK {
+  static constexpr int DEPTH = D;
   static constexpr int PIECES = 3;
   static constexpr bool KS = false;
   const float* p;
-  f32x4 r[2][4];
+  unsigned off;
+  f32x4 r[DEPTH][4];
   int row, half;
-  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int64_t, int64_t, int tid) {
+  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int tid) {
     row = tid >> 1;
     half = tid & 1;
-    p = (const float*)x.p + b * x.stride + (r0 + row) * x.ld + 16 * half;
+    p = (const float*)x.p + b * x.stride + r0 * x.ld;
+    off = (unsigned)row * (unsigned)x.ld + 16 * half;
   }
-  template <int SLOT>
+  template <int SLOT, bool CHECK>
   __device__ __forceinline__ void load(int64_t kt) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[SLOT][i] = *(const f32x4*)(p + kt * BK + 4 * i);
+    for (int i = 0; i < 4; ++i) r[SLOT][i] = *(const f32x4*)(p + kt * BK + off + 4 * i);
   }
   template <int SLOT>
   __device__ __forceinline__ void store(__bf16* planes) const {
@@ -255,49 +267,53 @@ struct FloatK {
   }
 };
 
-// fp32, bfloat16 or binary16, k the slow axis: thread t holds 8 columns of two of the slice's rows.
-// Columns and rows beyond the matrix are zero; only elements of the matrix are read.
+// fp32, bfloat16 or binary16, k the slow axis: thread t holds 8 columns of two of the slice's rows, 16
+// apart.  Columns and rows beyond the matrix are zero; only elements of the matrix are read.
 template <typename T>
 struct Pieces {
   static constexpr int N = std::is_same<T, float>::value ? 3 : std::is_same<T, _Float16>::value ? 2 : 1;
 };
-template <typename T, int TILE>
+template <typename T, int TILE, int D>
 struct FloatCol {
+  static constexpr int DEPTH = D;
   static constexpr int PIECES = Pieces<T>::N;
   static constexpr bool KS = true;
   typedef T v8 __attribute__((ext_vector_type(8), aligned(16)));
-  const T* p[2];
-  v8 r[2][2];
-  int64_t step, left[2];
-  int k[2], col, wide;  // wide: elements of the thread's 8 columns that exist
-  bool vec;             // all 8, in a row that starts on 16 bytes
+  const T* p;
+  unsigned off;
+  v8 r[DEPTH][2];
+  int64_t ld, left;
+  int k, col, wide;  // wide: elements of the thread's 8 columns that exist
+  bool vec;          // all 8, in rows that start on 16 bytes
   __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t c0, int64_t k0, int64_t k1, int tid) {
     col = 8 * (tid % (TILE / 8));
-    step = BK * x.ld;
+    k = tid / (TILE / 8);
+    ld = x.ld;
+    p = (const T*)x.p + b * x.stride + k0 * ld + c0;
+    off = (unsigned)k * (unsigned)ld + col;
     const int64_t in = x.cols - c0 - col;
     wide = in >= 8 ? 8 : in > 0 ? (int)in : 0;
     vec = x.vec && wide == 8;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      k[i] = tid / (TILE / 8) + 16 * i;
-      p[i] = (const T*)x.p + b * x.stride + (k0 + k[i]) * x.ld + c0 + col;
-      left[i] = wide ? k1 - k0 - k[i] : 0;
-    }
+    left = wide ? k1 - k0 - k : 0;
   }
-  template <int SLOT>
+  template <int SLOT, bool CHECK>
   __device__ __forceinline__ void load(int64_t kt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const int64_t at = kt * BK + 16 * i;
+      const T* q = p + at * ld + off;
+      if (!CHECK) {
+        r[SLOT][i] = *(const v8*)q;
+        continue;
+      }
       r[SLOT][i] = v8{};
-      if (kt * BK < left[i]) {
-        const T* at = p[i] + kt * step;
-        if (vec) {
-          r[SLOT][i] = *(const v8*)at;
-        } else {
+      if (at >= left) continue;
+      if (vec) {
+        r[SLOT][i] = *(const v8*)q;
+      } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (q < wide) r[SLOT][i][q] = at[q];
-        }
+        for (int e = 0; e < 8; ++e)
+          if (e < wide) r[SLOT][i][e] = q[e];
       }
     }
   }
@@ -315,7 +331,7 @@ struct FloatCol {
         pieces<PIECES>(x, v);
       }
 #pragma unroll
-      for (int q = 0; q < PIECES; ++q) *(bf16x8*)&planes[q * TILE * BK + ks_at<TILE>(k[i], col)] = v[q];
+      for (int q = 0; q < PIECES; ++q) *(bf16x8*)&planes[q * TILE * BK + ks_at<TILE>(k + 16 * i, col)] = v[q];
     }
   }
 };
@@ -340,12 +356,16 @@ struct Shape<64> {
   static constexpr int WN = 1, MTM = 1, MTN = 2;
 };
 
+// slices: of k; whole: the leading ones that need no checks
 template <int TILE, typename LA, typename LB>
-__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, __bf16* stage0, __bf16* stage1, int wm,
-                                         int wn, int lane, f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
+__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t whole, __bf16* stage0, __bf16* stage1,
+                                         int wm, int wn, int lane,
+                                         f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
   constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
   constexpr int PLANE = TILE * BK;
   constexpr int PA = LA::PIECES, PB = LB::PIECES;
+  constexpr int DEPTH = LA::DEPTH;
+  static_assert(DEPTH == LB::DEPTH && (DEPTH == 2 || DEPTH == 4), "the loops below step through 2 or 4 slots");
 #pragma unroll
   for (int mt = 0; mt < MTM; ++mt)
 #pragma unroll
@@ -373,35 +393,57 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, __bf16*
           }
       }
   };
-  // slice kt is multiplied from one stage while slice kt + 1 moves from registers to the other and
-  // the loads of slice kt + 2 are under way
+  auto load = [&](auto slot_c, auto check_c, int64_t kt) {
+    la.template load<decltype(slot_c)::value, decltype(check_c)::value>(kt);
+    lb.template load<decltype(slot_c)::value, decltype(check_c)::value>(kt);
+  };
+  auto store = [&](auto slot_c) {  // (slices alternate between the stages)
+    constexpr int slot = decltype(slot_c)::value;
+    __bf16* st = slot & 1 ? stage1 : stage0;
+    la.template store<slot>(st);
+    lb.template store<slot>(st + PA * PLANE);
+  };
+  // steady state: the loads of slice kt + DEPTH go into the registers that slice kt left, slice kt + 1 moves
+  // from registers to the other stage, slice kt is multiplied
   auto step = [&](auto slot_c, int64_t kt) {
     constexpr int slot = decltype(slot_c)::value;
-    __bf16* now = slot ? stage1 : stage0;
-    __bf16* next = slot ? stage0 : stage1;
-    if (kt + 2 < slices) {
-      la.template load<slot>(kt + 2);
-      lb.template load<slot>(kt + 2);
-    }
-    if (kt + 1 < slices) {
-      la.template store<1 - slot>(next);
-      lb.template store<1 - slot>(next + PA * PLANE);
-    }
-    compute(now);
+    load(slot_c, IC<0>{}, kt + DEPTH);
+    store(IC<(slot + 1) % DEPTH>{});
+    compute(slot & 1 ? stage1 : stage0);
     __syncthreads();
   };
-  la.template load<0>(0);
-  lb.template load<0>(0);
-  if (slices > 1) {
-    la.template load<1>(1);
-    lb.template load<1>(1);
+  auto last_step = [&](auto slot_c, int64_t kt) {
+    constexpr int slot = decltype(slot_c)::value;
+    if (kt >= slices) return;
+    if (kt + DEPTH < slices) load(slot_c, IC<1>{}, kt + DEPTH);
+    if (kt + 1 < slices) store(IC<(slot + 1) % DEPTH>{});
+    compute(slot & 1 ? stage1 : stage0);
+    __syncthreads();
+  };
+  load(IC<0>{}, IC<1>{}, 0);
+  if (slices > 1) load(IC<1>{}, IC<1>{}, 1);
+  if constexpr (DEPTH == 4) {
+    if (slices > 2) load(IC<2>{}, IC<1>{}, 2);
+    if (slices > 3) load(IC<3>{}, IC<1>{}, 3);
   }
-  la.template store<0>(stage0);
-  lb.template store<0>(stage0 + PA * PLANE);
+  store(IC<0>{});
   __syncthreads();
-  for (int64_t kt = 0; kt < slices; kt += 2) {
+  int64_t kt = 0;
+  for (; kt + 2 * DEPTH <= whole; kt += DEPTH) {
     step(IC<0>{}, kt);
-    if (kt + 1 < slices) step(IC<1>{}, kt + 1);
+    step(IC<1>{}, kt + 1);
+    if constexpr (DEPTH == 4) {
+      step(IC<2>{}, kt + 2);
+      step(IC<3>{}, kt + 3);
+    }
+  }
+  for (; kt < slices; kt += DEPTH) {
+    last_step(IC<0>{}, kt);
+    last_step(IC<1>{}, kt + 1);
+    if constexpr (DEPTH == 4) {
+      last_step(IC<2>{}, kt + 2);
+      last_step(IC<3>{}, kt + 3);
+    }
   }
 }
 
@@ -424,11 +466,12 @@ __global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
   const MxCodes q = tc.prob ? a.q[1] : a.q[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
-  CodesK<F, TILE> la, lb;
-  la.init(q, tc.b, tc.ti * TILE, 0, 0, tid);
-  lb.init(q, tc.b, tc.tj * TILE, 0, 0, tid);
+  CodesK<F, TILE, 4> la, lb;
+  la.init(q, tc.b, tc.ti * TILE, tid);
+  lb.init(q, tc.b, tc.tj * TILE, tid);
   f32x16 acc[MTM][MTN];
-  multiply<TILE>(la, lb, a.g.B / BK, stage0, stage1, wm, wn, lane, acc);
+  const int slices = a.g.B / BK;
+  multiply<TILE>(la, lb, slices, slices, stage0, stage1, wm, wn, lane, acc);
   constexpr int WAVES = TILE / 32;
   constexpr int PER = WAVES / 2 * MLDS_FLOATS * 4;
   static_assert(PER <= STAGE * 2, "LDS for the mirror");
@@ -472,17 +515,17 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
   f32x16 acc[MTM][MTN];
   if constexpr (LEFT) {
-    CodesK<F, TILE> la;
-    FloatCol<float, TILE> lb;
-    la.init(a.q, tc.b, tc.ti * TILE, 0, 0, tid);
+    CodesK<F, TILE, 2> la;
+    FloatCol<float, TILE, 2> lb;
+    la.init(a.q, tc.b, tc.ti * TILE, tid);
     lb.init(a.x, tc.b, tc.tj * TILE, 0, B, tid);
-    multiply<TILE>(la, lb, B / BK, stage0, stage1, wm, wn, lane, acc);
+    multiply<TILE>(la, lb, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
   } else {
-    FloatK<TILE> la;
-    CodesK<F, TILE> lb;
-    la.init(a.x, tc.b, tc.ti * TILE, 0, 0, tid);
-    lb.init(a.q, tc.b, tc.tj * TILE, 0, 0, tid);
-    multiply<TILE>(la, lb, B / BK, stage0, stage1, wm, wn, lane, acc);
+    FloatK<TILE, 2> la;
+    CodesK<F, TILE, 2> lb;
+    la.init(a.x, tc.b, tc.ti * TILE, tid);
+    lb.init(a.q, tc.b, tc.tj * TILE, tid);
+    multiply<TILE>(la, lb, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
   }
   const int64_t off = tc.b * (int64_t)B * B;
   const float* x = (const float*)a.x.p + off;
@@ -494,14 +537,20 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
     for (int nt = 0; nt < MTN; ++nt) {
       const int i0 = tc.ti * TILE + (wm * MTM + mt) * 32 + 4 * (lane >> 5);
       const int j = tc.tj * TILE + (wn * MTN + nt) * 32 + (lane & 31);
+      // (all loads of a sub-block before its stores)
+      if (dg) {
+        float xv[16], dv[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int i = i0 + 8 * (r >> 2) + (r & 3);
-        const int64_t at = (int64_t)i * B + j;
-        float v = acc[mt][nt][r];
-        if (dg) v += x[at] * dg[LEFT ? i : j];
-        out[at] = v;
+        for (int r = 0; r < 16; ++r) {
+          const int i = i0 + 8 * (r >> 2) + (r & 3);
+          xv[r] = x[i * B + j];
+          dv[r] = dg[LEFT ? i : j];
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[mt][nt][r] += xv[r] * dv[r];
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) out[(i0 + 8 * (r >> 2) + (r & 3)) * B + j] = acc[mt][nt][r];
     }
 }
 
@@ -549,13 +598,16 @@ __global__ __launch_bounds__(2 * TILE) void mx_grad_kernel(GradArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
   f32x16 acc[MTM][MTN];
-  FloatCol<T, TILE> la;
-  CodesCol<F, TILE> lb;
+  constexpr int D = sizeof(T) == 4 ? 2 : 4;
+  FloatCol<T, TILE, D> la;
+  CodesCol<F, TILE, D> lb;
   la.init(a.dy, 0, i0, k0, k1, tid);
-  lb.init(a.q, 0, j0, k0, k1, tid);
+  lb.init(a.q, j0, k0, k1, tid);
   // a tile of padding alone has no products
   const int64_t slices = i0 < a.out && j0 < a.in ? (k1 - k0 + BK - 1) / BK : 0;
-  multiply<TILE>(la, lb, slices, stage0, stage1, wm, wn, lane, acc);
+  const bool inside = a.dy.vec && i0 + TILE <= a.out && j0 + TILE <= a.q.row_groups * 32;
+  const int64_t whole = inside ? (k1 - k0) / BK : 0;
+  multiply<TILE>(la, lb, slices, whole, stage0, stage1, wm, wn, lane, acc);
 #pragma unroll
   for (int mt = 0; mt < MTM; ++mt)
 #pragma unroll
@@ -574,14 +626,19 @@ __global__ __launch_bounds__(2 * TILE) void mx_grad_kernel(GradArgs a) {
         const int64_t t = is / a.B * a.tc + js / a.B;
         base = a.G + (t * a.B + is % a.B) * a.B + j % a.B;
       }
+      auto row = [&](int r) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
+      float v[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int dr = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        float v = is + dr < a.out && j < a.in ? acc[mt][nt][r] : 0.f;
-        float* at = base + dr * ld;
-        if (a.splits == 1 && a.accumulate) v += *at;
-        *at = v;
+      for (int r = 0; r < 16; ++r) v[r] = is + row(r) < a.out && j < a.in ? acc[mt][nt][r] : 0.f;
+      if (a.splits == 1 && a.accumulate) {  // (all loads of a sub-block before its stores)
+        float old[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) old[r] = base[row(r) * ld];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] += old[r];
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) base[row(r) * ld] = v[r];
     }
 }
 
