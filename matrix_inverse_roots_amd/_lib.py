@@ -36,6 +36,21 @@ class DashVec(ctypes.Structure):
 
 
 _lib = None
+_torch_module = None
+_dtypes = {}  # element types by the names that _Args.ptr takes
+_precs = {}  # dash_prec by element type
+
+
+def _torch():
+    """torch, imported at the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _dtypes.update(float32=torch.float32, int32=torch.int32, uint8=torch.uint8)
+        _precs.update({torch.float32: DASH_FP32, torch.float16: DASH_FP16, torch.bfloat16: DASH_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def library() -> ctypes.CDLL:
@@ -115,17 +130,17 @@ class _Args:
     def __init__(self, call: str):
         self.call = call
         self.device = None
+        self.index = -1  # of that device
 
     def _tensor(self, t, name):
-        import torch
-
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _torch().Tensor):
             return False
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError("%s: %s must be a GPU tensor, got one on %s" % (self.call, name, t.device))
+        index = t.get_device()
         if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
+            self.device, self.index = t.device, index
+        elif index != self.index:
             raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, t.device,
                                                                                   self.device))
         return True
@@ -138,9 +153,7 @@ class _Args:
         if isinstance(t, int):
             return t
         if self._tensor(t, name):
-            import torch
-
-            want = {"float32": torch.float32, "int32": torch.int32, "uint8": torch.uint8}.get(dtype)
+            want = _dtypes.get(dtype)
             if want is not None and t.dtype != want:
                 raise ValueError("%s: %s must be %s, got %s" % (self.call, name, dtype, t.dtype))
             if not t.is_contiguous():
@@ -184,8 +197,9 @@ class _Args:
         have = _prec_of(t.dtype)
         if have is None or type not in (None, have):
             raise ValueError("%s: %s must be float32, float16 or bfloat16, got %s" % (self.call, name, t.dtype))
-        if tuple(t.shape) not in (((rows, cols), (1, rows, cols)) if N == 1 else ((N, rows, cols),)):
-            raise ValueError("%s: %s must be [%d, %d, %d], got %s" % (self.call, name, N, rows, cols, tuple(t.shape)))
+        shape = tuple(t.shape)
+        if shape != (N, rows, cols) and (N != 1 or shape != (rows, cols)):
+            raise ValueError("%s: %s must be [%d, %d, %d], got %s" % (self.call, name, N, rows, cols, shape))
         if t.numel() == 0:
             return t.data_ptr(), have, cols
         pitch = t.stride(-2) if rows > 1 else max(cols, t.stride(-2) if N == 1 else t.stride(0))
@@ -217,9 +231,19 @@ class _Args:
     def stream(self, stream):
         if stream is not None:
             return stream if isinstance(stream, int) else stream.cuda_stream
-        import torch
+        torch = _torch()
+        if self.device is None:
+            return torch.cuda.current_stream(None).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)  # (current_stream(device) without its object)
 
-        return torch.cuda.current_stream(self.device).cuda_stream
+    def run(self, fn, *args):
+        """fn(*args) with the tensors' device current, as a launch on that device's default stream needs;
+        raises DashError on a non-OK status."""
+        if self.device is None or self.index == _torch().cuda.current_device():
+            _check(self.call, fn(*args))
+        else:
+            with _torch().cuda.device(self.device):
+                _check(self.call, fn(*args))
 
 
 def _check(name, status):
@@ -235,9 +259,8 @@ def _nbytes(t):
 
 def _prec_of(dtype):
     """The dash_prec of a torch element type (None for others)."""
-    import torch
-
-    return {torch.float32: DASH_FP32, torch.float16: DASH_FP16, torch.bfloat16: DASH_BF16}.get(dtype)
+    _torch()
+    return _precs.get(dtype)
 
 
 def _tiles(shapes, B):
@@ -574,8 +597,7 @@ def dash_apply_vec(X, g_pieces, P: int, B: int, u_pieces, stream=None):
 def mx_buffers(N: int, rows: int, cols: int, fmt: int, device="cuda"):
     """(codes, scales): uint8 tensors [N, rows, bytes of a row] and [N, rows, groups] for N microscaled
     matrices of rows x cols."""
-    import torch
-
+    torch = _torch()
     g = -(-cols // 32)
     return (torch.empty((N, rows, g * (32 if fmt == DASH_MX_E4M3 else 16)), dtype=torch.uint8, device=device),
             torch.empty((N, rows, g), dtype=torch.uint8, device=device))
@@ -589,9 +611,8 @@ def dash_mx_quantize(src, N: int, rows: int, cols: int, fmt: int, codes=None, sc
     p, prec, pitch = a.rows(src, "src", N, rows, cols, type, ld)
     c = a.codes(codes, scales, "codes", N, rows, cols, fmt)
     ct = a.codes(codes_t, scales_t, "codes_t", N, cols, rows, fmt)
-    _check("dash_mx_quantize",
-           library().dash_mx_quantize(p, prec, N, rows, cols, pitch, fmt, *c, *ct, a.ptr(diag, "diag", numel=N * rows),
-                                      a.stream(stream)))
+    a.run(library().dash_mx_quantize, p, prec, N, rows, cols, pitch, fmt, *c, *ct, a.ptr(diag, "diag", numel=N * rows),
+          a.stream(stream))
 
 
 def dash_mx_dequantize(codes, scales, N: int, rows: int, cols: int, fmt: int, dst, diag=None, type=None, ld=None,
@@ -600,18 +621,16 @@ def dash_mx_dequantize(codes, scales, N: int, rows: int, cols: int, fmt: int, ds
     a = _Args("dash_mx_dequantize")
     c = a.codes(codes, scales, "codes", N, rows, cols, fmt)
     p, prec, pitch = a.rows(dst, "dst", N, rows, cols, type, ld)
-    _check("dash_mx_dequantize",
-           library().dash_mx_dequantize(*c, a.ptr(diag, "diag", numel=N * rows), N, rows, cols, fmt, prec, pitch, p,
-                                        a.stream(stream)))
+    a.run(library().dash_mx_dequantize, *c, a.ptr(diag, "diag", numel=N * rows), N, rows, cols, fmt, prec, pitch, p,
+          a.stream(stream))
 
 
 def dash_update_stats_mx(codes, scales, codes_t, scales_t, NG: int, B: int, fmt: int, beta: float, A, stream=None):
     a = _Args("dash_update_stats_mx")
     c = a.codes(codes, scales, "codes", NG, B, B, fmt)
     ct = a.codes(codes_t, scales_t, "codes_t", NG, B, B, fmt)
-    _check("dash_update_stats_mx",
-           library().dash_update_stats_mx(*c, *ct, NG, B, fmt, beta, a.ptr(A, "A", numel=2 * NG * B * B),
-                                          a.stream(stream)))
+    a.run(library().dash_update_stats_mx, *c, *ct, NG, B, fmt, beta, a.ptr(A, "A", numel=2 * NG * B * B),
+          a.stream(stream))
 
 
 def dash_apply_mx(XL, XL_scales, XR, XR_scales, G_stack, NG: int, B: int, fmt: int, U_stack, XL_diag=None, XR_diag=None,
@@ -620,10 +639,9 @@ def dash_apply_mx(XL, XL_scales, XR, XR_scales, G_stack, NG: int, B: int, fmt: i
     n = NG * B * B
     cl = a.codes(XL, XL_scales, "XL", NG, B, B, fmt)
     cr = a.codes(XR, XR_scales, "XR", NG, B, B, fmt)
-    _check("dash_apply_mx",
-           library().dash_apply_mx(*cl, a.ptr(XL_diag, "XL_diag", numel=NG * B), *cr,
-                                   a.ptr(XR_diag, "XR_diag", numel=NG * B), a.ptr(G_stack, "G_stack", numel=n), NG, B,
-                                   fmt, a.ptr(U_stack, "U_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream)))
+    a.run(library().dash_apply_mx, *cl, a.ptr(XL_diag, "XL_diag", numel=NG * B), *cr,
+          a.ptr(XR_diag, "XR_diag", numel=NG * B), a.ptr(G_stack, "G_stack", numel=n), NG, B, fmt,
+          a.ptr(U_stack, "U_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream))
 
 
 def dash_grad_stack_mx_workspace(T: int, out_features: int, in_features: int, type: int) -> int:
@@ -650,6 +668,5 @@ def dash_grad_stack_mx(dY, codes, scales, fmt: int, T: int, out_features: int, i
     p, prec, pitch = a.rows(dY, "dY", 1, T, out_features, type, ldy)
     c = a.codes(codes, scales, "codes", 1, T, in_features, fmt)
     n = _tiles([(out_features, in_features)], B) * B * B
-    _check("dash_grad_stack_mx",
-           library().dash_grad_stack_mx(p, prec, pitch, *c, fmt, T, out_features, in_features, B, int(bool(accumulate)),
-                                        a.ptr(G_stack, "G_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream)))
+    a.run(library().dash_grad_stack_mx, p, prec, pitch, *c, fmt, T, out_features, in_features, B, int(bool(accumulate)),
+          a.ptr(G_stack, "G_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream))
