@@ -99,10 +99,14 @@ dash_status grad_shape_check(int64_t T, int64_t out, int64_t in, int64_t ldy, da
   return most > MX_MAX_ELEMENTS ? DASH_ERR_SHAPE : DASH_OK;
 }
 // apply: the intermediate stack T = XL G, and for two-piece binary16 products the bounds of XL, G
-// and XR per block and T's per-wave maxima
+// and XR per block and T's per-wave maxima (with microscaled roots G's bound and the roots' scale bytes
+// in mx_apply_parts pieces, and T's maxima at up to mx_apply_waves)
 size_t ws_apply(int64_t N, int B) {
-  return stack_bytes(N, B, DASH_FP32) + 3 * align_up((size_t)N * sizeof(float), 256) +
-         align_up((size_t)N * ndb_parts(B) * sizeof(float), 256);
+  const size_t fp32 = 3 * align_up((size_t)N * sizeof(float), 256) +
+                      align_up((size_t)N * ndb_parts(B) * sizeof(float), 256);
+  const size_t mx = 2 * align_up((size_t)N * mx_apply_parts(B) * sizeof(float), 256) +
+                    align_up((size_t)N * mx_apply_waves(B) * sizeof(float), 256);
+  return stack_bytes(N, B, DASH_FP32) + (fp32 > mx ? fp32 : mx);
 }
 size_t ndb_bound_bytes(int64_t N, int B) {
   return align_up((size_t)N * sizeof(float), 256) + 5 * align_up((size_t)N * ndb_parts(B) * sizeof(float), 256);
@@ -1765,10 +1769,21 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
   if (!valid_B(B)) return DASH_ERR_SHAPE;
   if (!ws || !aligned(ws, 256) || ws_bytes < ws_apply(NG, B)) return DASH_ERR_WORKSPACE;
   Carver cv{(char*)ws, ws_bytes};
-  float* T = (float*)cv.take(stack_bytes(NG, B, DASH_FP32));
-  hipStream_t st = as_stream(stream);
-  TRY(launch_mx_apply(mx_codes(XL, XL_scales, B, B, fmt), XL_diag, G_stack, NG, B, fmt, true, T, st));
-  TRY(launch_mx_apply(mx_codes(XR, XR_scales, B, B, fmt), XR_diag, T, NG, B, fmt, false, U_stack, st));
+  MxApply p;
+  p.N = NG;
+  p.B = B;
+  p.xl = mx_codes(XL, XL_scales, B, B, fmt);
+  p.xr = mx_codes(XR, XR_scales, B, B, fmt);
+  p.xl_diag = XL_diag;
+  p.xr_diag = XR_diag;
+  p.G = G_stack;
+  p.U = U_stack;
+  p.parts = mx_apply_parts(B);
+  p.T = (float*)cv.take(stack_bytes(NG, B, DASH_FP32));
+  p.amax_g = (float*)cv.take((size_t)NG * p.parts * sizeof(float));
+  p.bytes = (unsigned*)cv.take((size_t)NG * p.parts * sizeof(unsigned));
+  p.amax_t = (float*)cv.take((size_t)NG * mx_apply_waves(B) * sizeof(float));
+  TRY(launch_mx_apply(p, fmt, as_stream(stream)));
   return DASH_OK;
 }
 

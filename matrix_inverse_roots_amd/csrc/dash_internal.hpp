@@ -323,12 +323,25 @@ hipError_t launch_mx_dequantize(const void* codes, const void* scales, const flo
                                 int64_t cols, dash_mx_fmt fmt, dash_prec type, int64_t ld, void* dst,
                                 hipStream_t stream);
 // Products with microscaled operands (mx_gemm.hip): A = [L; R] <- beta A + (1 - beta) [Q Q^T; Q' Q'^T] from
-// the codes of G's rows and columns; out = Q X (left) or X Q^T, with the root's fp32 diagonal; gradient
-// tiles dY^T Q in launch_tile_copy's order (ws: mx_grad_workspace_bytes).
+// the codes of G's rows and columns; gradient tiles dY^T Q in launch_tile_copy's order (ws:
+// mx_grad_workspace_bytes); the update below.
 hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG, int B, dash_mx_fmt fmt, float beta,
                            float* A, hipStream_t stream);
-hipError_t launch_mx_apply(const MxCodes& q, const float* diag, const float* X, int64_t NG, int B, dash_mx_fmt fmt,
-                           bool left, float* out, hipStream_t stream);
+// U = (XL G) XR^T: the roots' row codes and fp32 diagonals (or null), the intermediate T [N, B, B], and
+// bounds per block: max|G| and both roots' largest scale bytes in mx_apply_parts(B) pieces, max|T| in at
+// most mx_apply_waves(B) pieces
+struct MxApply {
+  int64_t N;
+  int B;
+  MxCodes xl, xr;
+  const float *xl_diag, *xr_diag, *G;
+  float *T, *U, *amax_g, *amax_t;
+  unsigned* bytes;
+  int parts;
+};
+inline int mx_apply_parts(int B) { return B >= 1024 ? 16 : B >= 512 ? 4 : 1; }
+inline int64_t mx_apply_waves(int B) { return (int64_t)(B / 64) * (B / 64) * 2; }
+hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream);
 size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in);
 hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
                           int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream);

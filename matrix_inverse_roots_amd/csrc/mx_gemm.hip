@@ -32,7 +32,6 @@ using IC = std::integral_constant<int, V>;
 constexpr int BK = 32;  // k-slice: one scale group
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -45,46 +44,59 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // counts, so a scale byte in that field is the scale (255 makes the results NaN).
 __device__ __forceinline__ float scale_of(unsigned byte) { return __builtin_bit_cast(float, byte << 23); }
 
-// 8 consecutive elements to bfloat16, from 8 bytes (E4M3) or 4 bytes (E2M1)
+// Two elements to bfloat16 or binary16: the two of a byte (E2M1, byte I of w) or of half a word (E4M3,
+// half I of w)
+template <typename TE>
+struct Pair;
+template <>
+struct Pair<__bf16> {
+  typedef bf16x2 type;
+  template <int I>
+  static __device__ __forceinline__ type e4m3(unsigned w, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, I);
+  }
+  template <int I>
+  static __device__ __forceinline__ type e2m1(unsigned w, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, I);
+  }
+};
+template <>
+struct Pair<_Float16> {
+  typedef f16x2 type;
+  template <int I>
+  static __device__ __forceinline__ type e4m3(unsigned w, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, I);
+  }
+  template <int I>
+  static __device__ __forceinline__ type e2m1(unsigned w, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, I);
+  }
+};
+
+// 8 consecutive elements, from 8 bytes (E4M3) or 4 (E2M1).  TOP: the exponent t for which the largest
+// element value times 2^t is in [2^13, 2^14)
 template <int F>
 struct Elem;
 template <>
 struct Elem<DASH_MX_E4M3> {
   typedef u32x2 raw8;
-  static constexpr int BITS = 8;
-  static __device__ __forceinline__ bf16x8 decode(raw8 r, float s) {
-    bf16x8 v;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[w], s, false);
-      const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[w], s, true);
-      v[4 * w] = a[0];
-      v[4 * w + 1] = a[1];
-      v[4 * w + 2] = b[0];
-      v[4 * w + 3] = b[1];
-    }
-    return v;
+  static constexpr int BITS = 8, TOP = 5;
+  template <typename TE>
+  static __device__ __forceinline__ typename Half<TE>::v8 decode(raw8 r, float s) {
+    const auto a = Pair<TE>::template e4m3<0>(r[0], s), b = Pair<TE>::template e4m3<1>(r[0], s);
+    const auto c = Pair<TE>::template e4m3<0>(r[1], s), d = Pair<TE>::template e4m3<1>(r[1], s);
+    return typename Half<TE>::v8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   }
 };
 template <>
 struct Elem<DASH_MX_E2M1> {
   typedef unsigned raw8;
-  static constexpr int BITS = 4;
-  static __device__ __forceinline__ bf16x8 decode(raw8 r, float s) {
-    bf16x8 v;
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 0);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 1);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 2);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 3);
-    v[0] = a[0];
-    v[1] = a[1];
-    v[2] = b[0];
-    v[3] = b[1];
-    v[4] = c[0];
-    v[5] = c[1];
-    v[6] = d[0];
-    v[7] = d[1];
-    return v;
+  static constexpr int BITS = 4, TOP = 11;
+  template <typename TE>
+  static __device__ __forceinline__ typename Half<TE>::v8 decode(raw8 r, float s) {
+    const auto a = Pair<TE>::template e2m1<0>(r, s), b = Pair<TE>::template e2m1<1>(r, s);
+    const auto c = Pair<TE>::template e2m1<2>(r, s), d = Pair<TE>::template e2m1<3>(r, s);
+    return typename Half<TE>::v8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   }
 };
 
@@ -123,10 +135,10 @@ __device__ __forceinline__ int ks_at(int k, int col) {
 
 // The MFMA operand of rows (columns) base .. base + 31, k = 16 ks .. 16 ks + 15: lane l holds row
 // l % 32, k = 8 (l / 32) .. + 7.
-template <int TILE, bool KS>
-__device__ __forceinline__ bf16x8 fragment(const __bf16* plane, int base, int ks, int lane) {
+template <int TILE, bool KS, typename TE>
+__device__ __forceinline__ typename Half<TE>::v8 fragment(const TE* plane, int base, int ks, int lane) {
   if constexpr (!KS) {
-    return *(const bf16x8*)&plane[kc_at(base + (lane & 31), 2 * ks + (lane >> 5))];
+    return *(const typename Half<TE>::v8*)&plane[kc_at(base + (lane & 31), 2 * ks + (lane >> 5))];
   } else {
     // transposing load: in each group of 16 lanes, lane 4 r + c points at four columns of row r; lane i
     // receives column i of the group's four rows
@@ -135,8 +147,7 @@ __device__ __forceinline__ bf16x8 fragment(const __bf16* plane, int base, int ks
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&plane[ks_at<TILE>(k, col)]);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&plane[ks_at<TILE>(k + 4, col)]);
-    const bf16x4 a = __builtin_bit_cast(bf16x4, lo), b = __builtin_bit_cast(bf16x4, hi);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(typename Half<TE>::v8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 }
 
@@ -149,8 +160,10 @@ __device__ __forceinline__ bf16x8 fragment(const __bf16* plane, int base, int ks
 // D: slices in the register ring, 4 where an operand is 16 bits wide or less and 2 beside fp32 (four
 // slices of it spill)
 // Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
-template <int F, int TILE, int D>
+// shift: added to the scale bytes (a power of two on every element).
+template <int F, int TILE, int D, typename E>
 struct CodesK {
+  typedef E TE;
   static constexpr int DEPTH = D;
   static constexpr int PIECES = 1;
   static constexpr bool KS = false;
@@ -159,10 +172,11 @@ struct CodesK {
   unsigned off_c, off_s;
   raw8 r[DEPTH][2];
   unsigned sc[DEPTH];
-  int row, half;
-  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int tid) {
+  int row, half, shift;
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int tid, int shift_ = 0) {
     row = tid >> 1;
     half = tid & 1;
+    shift = shift_;
     const int64_t at = b * q.rows + r0;
     c = q.codes + at * q.row_bytes;
     s = q.scales + at * q.row_groups;
@@ -177,11 +191,16 @@ struct CodesK {
     sc[SLOT] = (s + kt)[off_s];
   }
   template <int SLOT>
-  __device__ __forceinline__ void store(__bf16* planes) const {
-    const float f = scale_of(sc[SLOT]);
+  __device__ __forceinline__ void store(TE* planes) const {
+    unsigned byte = sc[SLOT];
+    if (!std::is_same<TE, __bf16>::value) {
+      const int moved = (int)byte + shift;
+      byte = byte == 255u ? 255u : moved > 0 ? (unsigned)moved : 0u;
+    }
+    const float f = scale_of(byte);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *(bf16x8*)&planes[kc_at(row, 2 * half + i)] = Elem<F>::decode(r[SLOT][i], f);
+      *(typename Half<TE>::v8*)&planes[kc_at(row, 2 * half + i)] = Elem<F>::template decode<TE>(r[SLOT][i], f);
   }
 };
 
@@ -189,6 +208,7 @@ struct CodesK {
 // slice's rows, 16 apart.  Columns beyond the stored row and rows beyond K are zero.
 template <int F, int TILE, int D>
 struct CodesCol {
+  typedef __bf16 TE;
   static constexpr int DEPTH = D;
   static constexpr int PIECES = 1;
   static constexpr bool KS = true;
@@ -228,23 +248,29 @@ struct CodesCol {
   __device__ __forceinline__ void store(__bf16* planes) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *(bf16x8*)&planes[ks_at<TILE>(k + 16 * i, col)] = Elem<F>::decode(r[SLOT][i], scale_of(sc[SLOT][i]));
+      *(bf16x8*)&planes[ks_at<TILE>(k + 16 * i, col)] =
+          Elem<F>::template decode<TE>(r[SLOT][i], scale_of(sc[SLOT][i]));
   }
 };
 
-// fp32, k contiguous, three pieces: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
+// fp32, k contiguous, two binary16 pieces of 2^e x: thread t holds 16 k of row t / 2.  Rows of the tile
+// all exist.  m1 is -1 (see split2).
 template <int TILE, int D>
 struct FloatK {
+  typedef _Float16 TE;
   static constexpr int DEPTH = D;
-  static constexpr int PIECES = 3;
+  static constexpr int PIECES = 2;
   static constexpr bool KS = false;
   const float* p;
   unsigned off;
-  f32x4 r[DEPTH][4];
-  int row, half;
-  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int tid) {
+  f32x4 r[D][4];
+  int row, half, e;
+  float m1;
+  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int tid, int e_, float m1_) {
     row = tid >> 1;
     half = tid & 1;
+    e = e_;
+    m1 = m1_;
     p = (const float*)x.p + b * x.stride + r0 * x.ld;
     off = (unsigned)row * (unsigned)x.ld + 16 * half;
   }
@@ -254,20 +280,64 @@ struct FloatK {
     for (int i = 0; i < 4; ++i) r[SLOT][i] = *(const f32x4*)(p + kt * BK + off + 4 * i);
   }
   template <int SLOT>
-  __device__ __forceinline__ void store(__bf16* planes) const {
+  __device__ __forceinline__ void store(TE* planes) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float x[8] = {r[SLOT][2 * i][0],     r[SLOT][2 * i][1],     r[SLOT][2 * i][2],     r[SLOT][2 * i][3],
-                          r[SLOT][2 * i + 1][0], r[SLOT][2 * i + 1][1], r[SLOT][2 * i + 1][2], r[SLOT][2 * i + 1][3]};
-      bf16x8 v[3];
-      pieces<3>(x, v);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) *(bf16x8*)&planes[q * TILE * BK + kc_at(row, 2 * half + i)] = v[q];
+      f16x8 p0, p1;
+      split2(r[SLOT][2 * i], r[SLOT][2 * i + 1], e, m1, p0, p1);
+      TE* at = planes + kc_at(row, 2 * half + i);
+      *(f16x8*)at = p0;
+      *(f16x8*)(at + TILE * BK) = p1;
     }
   }
 };
 
-// fp32, bfloat16 or binary16, k the slow axis: thread t holds 8 columns of two of the slice's rows, 16
+// fp32, k the slow axis, two binary16 pieces of 2^e x: thread t holds 8 columns of two of the slice's
+// rows, 16 apart.  The tile's columns and the slices' rows all exist.
+template <int TILE, int D>
+struct FloatCol16 {
+  typedef _Float16 TE;
+  static constexpr int DEPTH = D;
+  static constexpr int PIECES = 2;
+  static constexpr bool KS = true;
+  const float* p;
+  unsigned off;
+  f32x4 r[D][2][2];
+  int64_t ld;
+  int k, col, e;
+  float m1;
+  __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t c0, int tid, int e_, float m1_) {
+    col = 8 * (tid % (TILE / 8));
+    k = tid / (TILE / 8);
+    ld = x.ld;
+    e = e_;
+    m1 = m1_;
+    p = (const float*)x.p + b * x.stride + c0;
+    off = (unsigned)k * (unsigned)ld + col;
+  }
+  template <int SLOT, bool CHECK>
+  __device__ __forceinline__ void load(int64_t kt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* q = p + (kt * BK + 16 * i) * ld + off;
+      r[SLOT][i][0] = *(const f32x4*)q;
+      r[SLOT][i][1] = *(const f32x4*)(q + 4);
+    }
+  }
+  template <int SLOT>
+  __device__ __forceinline__ void store(TE* planes) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f16x8 p0, p1;
+      split2(r[SLOT][i][0], r[SLOT][i][1], e, m1, p0, p1);
+      TE* at = planes + ks_at<TILE>(k + 16 * i, col);
+      *(f16x8*)at = p0;
+      *(f16x8*)(at + TILE * BK) = p1;
+    }
+  }
+};
+
+// fp32, bfloat16 or binary16, k the slow axis, in bfloat16 pieces: thread t holds 8 columns of two of the slice's rows, 16
 // apart.  Columns and rows beyond the matrix are zero; only elements of the matrix are read.
 template <typename T>
 struct Pieces {
@@ -275,6 +345,7 @@ struct Pieces {
 };
 template <typename T, int TILE, int D>
 struct FloatCol {
+  typedef __bf16 TE;
   static constexpr int DEPTH = D;
   static constexpr int PIECES = Pieces<T>::N;
   static constexpr bool KS = true;
@@ -358,12 +429,14 @@ struct Shape<64> {
 
 // slices: of k; whole: the leading ones that need no checks
 template <int TILE, typename LA, typename LB>
-__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t whole, __bf16* stage0, __bf16* stage1,
-                                         int wm, int wn, int lane,
+__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t whole, typename LA::TE* stage0,
+                                         typename LA::TE* stage1, int wm, int wn, int lane,
                                          f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
   constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
   constexpr int PLANE = TILE * BK;
   constexpr int PA = LA::PIECES, PB = LB::PIECES;
+  typedef typename LA::TE TE;
+  static_assert(std::is_same<TE, typename LB::TE>::value, "operands of one type");
   constexpr int DEPTH = LA::DEPTH;
   static_assert(DEPTH == LB::DEPTH && (DEPTH == 2 || DEPTH == 4), "the loops below step through 2 or 4 slots");
 #pragma unroll
@@ -374,12 +447,12 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
       for (int r = 0; r < 16; ++r) acc[mt][nt][r] = 0.f;
   if (slices <= 0) return;
 
-  auto compute = [&](const __bf16* st) {
+  auto compute = [&](const TE* st) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
       for (int pb = 0; pb < PB; ++pb) {
-        bf16x8 bv[MTN];
+        typename Half<TE>::v8 bv[MTN];
 #pragma unroll
         for (int nt = 0; nt < MTN; ++nt)
           bv[nt] = fragment<TILE, LB::KS>(st + (PA + pb) * PLANE, (wn * MTN + nt) * 32, ks, lane);
@@ -387,9 +460,9 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
         for (int pa = 0; pa < PA; ++pa)
 #pragma unroll
           for (int mt = 0; mt < MTM; ++mt) {
-            const bf16x8 av = fragment<TILE, LA::KS>(st + pa * PLANE, (wm * MTM + mt) * 32, ks, lane);
+            const auto av = fragment<TILE, LA::KS>(st + pa * PLANE, (wm * MTM + mt) * 32, ks, lane);
 #pragma unroll
-            for (int nt = 0; nt < MTN; ++nt) acc[mt][nt] = Half<__bf16>::mfma(av, bv[nt], acc[mt][nt]);
+            for (int nt = 0; nt < MTN; ++nt) acc[mt][nt] = Half<TE>::mfma(av, bv[nt], acc[mt][nt]);
           }
       }
   };
@@ -399,7 +472,7 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
   };
   auto store = [&](auto slot_c) {  // (slices alternate between the stages)
     constexpr int slot = decltype(slot_c)::value;
-    __bf16* st = slot & 1 ? stage1 : stage0;
+    TE* st = slot & 1 ? stage1 : stage0;
     la.template store<slot>(st);
     lb.template store<slot>(st + PA * PLANE);
   };
@@ -466,7 +539,7 @@ __global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
   const MxCodes q = tc.prob ? a.q[1] : a.q[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
-  CodesK<F, TILE, 4> la, lb;
+  CodesK<F, TILE, 4, __bf16> la, lb;
   la.init(q, tc.b, tc.ti * TILE, tid);
   lb.init(q, tc.b, tc.tj * TILE, tid);
   f32x16 acc[MTM][MTN];
@@ -493,50 +566,81 @@ hipError_t launch_stats(StatsArgs& a, hipStream_t stream) {
 // ------------------------------------------------------------------------------------------------
 // Update: T = XL G and U = T XR^T, each with the root's diagonal added in fp32
 // ------------------------------------------------------------------------------------------------
+//
+// The floating operand is brought to binary16's upper range by a power of two per block (2^13 <= 2^e
+// max|x| < 2^14) and cut into two binary16 pieces, which hold 22 of its 24 significant bits (see
+// gemm_split.hip); the root's elements are binary16 numbers under a power of two per block (the largest
+// scale's elements below 2^14; elements 2^-38 of the block's largest lose bits to binary16's
+// subnormals).  Two matrix passes per product, where bfloat16 pieces would take three.
 
 struct ApplyArgs {
   GemmArgs g;  // N, B and the tile map only
   MxCodes q;
   MxFloats x;
-  const float* diag;  // [N, B] or null: + diag[i] x[i][j] (LEFT) or + x[i][j] diag[j]
+  const float* diag;      // [N, B] or null: + diag[i] x[i][j] (LEFT) or + x[i][j] diag[j]
   float* out;
+  const float* amax;      // [N, parts]: bounds of |x|
+  int parts;
+  const unsigned* bytes;  // [N, byte_parts]: the largest scale byte short of 255 of XL and (<< 8) of XR
+  int byte_parts;
+  float* amax_out;        // LEFT: [N, tiles, waves]: the largest |out| each wave stored
 };
 
 // LEFT: out = Q X (Q's rows, X's columns); else out = X Q^T (X's rows, Q's rows as columns)
 template <int F, int TILE, bool LEFT>
 __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
-  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
-  constexpr int STAGE = 4 * TILE * BK;
-  __shared__ __attribute__((aligned(16))) __bf16 stage0[STAGE];
-  __shared__ __attribute__((aligned(16))) __bf16 stage1[STAGE];
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, WAVES = TILE / 32;
+  constexpr int STAGE = 3 * TILE * BK;
+  __shared__ __attribute__((aligned(16))) _Float16 stage0[STAGE];
+  __shared__ __attribute__((aligned(16))) _Float16 stage1[STAGE];
   const TileCoord tc = decode_tile(a.g, false);
   const int B = a.g.B;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
+  float m = 0.f;
+  unsigned top = 0;
+  for (int p = lane; p < a.parts; p += 64) m = fmaxf(m, a.amax[tc.b * a.parts + p]);
+  for (int p = lane; p < a.byte_parts; p += 64) {
+    const unsigned v = a.bytes[tc.b * a.byte_parts + p];
+    const unsigned c = LEFT ? v & 255u : v >> 8;
+    top = c > top ? c : top;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned c = __shfl_xor(top, o, 64);
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    top = c > top ? c : top;
+  }
+  const int ex = __builtin_amdgcn_readfirstlane(top_exp(m));
+  const int shift = __builtin_amdgcn_readfirstlane(127 + Elem<F>::TOP - (int)top);
+  float m1 = -1.f;
+  asm("" : "+s"(m1));  // (no instruction: hides the constant -1 from the optimiser)
   f32x16 acc[MTM][MTN];
+  CodesK<F, TILE, 2, _Float16> lq;
+  lq.init(a.q, tc.b, (LEFT ? tc.ti : tc.tj) * TILE, tid, shift);
   if constexpr (LEFT) {
-    CodesK<F, TILE, 2> la;
-    FloatCol<float, TILE, 2> lb;
-    la.init(a.q, tc.b, tc.ti * TILE, tid);
-    lb.init(a.x, tc.b, tc.tj * TILE, 0, B, tid);
-    multiply<TILE>(la, lb, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
+    FloatCol16<TILE, 2> lx;
+    lx.init(a.x, tc.b, tc.tj * TILE, tid, ex, m1);
+    multiply<TILE>(lq, lx, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
   } else {
-    FloatK<TILE, 2> la;
-    CodesK<F, TILE, 2> lb;
-    la.init(a.x, tc.b, tc.ti * TILE, tid);
-    lb.init(a.q, tc.b, tc.tj * TILE, tid);
-    multiply<TILE>(la, lb, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
+    FloatK<TILE, 2> lx;
+    lx.init(a.x, tc.b, tc.ti * TILE, tid, ex, m1);
+    multiply<TILE>(lx, lq, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
   }
   const int64_t off = tc.b * (int64_t)B * B;
   const float* x = (const float*)a.x.p + off;
   const float* dg = a.diag ? a.diag + tc.b * B : nullptr;
   float* out = a.out + off;
+  const int es = -ex - shift;
+  float most = 0.f;
 #pragma unroll
   for (int mt = 0; mt < MTM; ++mt)
 #pragma unroll
     for (int nt = 0; nt < MTN; ++nt) {
       const int i0 = tc.ti * TILE + (wm * MTM + mt) * 32 + 4 * (lane >> 5);
       const int j = tc.tj * TILE + (wn * MTN + nt) * 32 + (lane & 31);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[mt][nt][r] = ldexpf(acc[mt][nt][r], es);
       // (all loads of a sub-block before its stores)
       if (dg) {
         float xv[16], dv[16];
@@ -550,18 +654,96 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
         for (int r = 0; r < 16; ++r) acc[mt][nt][r] += xv[r] * dv[r];
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r) out[(i0 + 8 * (r >> 2) + (r & 3)) * B + j] = acc[mt][nt][r];
+      for (int r = 0; r < 16; ++r) {
+        out[(i0 + 8 * (r >> 2) + (r & 3)) * B + j] = acc[mt][nt][r];
+        if (LEFT) most = fmaxf(most, fabsf(acc[mt][nt][r]));  // (NaN leaves it unchanged)
+      }
     }
+  if (LEFT) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+    if (lane == 0) a.amax_out[(tc.b * a.g.tiles + tc.ti * a.g.tdim + tc.tj) * WAVES + wave] = most;
+  }
 }
 
-template <int F, int TILE, bool LEFT>
-hipError_t launch_apply_one(ApplyArgs& a, hipStream_t stream) {
-  a.g.tdim = a.g.B / TILE;
+// Bounds of a block in `parts` pieces: max|G| (NaN passed over) and both roots' largest scale bytes
+__global__ __launch_bounds__(256) void mx_bounds_kernel(const float* G, const uint8_t* sl, const uint8_t* sr, int B,
+                                                        int parts, float* amax, unsigned* bytes) {
+  const int64_t b = blockIdx.x / parts;
+  const int p = (int)(blockIdx.x - b * parts);
+  const int64_t n = (int64_t)B * B / parts, ns = (int64_t)B * B / MX_GROUP / parts;
+  const f32x4* g = (const f32x4*)(G + b * B * B + p * n);
+  float m = 0.f;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < n / 4; i += 256) {
+    const f32x4 v = g[i];
+    m = fmaxf(m, fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+  }
+  const int64_t s0 = b * B * B / MX_GROUP + p * ns;
+  unsigned l = 0, r = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < ns; i += 256) {
+    const unsigned x = sl[s0 + i], y = sr[s0 + i];
+    l = x != 255u && x > l ? x : l;
+    r = y != 255u && y > r ? y : r;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned x = __shfl_xor(l, o, 64), y = __shfl_xor(r, o, 64);
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    l = x > l ? x : l;
+    r = y > r ? y : r;
+  }
+  __shared__ float ms[4];
+  __shared__ unsigned bs[4];
+  if ((threadIdx.x & 63) == 0) {
+    ms[threadIdx.x >> 6] = m;
+    bs[threadIdx.x >> 6] = l | r << 8;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 4; ++w) {
+      m = fmaxf(m, ms[w]);
+      l = (bs[w] & 255u) > l ? bs[w] & 255u : l;
+      r = (bs[w] >> 8) > r ? bs[w] >> 8 : r;
+    }
+    amax[blockIdx.x] = m;
+    bytes[blockIdx.x] = l | r << 8;
+  }
+}
+
+template <int F, int TILE>
+hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream) {
+  const int B = p.B;
+  a.g.tdim = B / TILE;
   a.g.tiles = a.g.tdim * a.g.tdim;
-  const int64_t grid = a.g.N * a.g.tiles;
+  const int64_t grid = p.N * a.g.tiles;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, LEFT>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  a.q = p.xl;
+  a.diag = p.xl_diag;
+  a.x.p = p.G;
+  a.out = p.T;
+  a.amax = p.amax_g;
+  a.parts = p.parts;
+  a.amax_out = p.amax_t;
+  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, true>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.q = p.xr;
+  a.diag = p.xr_diag;
+  a.x.p = p.T;
+  a.out = p.U;
+  a.amax = p.amax_t;
+  a.parts = a.g.tiles * (TILE / 32);
+  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, false>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   return hipGetLastError();
+}
+
+template <int F>
+hipError_t launch_apply_fmt(ApplyArgs& a, const MxApply& p, hipStream_t stream) {
+  return p.B % 256 == 0   ? launch_apply_tile<F, 256>(a, p, stream)
+         : p.B % 128 == 0 ? launch_apply_tile<F, 128>(a, p, stream)
+                          : launch_apply_tile<F, 64>(a, p, stream);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -742,32 +924,24 @@ hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG,
                         : launch_stats<DASH_MX_E2M1, 64>(a, stream);
 }
 
-template <int F>
-static hipError_t apply_tile(ApplyArgs& a, bool left, hipStream_t stream) {
-  const int B = a.g.B;
-  if (left)
-    return B % 256 == 0   ? launch_apply_one<F, 256, true>(a, stream)
-           : B % 128 == 0 ? launch_apply_one<F, 128, true>(a, stream)
-                          : launch_apply_one<F, 64, true>(a, stream);
-  return B % 256 == 0   ? launch_apply_one<F, 256, false>(a, stream)
-         : B % 128 == 0 ? launch_apply_one<F, 128, false>(a, stream)
-                        : launch_apply_one<F, 64, false>(a, stream);
-}
-
-hipError_t launch_mx_apply(const MxCodes& q, const float* diag, const float* X, int64_t NG, int B, dash_mx_fmt fmt,
-                           bool left, float* out, hipStream_t stream) {
+hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream) {
+  const int64_t grid = p.N * p.parts;
+  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(mx_bounds_kernel, dim3((unsigned)grid), dim3(256), 0, stream, p.G, p.xl.scales, p.xr.scales, p.B,
+                     p.parts, p.amax_g, p.bytes);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   ApplyArgs a;
-  a.g.N = NG;
-  a.g.B = B;
+  a.g.N = p.N;
+  a.g.B = p.B;
   a.g.nprob = 1;
-  a.q = q;
-  a.x.p = X;
-  a.x.ld = B;
-  a.x.stride = (int64_t)B * B;
-  a.x.cols = B;
-  a.diag = diag;
-  a.out = out;
-  return fmt == DASH_MX_E4M3 ? apply_tile<DASH_MX_E4M3>(a, left, stream) : apply_tile<DASH_MX_E2M1>(a, left, stream);
+  a.x.ld = p.B;
+  a.x.stride = (int64_t)p.B * p.B;
+  a.x.cols = p.B;
+  a.bytes = p.bytes;
+  a.byte_parts = p.parts;
+  return fmt == DASH_MX_E4M3 ? launch_apply_fmt<DASH_MX_E4M3>(a, p, stream)
+                             : launch_apply_fmt<DASH_MX_E2M1>(a, p, stream);
 }
 
 size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in) {
