@@ -120,9 +120,12 @@ __device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&p)[P]) {
 // LDS planes: TILE x 32 bfloat16
 // ------------------------------------------------------------------------------------------------
 
-// [row][32 k]: rows of four 16-byte chunks; the chunk index is xored with bits 2-3 of the row, so
-// the 16-byte reads of 16 consecutive rows fall on 16 distinct slots of the 64 banks
-__device__ __forceinline__ int kc_at(int row, int chunk) { return row * BK + 8 * (chunk ^ ((row >> 2) & 3)); }
+// [row][32 k]: rows of four 16-byte chunks; the chunk index is xored with bits 2-3 and bit 1 of the row.
+// The 16-byte reads of 16 rows then fall on 16 distinct slots of 256 bytes, and the 16-byte writes of 8
+// lanes (two chunks of four rows, or four of two) on 8 distinct slots of 128 bytes
+__device__ __forceinline__ int kc_at(int row, int chunk) {
+  return row * BK + 8 * (chunk ^ ((row >> 2) & 3) ^ ((row >> 1) & 1));
+}
 
 // [k][TILE]: the 64-byte block of 32 columns is xored with k % 4 (with 64 columns, two blocks to a row
 // of half the banks, with bit 1 of k), so the four rows that one transposing load reads fall on distinct
@@ -157,8 +160,7 @@ __device__ __forceinline__ typename Half<TE>::v8 fragment(const TE* plane, int b
 // into LDS planes.  An address is a wave-uniform base that moves with kt plus a 32-bit lane offset.
 // ------------------------------------------------------------------------------------------------
 
-// D: slices in the register ring, 4 where an operand is 16 bits wide or less and 2 beside fp32 (four
-// slices of it spill)
+// D: slices in the register ring, 4, but 2 beside fp32 in 256 x 256 tiles (where four spill)
 // Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
 // shift: added to the scale bytes (a power of two on every element).
 template <int F, int TILE, int D, typename E>
@@ -253,8 +255,8 @@ struct CodesCol {
   }
 };
 
-// fp32, k contiguous, two binary16 pieces of 2^e x: thread t holds 16 k of row t / 2.  Rows of the tile
-// all exist.  m1 is -1 (see split2).
+// fp32, k contiguous, two binary16 pieces of 2^e x: thread t holds 8 k of rows t / 4 and t / 4 + TILE / 2
+// (four lanes read a row's 128 bytes).  Rows of the tile all exist.  m1 is -1 (see split2).
 template <int TILE, int D>
 struct FloatK {
   typedef _Float16 TE;
@@ -263,29 +265,35 @@ struct FloatK {
   static constexpr bool KS = false;
   const float* p;
   unsigned off;
-  f32x4 r[D][4];
-  int row, half, e;
+  f32x4 r[D][2][2];
+  int64_t half;  // elements from one of the thread's rows to the other
+  int row, chunk, e;
   float m1;
   __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int tid, int e_, float m1_) {
-    row = tid >> 1;
-    half = tid & 1;
+    row = tid >> 2;
+    chunk = tid & 3;
     e = e_;
     m1 = m1_;
     p = (const float*)x.p + b * x.stride + r0 * x.ld;
-    off = (unsigned)row * (unsigned)x.ld + 16 * half;
+    half = x.ld * (TILE / 2);
+    off = (unsigned)row * (unsigned)x.ld + 8 * chunk;
   }
   template <int SLOT, bool CHECK>
   __device__ __forceinline__ void load(int64_t kt) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[SLOT][i] = *(const f32x4*)(p + kt * BK + off + 4 * i);
+    for (int i = 0; i < 2; ++i) {
+      const float* q = p + kt * BK + i * half + off;
+      r[SLOT][i][0] = *(const f32x4*)q;
+      r[SLOT][i][1] = *(const f32x4*)(q + 4);
+    }
   }
   template <int SLOT>
   __device__ __forceinline__ void store(TE* planes) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       f16x8 p0, p1;
-      split2(r[SLOT][2 * i], r[SLOT][2 * i + 1], e, m1, p0, p1);
-      TE* at = planes + kc_at(row, 2 * half + i);
+      split2(r[SLOT][i][0], r[SLOT][i][1], e, m1, p0, p1);
+      TE* at = planes + kc_at(row + i * (TILE / 2), chunk);
       *(f16x8*)at = p0;
       *(f16x8*)(at + TILE * BK) = p1;
     }
@@ -427,44 +435,57 @@ struct Shape<64> {
   static constexpr int WN = 1, MTM = 1, MTN = 2;
 };
 
-// slices: of k; whole: the leading ones that need no checks
-template <int TILE, typename LA, typename LB>
-__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t whole, typename LA::TE* stage0,
-                                         typename LA::TE* stage1, int wm, int wn, int lane,
-                                         f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
+// One slice: PA planes of A at st, PB planes of B at stb
+template <int TILE, int PA, int PB, bool KSA, bool KSB, typename TE>
+__device__ __forceinline__ void multiply_slice(const TE* st, const TE* stb, int wm, int wn, int lane,
+                                               f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
   constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
   constexpr int PLANE = TILE * BK;
-  constexpr int PA = LA::PIECES, PB = LB::PIECES;
-  typedef typename LA::TE TE;
-  static_assert(std::is_same<TE, typename LB::TE>::value, "operands of one type");
-  constexpr int DEPTH = LA::DEPTH;
-  static_assert(DEPTH == LB::DEPTH && (DEPTH == 2 || DEPTH == 4), "the loops below step through 2 or 4 slots");
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int pb = 0; pb < PB; ++pb) {
+      typename Half<TE>::v8 bv[MTN];
+#pragma unroll
+      for (int nt = 0; nt < MTN; ++nt)
+        bv[nt] = fragment<TILE, KSB>(stb + pb * PLANE, (wn * MTN + nt) * 32, ks, lane);
+#pragma unroll
+      for (int pa = 0; pa < PA; ++pa)
+#pragma unroll
+        for (int mt = 0; mt < MTM; ++mt) {
+          const auto av = fragment<TILE, KSA>(st + pa * PLANE, (wm * MTM + mt) * 32, ks, lane);
+#pragma unroll
+          for (int nt = 0; nt < MTN; ++nt) acc[mt][nt] = Half<TE>::mfma(av, bv[nt], acc[mt][nt]);
+        }
+    }
+}
+
+template <int MTM, int MTN>
+__device__ __forceinline__ void clear(f32x16 (&acc)[MTM][MTN]) {
 #pragma unroll
   for (int mt = 0; mt < MTM; ++mt)
 #pragma unroll
     for (int nt = 0; nt < MTN; ++nt)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[mt][nt][r] = 0.f;
+}
+
+// slices: of k; whole: the leading ones that need no checks
+template <int TILE, typename LA, typename LB>
+__device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t whole, typename LA::TE* stage0,
+                                         typename LA::TE* stage1, int wm, int wn, int lane,
+                                         f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
+  constexpr int PLANE = TILE * BK;
+  constexpr int PA = LA::PIECES, PB = LB::PIECES;
+  typedef typename LA::TE TE;
+  static_assert(std::is_same<TE, typename LB::TE>::value, "operands of one type");
+  constexpr int DEPTH = LA::DEPTH;
+  static_assert(DEPTH == LB::DEPTH && (DEPTH == 2 || DEPTH == 4), "the loops below step through 2 or 4 slots");
+  clear(acc);
   if (slices <= 0) return;
 
   auto compute = [&](const TE* st) {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int pb = 0; pb < PB; ++pb) {
-        typename Half<TE>::v8 bv[MTN];
-#pragma unroll
-        for (int nt = 0; nt < MTN; ++nt)
-          bv[nt] = fragment<TILE, LB::KS>(st + (PA + pb) * PLANE, (wn * MTN + nt) * 32, ks, lane);
-#pragma unroll
-        for (int pa = 0; pa < PA; ++pa)
-#pragma unroll
-          for (int mt = 0; mt < MTM; ++mt) {
-            const auto av = fragment<TILE, LA::KS>(st + pa * PLANE, (wm * MTM + mt) * 32, ks, lane);
-#pragma unroll
-            for (int nt = 0; nt < MTN; ++nt) acc[mt][nt] = Half<TE>::mfma(av, bv[nt], acc[mt][nt]);
-          }
-      }
+    multiply_slice<TILE, PA, PB, LA::KS, LB::KS>(st, st + PA * PLANE, wm, wn, lane, acc);
   };
   auto load = [&](auto slot_c, auto check_c, int64_t kt) {
     la.template load<decltype(slot_c)::value, decltype(check_c)::value>(kt);
@@ -521,6 +542,112 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
 }
 
 // ------------------------------------------------------------------------------------------------
+// Two microscaled operands, k contiguous in both, B a multiple of 128
+// ------------------------------------------------------------------------------------------------
+//
+// A 32-k slice of a row is 16 or 32 bytes: loaded slice by slice, every load touches one cache line per
+// row and uses a quarter of it or less, and the lines per load bound the product (1.69 ms for the
+// statistics of 384 E4M3 tiles of 1024).  So 128 k of a row are loaded at once, 16 consecutive k by each
+// of 8 neighbouring lanes, and slice s of the four takes k = 4 s .. 4 s + 3 of every lane's 16: any
+// 32 k make a slice as long as both operands agree.  A thread holds such pieces of four rows, TILE / 4
+// apart, in two buffers.
+template <int F, int TILE>
+struct CodesWide {
+  typedef unsigned raw16 __attribute__((ext_vector_type(F == DASH_MX_E4M3 ? 4 : 2)));
+  const uint8_t *c, *s;
+  unsigned off_c, off_s;
+  int64_t row_c, row_s;  // TILE / 4 rows
+  raw16 r[2][4];
+  unsigned sc[2][4];
+  int row, lane8;
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int tid) {
+    row = tid >> 3;
+    lane8 = tid & 7;
+    const int64_t at = b * q.rows + r0;
+    c = q.codes + at * q.row_bytes;
+    s = q.scales + at * q.row_groups;
+    row_c = q.row_bytes * (TILE / 4);
+    row_s = q.row_groups * (TILE / 4);
+    off_c = (unsigned)row * (unsigned)q.row_bytes + lane8 * (2 * Elem<F>::BITS);
+    off_s = (unsigned)row * (unsigned)q.row_groups + lane8 / 2;
+  }
+  template <int BUF>
+  __device__ __forceinline__ void load(int quad) {  // slices 4 quad .. 4 quad + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[BUF][i] = *(const raw16*)(c + i * row_c + quad * (16 * Elem<F>::BITS) + off_c);
+      sc[BUF][i] = (s + i * row_s + quad * 4)[off_s];
+    }
+  }
+  template <int BUF, int SLICE>
+  __device__ __forceinline__ void store(__bf16* plane) const {
+    typedef __bf16 v4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = scale_of(sc[BUF][i]);
+      bf16x2 lo, hi;
+      if constexpr (F == DASH_MX_E4M3) {
+        lo = Pair<__bf16>::e4m3<0>(r[BUF][i][SLICE], f);
+        hi = Pair<__bf16>::e4m3<1>(r[BUF][i][SLICE], f);
+      } else {
+        lo = Pair<__bf16>::e2m1<2 * (SLICE & 1)>(r[BUF][i][SLICE / 2], f);
+        hi = Pair<__bf16>::e2m1<2 * (SLICE & 1) + 1>(r[BUF][i][SLICE / 2], f);
+      }
+      *(v4*)&plane[kc_at(row + i * (TILE / 4), lane8 >> 1) + 4 * (lane8 & 1)] = v4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  }
+};
+
+// quads: of 128 k.  same: both operands are the same rows (B's planes are then A's)
+template <int F, int TILE>
+__device__ __forceinline__ void multiply_wide(CodesWide<F, TILE>& la, CodesWide<F, TILE>& lb, bool same, int quads,
+                                              __bf16* stage0, __bf16* stage1, int wm, int wn, int lane,
+                                              f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
+  constexpr int PLANE = TILE * BK;
+  const int second = same ? 0 : PLANE;
+  clear(acc);
+  auto load = [&](auto buf_c, int quad) {
+    la.template load<decltype(buf_c)::value>(quad);
+    if (!same) lb.template load<decltype(buf_c)::value>(quad);
+  };
+  auto store = [&](auto buf_c, auto slice_c) {
+    constexpr int slice = decltype(slice_c)::value;
+    __bf16* st = slice & 1 ? stage1 : stage0;
+    la.template store<decltype(buf_c)::value, slice>(st);
+    if (!same) lb.template store<decltype(buf_c)::value, slice>(st + PLANE);
+  };
+  auto compute = [&](const __bf16* st) {
+    multiply_slice<TILE, 1, 1, false, false>(st, st + second, wm, wn, lane, acc);
+  };
+  // four slices: each is multiplied while the next moves to the other stage; once the last one has left
+  // its buffer, the buffer is loaded with the quad after the next
+  auto four = [&](auto buf_c, int quad) {
+    constexpr int buf = decltype(buf_c)::value;
+    store(buf_c, IC<1>{});
+    compute(stage0);
+    __syncthreads();
+    store(buf_c, IC<2>{});
+    compute(stage1);
+    __syncthreads();
+    store(buf_c, IC<3>{});
+    compute(stage0);
+    __syncthreads();
+    if (quad + 2 < quads) load(buf_c, quad + 2);
+    if (quad + 1 < quads) store(IC<1 - buf>{}, IC<0>{});
+    compute(stage1);
+    __syncthreads();
+  };
+  load(IC<0>{}, 0);
+  if (quads > 1) load(IC<1>{}, 1);
+  store(IC<0>{}, IC<0>{});
+  __syncthreads();
+  for (int quad = 0; quad < quads; quad += 2) {
+    four(IC<0>{}, quad);
+    if (quad + 1 < quads) four(IC<1>{}, quad + 1);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
 // Statistics: L <- beta L + (1 - beta) Q Q^T from row codes, R from column codes (two problems)
 // ------------------------------------------------------------------------------------------------
 
@@ -528,6 +655,81 @@ struct StatsArgs {
   GemmArgs g;
   MxCodes q[2];
 };
+
+// A <- beta A + (1 - beta) acc for the tile and its mirror, the arithmetic and the accesses of epilogue_split
+// (32 x 32 sub-blocks; on a diagonal tile those below the diagonal store nothing and those on it their
+// upper part and its mirror).  The old values of AHEAD sub-blocks are under way at a time: loaded one
+// sub-block at a time, their latency was a third of the launch.
+template <int TILE>
+__device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoord& tc, float* A,
+                                               const f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN], int wm, int wn,
+                                               int lane, float* mlds) {
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, SUBS = MTM * MTN, AHEAD = SUBS < 4 ? SUBS : 4;
+  constexpr int NT = 2;  // non-temporal: A passes through once (B = 1024 1551 -> 1514 us, 256 600 -> 620 us)
+  const int B = a.g.B;
+  const float al = a.g.epi.alpha, be = a.g.epi.delta;
+  const uint64_t at = (uint64_t)(A + tc.b * (int64_t)B * B);  // (the same in every lane: say so)
+  const uint64_t base = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32) |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, B * B * 4, BUFFER_RSRC_WORD3);
+  const int li = lane & 31, h = lane >> 5;
+  const int swm = __builtin_amdgcn_readfirstlane(wm), swn = __builtin_amdgcn_readfirstlane(wn);
+  const int vlane = (4 * h * B + li) * 4;                   // lane part: row 4 h, column li
+  const int vmir = ((lane >> 3) * B + 4 * (lane & 7)) * 4;  // mirror: row lane / 8, column 4 (lane % 8)
+  const bool diag = tc.ti == tc.tj;
+  auto row_of = [&](int t) { return (swm * MTM + t / MTN) * 32; };
+  auto col_of = [&](int t) { return (swn * MTN + t % MTN) * 32; };
+  float old[AHEAD][16];
+  auto load = [&](int t, float (&ev)[16]) {
+    if (diag && row_of(t) > col_of(t)) return;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int i = tc.ti * TILE + row_of(t) + 8 * (r >> 2) + (r & 3);
+      ev[r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                            rs, vlane, (i * B + tc.tj * TILE + col_of(t)) * 4, NT));
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < AHEAD; ++t) load(t, old[t]);
+#pragma unroll
+  for (int t = 0; t < SUBS; ++t) {
+    const int ib = row_of(t), jb = col_of(t);
+    if (!(diag && ib > jb)) {
+      const int row0 = tc.ti * TILE + ib, col0 = tc.tj * TILE + jb;
+      const bool masked = row0 == col0;
+      float v[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] = al * acc[t / MTN][t % MTN][r] + be * old[t % AHEAD][r];
+        if (!masked || 8 * (r >> 2) + (r & 3) + 4 * h <= li)
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v[r]), rs, vlane,
+                                                ((row0 + 8 * (r >> 2) + (r & 3)) * B + col0) * 4, NT);
+      }
+      // the transposed sub-block through the wave's own LDS
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(f32x4*)&mlds[li * MLDS_PITCH + 8 * q + 4 * h] = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int rr = 8 * q + (lane >> 3), cc = 4 * (lane & 7);
+        const f32x4 x = *(const f32x4*)&mlds[rr * MLDS_PITCH + cc];
+        const int so = ((col0 + 8 * q) * B + row0) * 4;
+        if (!masked) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rs, vmir, so, NT);
+        } else {  // only the mirror's strict lower part
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = x[e];  // (a bit cast of a vector's element itself takes element 0)
+            if (cc + e < rr)
+              __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, y), rs, vmir + 4 * e, so, NT);
+          }
+        }
+      }
+    }
+    if (t + AHEAD < SUBS) load(t + AHEAD, old[t % AHEAD]);
+  }
+}
 
 template <int F, int TILE>
 __global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
@@ -539,18 +741,23 @@ __global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
   const MxCodes q = tc.prob ? a.q[1] : a.q[0];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
-  CodesK<F, TILE, 4, __bf16> la, lb;
-  la.init(q, tc.b, tc.ti * TILE, tid);
-  lb.init(q, tc.b, tc.tj * TILE, tid);
   f32x16 acc[MTM][MTN];
-  const int slices = a.g.B / BK;
-  multiply<TILE>(la, lb, slices, slices, stage0, stage1, wm, wn, lane, acc);
+  if constexpr (TILE >= 128) {
+    CodesWide<F, TILE> la, lb;
+    la.init(q, tc.b, tc.ti * TILE, tid);
+    lb.init(q, tc.b, tc.tj * TILE, tid);
+    multiply_wide(la, lb, tc.ti == tc.tj, a.g.B / 128, stage0, stage1, wm, wn, lane, acc);
+  } else {
+    CodesK<F, TILE, 4, __bf16> la, lb;
+    la.init(q, tc.b, tc.ti * TILE, tid);
+    lb.init(q, tc.b, tc.tj * TILE, tid);
+    multiply<TILE>(la, lb, a.g.B / BK, a.g.B / BK, stage0, stage1, wm, wn, lane, acc);
+  }
   constexpr int WAVES = TILE / 32;
   constexpr int PER = WAVES / 2 * MLDS_FLOATS * 4;
   static_assert(PER <= STAGE * 2, "LDS for the mirror");
   float* mlds = (float*)(wave < WAVES / 2 ? (void*)stage0 : (void*)stage1) + (wave % (WAVES / 2)) * MLDS_FLOATS;
-  epilogue_split<MTM, MTN, MTM * 32, MTN * 32, true, false, TILE, false, false>(
-      a.g, tc, tc.prob ? a.g.p1 : a.g.p0, acc, wm, wn, lane, nullptr, mlds);
+  stats_epilogue<TILE>(a, tc, (float*)(tc.prob ? a.g.p1.D : a.g.p0.D), acc, wm, wn, lane, mlds);
 }
 
 template <int F, int TILE>
@@ -780,7 +987,7 @@ __global__ __launch_bounds__(2 * TILE) void mx_grad_kernel(GradArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
   f32x16 acc[MTM][MTN];
-  constexpr int D = sizeof(T) == 4 ? 2 : 4;
+  constexpr int D = sizeof(T) == 4 && TILE == 256 ? 2 : 4;
   FloatCol<T, TILE, D> la;
   CodesCol<F, TILE, D> lb;
   la.init(a.dy, 0, i0, k0, k1, tid);
@@ -831,8 +1038,19 @@ __global__ __launch_bounds__(256) void mx_grad_join_kernel(GradArgs a, int64_t p
   if (e >= a.tr * a.B * quads) return;
   const int64_t i = e / quads, j = 4 * (e - i * quads);
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (i < a.out && j < a.in)
-    for (int s = 0; s < a.splits; ++s) v += *(const f32x4*)(a.part + (s * pm + i) * pn + j);
+  if (i < a.out && j < a.in) {
+    const float* p = a.part + i * pn + j;
+    const int64_t step = pm * pn;
+    int s = 0;
+    for (; s + 8 <= a.splits; s += 8) {  // (eight loads under way at a time)
+      f32x4 x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = *(const f32x4*)(p + (s + q) * step);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v += x[q];
+    }
+    for (; s < a.splits; ++s) v += *(const f32x4*)(p + s * step);
+  }
   const int64_t t = i / a.B * a.tc + j / a.B;
   f32x4* at = (f32x4*)(a.G + (t * a.B + i % a.B) * a.B + j % a.B);
   *at = a.accumulate ? *at + v : v;
@@ -910,9 +1128,7 @@ hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG,
   a.g.epi.alpha = 1.f - beta;
   a.g.epi.delta = beta;
   a.g.p0.D = A;
-  a.g.p0.E = A;
   a.g.p1.D = A + NG * (int64_t)B * B;
-  a.g.p1.E = A + NG * (int64_t)B * B;
   a.q[0] = rows;
   a.q[1] = cols;
   if (fmt == DASH_MX_E4M3)
