@@ -1791,7 +1791,7 @@ dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, das
   if (!bytes) return DASH_ERR_INVALID_ARG;
   const dash_status st = grad_shape_check(T, out, in, out, type);
   if (st != DASH_OK) return st;
-  *bytes = mx_grad_workspace_bytes(T, out, in);
+  *bytes = mx_grad_workspace_bytes(T, out, in, type);
   return DASH_OK;
 }
 
@@ -1805,7 +1805,7 @@ dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, cons
     return DASH_ERR_INVALID_ARG;
   if (!G_stack || !aligned(G_stack, 16) || G_stack == dY || G_stack == codes) return DASH_ERR_INVALID_ARG;
   if (!valid_B(B)) return DASH_ERR_SHAPE;
-  const size_t need = mx_grad_workspace_bytes(T, out, in);
+  const size_t need = mx_grad_workspace_bytes(T, out, in, type);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return DASH_ERR_WORKSPACE;
   TRY(launch_mx_grad(dY, type, ldy, mx_codes(codes, scales, T, in, fmt), fmt, T, out, in, B, accumulate != 0, G_stack, ws,
                      as_stream(stream)));

@@ -340,9 +340,13 @@ struct MxApply {
   int parts;
 };
 inline int mx_apply_parts(int B) { return B >= 1024 ? 16 : B >= 512 ? 4 : 1; }
-inline int64_t mx_apply_waves(int B) { return (int64_t)(B / 64) * (B / 64) * 2; }
+inline int64_t mx_apply_waves(int B) {
+  const int64_t a = B / 64, b = (B + 127) / 128, c = (B + 255) / 256;  // tiles of 64, 128, 256
+  const int64_t w = 2 * a * a > 4 * b * b ? 2 * a * a : 4 * b * b;
+  return w > 8 * c * c ? w : 8 * c * c;
+}
 hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream);
-size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in);
+size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in, dash_prec type);
 hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
                           int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream);
 

@@ -18,6 +18,7 @@
 // slow axis as [k][TILE], read back k-major by the transposing LDS load.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "gemm_common.hpp"
@@ -161,7 +162,7 @@ __device__ __forceinline__ typename Half<TE>::v8 fragment(const TE* plane, int b
 // ------------------------------------------------------------------------------------------------
 
 // D: slices in the register ring, 4, but 2 beside fp32 in 256 x 256 tiles (where four spill)
-// Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows of the tile all exist.
+// Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows beyond `rows` are zero.
 // shift: added to the scale bytes (a power of two on every element).
 template <int F, int TILE, int D, typename E>
 struct CodesK {
@@ -175,8 +176,10 @@ struct CodesK {
   raw8 r[DEPTH][2];
   unsigned sc[DEPTH];
   int row, half, shift;
+  bool in;
   __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int tid, int shift_ = 0) {
     row = tid >> 1;
+    in = r0 + row < q.rows;
     half = tid & 1;
     shift = shift_;
     const int64_t at = b * q.rows + r0;
@@ -187,6 +190,11 @@ struct CodesK {
   }
   template <int SLOT, bool CHECK>
   __device__ __forceinline__ void load(int64_t kt) {
+    if (CHECK) {
+      r[SLOT][0] = r[SLOT][1] = raw8{};
+      sc[SLOT] = 0;
+      if (!in) return;
+    }
     const raw8* p = (const raw8*)(c + kt * (BK * Elem<F>::BITS / 8) + off_c);
     r[SLOT][0] = p[0];
     r[SLOT][1] = p[1];
@@ -256,7 +264,8 @@ struct CodesCol {
 };
 
 // fp32, k contiguous, two binary16 pieces of 2^e x: thread t holds 8 k of rows t / 4 and t / 4 + TILE / 2
-// (four lanes read a row's 128 bytes).  Rows of the tile all exist.  m1 is -1 (see split2).
+// (four lanes read a row's 128 bytes).  Rows from x.cols on (the matrices are square) are zero.  m1 is
+// -1 (see split2).
 template <int TILE, int D>
 struct FloatK {
   typedef _Float16 TE;
@@ -268,12 +277,15 @@ struct FloatK {
   f32x4 r[D][2][2];
   int64_t half;  // elements from one of the thread's rows to the other
   int row, chunk, e;
+  bool in[2];
   float m1;
   __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t r0, int tid, int e_, float m1_) {
     row = tid >> 2;
     chunk = tid & 3;
     e = e_;
     m1 = m1_;
+    in[0] = r0 + row < x.cols;
+    in[1] = r0 + row + TILE / 2 < x.cols;
     p = (const float*)x.p + b * x.stride + r0 * x.ld;
     half = x.ld * (TILE / 2);
     off = (unsigned)row * (unsigned)x.ld + 8 * chunk;
@@ -282,6 +294,10 @@ struct FloatK {
   __device__ __forceinline__ void load(int64_t kt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (CHECK) {
+        r[SLOT][i][0] = r[SLOT][i][1] = f32x4{};
+        if (!in[i]) continue;
+      }
       const float* q = p + kt * BK + i * half + off;
       r[SLOT][i][0] = *(const f32x4*)q;
       r[SLOT][i][1] = *(const f32x4*)(q + 4);
@@ -301,7 +317,7 @@ struct FloatK {
 };
 
 // fp32, k the slow axis, two binary16 pieces of 2^e x: thread t holds 8 columns of two of the slice's
-// rows, 16 apart.  The tile's columns and the slices' rows all exist.
+// rows, 16 apart.  Columns beyond the matrix are zero; the slices' rows all exist.
 template <int TILE, int D>
 struct FloatCol16 {
   typedef _Float16 TE;
@@ -313,6 +329,7 @@ struct FloatCol16 {
   f32x4 r[D][2][2];
   int64_t ld;
   int k, col, e;
+  bool in;
   float m1;
   __device__ __forceinline__ void init(const MxFloats& x, int64_t b, int64_t c0, int tid, int e_, float m1_) {
     col = 8 * (tid % (TILE / 8));
@@ -320,6 +337,7 @@ struct FloatCol16 {
     ld = x.ld;
     e = e_;
     m1 = m1_;
+    in = c0 + col < x.cols;
     p = (const float*)x.p + b * x.stride + c0;
     off = (unsigned)k * (unsigned)ld + col;
   }
@@ -327,6 +345,10 @@ struct FloatCol16 {
   __device__ __forceinline__ void load(int64_t kt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (CHECK) {
+        r[SLOT][i][0] = r[SLOT][i][1] = f32x4{};
+        if (!in) continue;
+      }
       const float* q = p + (kt * BK + 16 * i) * ld + off;
       r[SLOT][i][0] = *(const f32x4*)q;
       r[SLOT][i][1] = *(const f32x4*)(q + 4);
@@ -470,6 +492,19 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[MTM][MTN]) {
       for (int r = 0; r < 16; ++r) acc[mt][nt][r] = 0.f;
 }
 
+// Time of a launch by tile width, in us per k-slice: `lat` is what a slice takes in a compute unit with
+// one workgroup or few, `thr` each workgroup's share where a unit holds `cap` of them.  A launch is full
+// rounds of 256 cap workgroups and a last one.
+struct TileRate {
+  int tile;
+  double lat, thr;
+  int cap;
+};
+inline double slice_time(const TileRate& r, double workgroups) {
+  const double w = workgroups / 256, full = floor(w / r.cap), rest = w - full * r.cap;
+  return full * r.thr * r.cap + (rest > 0 ? (r.lat > r.thr * rest ? r.lat : r.thr * rest) : 0);
+}
+
 // slices: of k; whole: the leading ones that need no checks
 template <int TILE, typename LA, typename LB>
 __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t whole, typename LA::TE* stage0,
@@ -542,108 +577,115 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
 }
 
 // ------------------------------------------------------------------------------------------------
-// Two microscaled operands, k contiguous in both, B a multiple of 128
+// Two microscaled operands, k contiguous in both
 // ------------------------------------------------------------------------------------------------
 //
 // A 32-k slice of a row is 16 or 32 bytes: loaded slice by slice, every load touches one cache line per
-// row and uses a quarter of it or less, and the lines per load bound the product (1.69 ms for the
-// statistics of 384 E4M3 tiles of 1024).  So 128 k of a row are loaded at once, 16 consecutive k by each
-// of 8 neighbouring lanes, and slice s of the four takes k = 4 s .. 4 s + 3 of every lane's 16: any
-// 32 k make a slice as long as both operands agree.  A thread holds such pieces of four rows, TILE / 4
-// apart, in two buffers.
-template <int F, int TILE>
+// row and uses a quarter of it or less, and the lines per load bounded the product.  So 128 k of a row
+// are loaded at once, 16 consecutive k by each of 8 neighbouring lanes, and slice s of the four takes
+// k = 4 s .. 4 s + 3 of every lane's 16: any 32 k make a slice as long as both operands agree.  A thread
+// holds such pieces of four rows, TILE / 4 = 32 apart.  Rows and k beyond B (a multiple of 64) are zero.
+// EDGE: B is not a multiple of 128.
+template <int F, int TILE, bool EDGE>
 struct CodesWide {
+  static_assert(TILE == 128, "the passes of 32 rows lie inside or outside B as a whole");
   typedef unsigned raw16 __attribute__((ext_vector_type(F == DASH_MX_E4M3 ? 4 : 2)));
   const uint8_t *c, *s;
   unsigned off_c, off_s;
-  int64_t row_c, row_s;  // TILE / 4 rows
-  raw16 r[2][4];
-  unsigned sc[2][4];
-  int row, lane8;
-  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int64_t r0, int tid) {
+  int64_t row_c, row_s;  // 32 rows
+  raw16 r[4];
+  unsigned sc[4];
+  int row, lane8, B, rows;  // rows: of the tile that exist
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int r0, int B_, int tid) {
     row = tid >> 3;
     lane8 = tid & 7;
+    B = B_;
+    rows = B - r0;
     const int64_t at = b * q.rows + r0;
     c = q.codes + at * q.row_bytes;
     s = q.scales + at * q.row_groups;
-    row_c = q.row_bytes * (TILE / 4);
-    row_s = q.row_groups * (TILE / 4);
+    row_c = q.row_bytes * 32;
+    row_s = q.row_groups * 32;
     off_c = (unsigned)row * (unsigned)q.row_bytes + lane8 * (2 * Elem<F>::BITS);
     off_s = (unsigned)row * (unsigned)q.row_groups + lane8 / 2;
   }
-  template <int BUF>
-  __device__ __forceinline__ void load(int quad) {  // slices 4 quad .. 4 quad + 3
+  __device__ __forceinline__ void load(int quad) {  // k = 128 quad .. 128 quad + 127
+    auto piece = [&](int i) {
+      r[i] = *(const raw16*)(c + i * row_c + quad * (16 * Elem<F>::BITS) + off_c);
+      sc[i] = (s + i * row_s + quad * 4)[off_s];
+    };
+    if (!EDGE || (rows >= TILE && 128 * quad + 128 <= B)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r[BUF][i] = *(const raw16*)(c + i * row_c + quad * (16 * Elem<F>::BITS) + off_c);
-      sc[BUF][i] = (s + i * row_s + quad * 4)[off_s];
+      for (int i = 0; i < 4; ++i) piece(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[i] = raw16{};
+        sc[i] = 0;
+        if (32 * i < rows && 128 * quad + 16 * lane8 < B) piece(i);
+      }
     }
   }
-  template <int BUF, int SLICE>
+  template <int SLICE>
   __device__ __forceinline__ void store(__bf16* plane) const {
     typedef __bf16 v4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float f = scale_of(sc[BUF][i]);
+      const float f = scale_of(sc[i]);
       bf16x2 lo, hi;
       if constexpr (F == DASH_MX_E4M3) {
-        lo = Pair<__bf16>::e4m3<0>(r[BUF][i][SLICE], f);
-        hi = Pair<__bf16>::e4m3<1>(r[BUF][i][SLICE], f);
+        lo = Pair<__bf16>::e4m3<0>(r[i][SLICE], f);
+        hi = Pair<__bf16>::e4m3<1>(r[i][SLICE], f);
       } else {
-        lo = Pair<__bf16>::e2m1<2 * (SLICE & 1)>(r[BUF][i][SLICE / 2], f);
-        hi = Pair<__bf16>::e2m1<2 * (SLICE & 1) + 1>(r[BUF][i][SLICE / 2], f);
+        lo = Pair<__bf16>::e2m1<2 * (SLICE & 1)>(r[i][SLICE / 2], f);
+        hi = Pair<__bf16>::e2m1<2 * (SLICE & 1) + 1>(r[i][SLICE / 2], f);
       }
-      *(v4*)&plane[kc_at(row + i * (TILE / 4), lane8 >> 1) + 4 * (lane8 & 1)] = v4{lo[0], lo[1], hi[0], hi[1]};
+      *(v4*)&plane[kc_at(row + i * 32, lane8 >> 1) + 4 * (lane8 & 1)] = v4{lo[0], lo[1], hi[0], hi[1]};
     }
   }
 };
 
-// quads: of 128 k.  same: both operands are the same rows (B's planes are then A's)
-template <int F, int TILE>
-__device__ __forceinline__ void multiply_wide(CodesWide<F, TILE>& la, CodesWide<F, TILE>& lb, bool same, int quads,
+// quads: of 128 k.  same: both operands are the same rows (B's plane is then A's)
+template <int F, int TILE, bool EDGE>
+__device__ __forceinline__ void multiply_wide(CodesWide<F, TILE, EDGE>& la, CodesWide<F, TILE, EDGE>& lb, bool same, int quads,
                                               __bf16* stage0, __bf16* stage1, int wm, int wn, int lane,
                                               f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
   constexpr int PLANE = TILE * BK;
   const int second = same ? 0 : PLANE;
   clear(acc);
-  auto load = [&](auto buf_c, int quad) {
-    la.template load<decltype(buf_c)::value>(quad);
-    if (!same) lb.template load<decltype(buf_c)::value>(quad);
+  auto load = [&](int quad) {
+    la.load(quad);
+    if (!same) lb.load(quad);
   };
-  auto store = [&](auto buf_c, auto slice_c) {
+  auto store = [&](auto slice_c) {
     constexpr int slice = decltype(slice_c)::value;
     __bf16* st = slice & 1 ? stage1 : stage0;
-    la.template store<decltype(buf_c)::value, slice>(st);
-    if (!same) lb.template store<decltype(buf_c)::value, slice>(st + PLANE);
+    la.template store<slice>(st);
+    if (!same) lb.template store<slice>(st + PLANE);
   };
   auto compute = [&](const __bf16* st) {
     multiply_slice<TILE, 1, 1, false, false>(st, st + second, wm, wn, lane, acc);
   };
-  // four slices: each is multiplied while the next moves to the other stage; once the last one has left
-  // its buffer, the buffer is loaded with the quad after the next
-  auto four = [&](auto buf_c, int quad) {
-    constexpr int buf = decltype(buf_c)::value;
-    store(buf_c, IC<1>{});
-    compute(stage0);
-    __syncthreads();
-    store(buf_c, IC<2>{});
-    compute(stage1);
-    __syncthreads();
-    store(buf_c, IC<3>{});
-    compute(stage0);
-    __syncthreads();
-    if (quad + 2 < quads) load(buf_c, quad + 2);
-    if (quad + 1 < quads) store(IC<1 - buf>{}, IC<0>{});
-    compute(stage1);
-    __syncthreads();
-  };
-  load(IC<0>{}, 0);
-  if (quads > 1) load(IC<1>{}, 1);
-  store(IC<0>{}, IC<0>{});
+  load(0);
+  store(IC<0>{});
   __syncthreads();
-  for (int quad = 0; quad < quads; quad += 2) {
-    four(IC<0>{}, quad);
-    if (quad + 1 < quads) four(IC<1>{}, quad + 1);
+  // each slice is multiplied while the next moves to the other stage; the next quad is loaded as soon as
+  // the last slice has left the registers (a second set of them would cost the third workgroup per
+  // compute unit, which hides more: 1.51 -> 1.35 ms for 384 tiles of 1024)
+  for (int quad = 0; quad < quads; ++quad) {
+    store(IC<1>{});
+    compute(stage0);
+    __syncthreads();
+    store(IC<2>{});
+    compute(stage1);
+    __syncthreads();
+    store(IC<3>{});
+    if (quad + 1 < quads) load(quad + 1);
+    compute(stage0);
+    __syncthreads();
+    if (quad + 1 < quads) store(IC<0>{});
+    compute(stage1);
+    __syncthreads();
   }
 }
 
@@ -660,7 +702,7 @@ struct StatsArgs {
 // (32 x 32 sub-blocks; on a diagonal tile those below the diagonal store nothing and those on it their
 // upper part and its mirror).  The old values of AHEAD sub-blocks are under way at a time: loaded one
 // sub-block at a time, their latency was a third of the launch.
-template <int TILE>
+template <int TILE, bool EDGE>
 __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoord& tc, float* A,
                                                const f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN], int wm, int wn,
                                                int lane, float* mlds) {
@@ -680,9 +722,14 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
   const bool diag = tc.ti == tc.tj;
   auto row_of = [&](int t) { return (swm * MTM + t / MTN) * 32; };
   auto col_of = [&](int t) { return (swn * MTN + t % MTN) * 32; };
+  // (sub-blocks lie inside or outside B as a whole)
+  auto kept = [&](int t) {
+    return !(diag && row_of(t) > col_of(t)) &&
+           (!EDGE || (tc.ti * TILE + row_of(t) < B && tc.tj * TILE + col_of(t) < B));
+  };
   float old[AHEAD][16];
   auto load = [&](int t, float (&ev)[16]) {
-    if (diag && row_of(t) > col_of(t)) return;
+    if (!kept(t)) return;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int i = tc.ti * TILE + row_of(t) + 8 * (r >> 2) + (r & 3);
@@ -695,7 +742,7 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
 #pragma unroll
   for (int t = 0; t < SUBS; ++t) {
     const int ib = row_of(t), jb = col_of(t);
-    if (!(diag && ib > jb)) {
+    if (kept(t)) {
       const int row0 = tc.ti * TILE + ib, col0 = tc.tj * TILE + jb;
       const bool masked = row0 == col0;
       float v[16];
@@ -731,9 +778,13 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
   }
 }
 
-template <int F, int TILE>
-__global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
-  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN;
+// 128-wide tiles, three workgroups to a compute unit: one's loads and stores of A run under the others'
+// products.  (256-wide ones, one to a unit, took 1.50 ms where these take 1.37 at B = 1024, 394 us against
+// 327 at 200 x 768, and 3 % less at B = 4096; with B an odd multiple of 64, 64-wide tiles took 6 % more at
+// B = 192 and 86 % more at 1600.)  B = 64: one 64-wide tile.
+template <int F, int TILE, bool EDGE>
+__global__ __launch_bounds__(2 * TILE, 3) void mx_stats_kernel(StatsArgs a) {
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, WAVES = TILE / 32;
   constexpr int STAGE = 2 * TILE * BK;
   __shared__ __attribute__((aligned(16))) __bf16 stage0[STAGE];
   __shared__ __attribute__((aligned(16))) __bf16 stage1[STAGE];
@@ -742,32 +793,38 @@ __global__ __launch_bounds__(2 * TILE) void mx_stats_kernel(StatsArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
   f32x16 acc[MTM][MTN];
-  if constexpr (TILE >= 128) {
-    CodesWide<F, TILE> la, lb;
-    la.init(q, tc.b, tc.ti * TILE, tid);
-    lb.init(q, tc.b, tc.tj * TILE, tid);
-    multiply_wide(la, lb, tc.ti == tc.tj, a.g.B / 128, stage0, stage1, wm, wn, lane, acc);
+  if constexpr (TILE == 128) {
+    CodesWide<F, TILE, EDGE> la, lb;
+    la.init(q, tc.b, tc.ti * TILE, a.g.B, tid);
+    lb.init(q, tc.b, tc.tj * TILE, a.g.B, tid);
+    multiply_wide(la, lb, tc.ti == tc.tj, (a.g.B + 127) / 128, stage0, stage1, wm, wn, lane, acc);
   } else {
     CodesK<F, TILE, 4, __bf16> la, lb;
     la.init(q, tc.b, tc.ti * TILE, tid);
     lb.init(q, tc.b, tc.tj * TILE, tid);
     multiply<TILE>(la, lb, a.g.B / BK, a.g.B / BK, stage0, stage1, wm, wn, lane, acc);
   }
-  constexpr int WAVES = TILE / 32;
   constexpr int PER = WAVES / 2 * MLDS_FLOATS * 4;
   static_assert(PER <= STAGE * 2, "LDS for the mirror");
   float* mlds = (float*)(wave < WAVES / 2 ? (void*)stage0 : (void*)stage1) + (wave % (WAVES / 2)) * MLDS_FLOATS;
-  stats_epilogue<TILE>(a, tc, (float*)(tc.prob ? a.g.p1.D : a.g.p0.D), acc, wm, wn, lane, mlds);
+  stats_epilogue<TILE, EDGE>(a, tc, (float*)(tc.prob ? a.g.p1.D : a.g.p0.D), acc, wm, wn, lane, mlds);
 }
 
-template <int F, int TILE>
+template <int F, int TILE, bool EDGE>
 hipError_t launch_stats(StatsArgs& a, hipStream_t stream) {
-  a.g.tdim = a.g.B / TILE;
+  a.g.tdim = (a.g.B + TILE - 1) / TILE;
   a.g.tiles = a.g.tdim * (a.g.tdim + 1) / 2;
   const int64_t grid = 2 * a.g.N * a.g.tiles;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_stats_kernel<F, TILE>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  hipLaunchKernelGGL((mx_stats_kernel<F, TILE, EDGE>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   return hipGetLastError();
+}
+
+template <int F>
+hipError_t stats_of_width(StatsArgs& a, hipStream_t stream) {
+  return a.g.B == 64         ? launch_stats<F, 64, false>(a, stream)
+         : a.g.B % 128 == 0 ? launch_stats<F, 128, false>(a, stream)
+                            : launch_stats<F, 128, true>(a, stream);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -822,17 +879,18 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
   const int shift = __builtin_amdgcn_readfirstlane(127 + Elem<F>::TOP - (int)top);
   float m1 = -1.f;
   asm("" : "+s"(m1));  // (no instruction: hides the constant -1 from the optimiser)
+  const int whole = (tc.ti + 1) * TILE <= B && (tc.tj + 1) * TILE <= B ? B / BK : 0;
   f32x16 acc[MTM][MTN];
   CodesK<F, TILE, 2, _Float16> lq;
   lq.init(a.q, tc.b, (LEFT ? tc.ti : tc.tj) * TILE, tid, shift);
   if constexpr (LEFT) {
     FloatCol16<TILE, 2> lx;
     lx.init(a.x, tc.b, tc.tj * TILE, tid, ex, m1);
-    multiply<TILE>(lq, lx, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
+    multiply<TILE>(lq, lx, B / BK, whole, stage0, stage1, wm, wn, lane, acc);
   } else {
     FloatK<TILE, 2> lx;
     lx.init(a.x, tc.b, tc.ti * TILE, tid, ex, m1);
-    multiply<TILE>(lx, lq, B / BK, B / BK, stage0, stage1, wm, wn, lane, acc);
+    multiply<TILE>(lx, lq, B / BK, whole, stage0, stage1, wm, wn, lane, acc);
   }
   const int64_t off = tc.b * (int64_t)B * B;
   const float* x = (const float*)a.x.p + off;
@@ -844,6 +902,8 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
   for (int mt = 0; mt < MTM; ++mt)
 #pragma unroll
     for (int nt = 0; nt < MTN; ++nt) {
+      // (sub-blocks lie inside or outside B as a whole)
+      if (tc.ti * TILE + (wm * MTM + mt) * 32 >= B || tc.tj * TILE + (wn * MTN + nt) * 32 >= B) continue;
       const int i0 = tc.ti * TILE + (wm * MTM + mt) * 32 + 4 * (lane >> 5);
       const int j = tc.tj * TILE + (wn * MTN + nt) * 32 + (lane & 31);
 #pragma unroll
@@ -921,8 +981,7 @@ __global__ __launch_bounds__(256) void mx_bounds_kernel(const float* G, const ui
 
 template <int F, int TILE>
 hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream) {
-  const int B = p.B;
-  a.g.tdim = B / TILE;
+  a.g.tdim = (p.B + TILE - 1) / TILE;
   a.g.tiles = a.g.tdim * a.g.tdim;
   const int64_t grid = p.N * a.g.tiles;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
@@ -946,11 +1005,29 @@ hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream)
   return hipGetLastError();
 }
 
+// The tile with the least predicted time.  Measured with tiles of 64 / 128 / 256 (both products and the
+// bounds, us): 2 x 128 24 / 26 / 33, 30 x 704 200 / 187 / 219, 16 x 1024 295 / 195 / 175, 100 x 1088
+// 2137 / 1739 / 1622, 384 x 1024 6831 / 5028 / 4275; the rates are fitted to 22 such shapes, B 64 .. 3136.
+constexpr TileRate APPLY_RATES[3] = {{64, 0.9, 0.28, 4}, {128, 1.0, 0.8, 2}, {256, 1.85, 2.5, 1}};
+int apply_tile(int64_t N, int B) {
+  int best = 64;
+  double least = INFINITY;
+  for (const TileRate& r : APPLY_RATES) {
+    const double side = (B + r.tile - 1) / r.tile, t = slice_time(r, (double)N * side * side);
+    if (t < least) {
+      least = t;
+      best = r.tile;
+    }
+  }
+  return best;
+}
+
 template <int F>
 hipError_t launch_apply_fmt(ApplyArgs& a, const MxApply& p, hipStream_t stream) {
-  return p.B % 256 == 0   ? launch_apply_tile<F, 256>(a, p, stream)
-         : p.B % 128 == 0 ? launch_apply_tile<F, 128>(a, p, stream)
-                          : launch_apply_tile<F, 64>(a, p, stream);
+  const int tile = apply_tile(p.N, p.B);
+  return tile == 256   ? launch_apply_tile<F, 256>(a, p, stream)
+         : tile == 128 ? launch_apply_tile<F, 128>(a, p, stream)
+                       : launch_apply_tile<F, 64>(a, p, stream);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1056,28 +1133,44 @@ __global__ __launch_bounds__(256) void mx_grad_join_kernel(GradArgs a, int64_t p
   *at = a.accumulate ? *at + v : v;
 }
 
-constexpr int GRAD_CHUNK_MIN = 512;  // tokens a split has at least
-
-// The launch's shape: kernel tile, tiles, and splits of the token axis so that few tiles still fill
-// the 256 compute units.
+// The launch's shape: kernel tile, tiles, and splits of the token axis so that few tiles still fill the
+// chip, joined by a second launch: the pair with the least predicted time.  Measured with the best
+// split for tiles of 64 / 128 / 256 (us, E4M3, bfloat16 dY unless said): 1 x 256 x 192 (tokens x out x in)
+// 9 / 10 / 13, 2048 x 1024 x 1024 21 / 25 / 34, 65536 x 256 x 256 32 / 27 / 50, 4096 x 2048 x 2048 68 / 50 /
+// 59, 50000 x 520 x 264 fp32 138 / 103 / 139, 4096 x 2048 x 8192 294 / 166 / 129.  The rates (each further
+// piece of dY adds half of one; 1.4 slices to start and end; a join 3.2 us and 1.2 per 10^6 partial sums)
+// are fitted to 20 such shapes, over which the choice is 2 % from the best on average.
+constexpr TileRate GRAD_RATES[3] = {{64, 0.19, 0.17, 4}, {128, 0.47, 0.365, 2}, {256, 1.15, 1.15, 1}};
 struct GradShape {
-  int tile;
-  int64_t gm, gn, chunk;
-  int splits;
+  int tile = 64;
+  int64_t gm = 1, gn = 1, chunk = 0;
+  int splits = 1;
 };
-GradShape grad_shape(int64_t T, int64_t out, int64_t in) {
-  GradShape g;
-  g.tile = out <= 64 || in <= 64 ? 64 : out <= 128 || in <= 128 ? 128 : 256;
-  g.gm = (out + g.tile - 1) / g.tile;
-  g.gn = (in + g.tile - 1) / g.tile;
-  const int64_t tiles = g.gm * g.gn;
-  int64_t s = 256 / tiles;
-  if (s > T / GRAD_CHUNK_MIN) s = T / GRAD_CHUNK_MIN;
-  if (s < 1) s = 1;
-  g.chunk = ((T + s - 1) / s + BK - 1) / BK * BK;
-  g.splits = g.chunk ? (int)((T + g.chunk - 1) / g.chunk) : 1;
-  if (g.splits < 1) g.splits = 1;
-  return g;
+GradShape grad_shape(int64_t T, int64_t out, int64_t in, dash_prec type) {
+  const int pieces = type == DASH_FP32 ? 3 : type == DASH_FP16 ? 2 : 1;
+  GradShape best;
+  double least = INFINITY;
+  for (const TileRate& r : GRAD_RATES) {
+    const int64_t gm = (out + r.tile - 1) / r.tile, gn = (in + r.tile - 1) / r.tile, tiles = gm * gn;
+    for (int round = 0; round <= 2 * r.cap; ++round) {  // one split, or splits that fill `round` per unit
+      int64_t s = round == 0 ? 1 : 256 * round / tiles;
+      if (s > (T + 2 * BK - 1) / (2 * BK)) s = (T + 2 * BK - 1) / (2 * BK);
+      if (s < 1 || (round > 0 && s == 1)) s = 1;
+      const int64_t chunk = ((T + s - 1) / s + BK - 1) / BK * BK;
+      const int splits = chunk ? (int)((T + chunk - 1) / chunk) : 1;
+      double t = (chunk / BK + 1.4) * (1 + 0.5 * (pieces - 1)) * slice_time(r, (double)tiles * splits);
+      if (splits > 1) t += 3.2 + 1.2e-6 * (double)tiles * r.tile * r.tile * splits;
+      if (t < least) {
+        least = t;
+        best.tile = r.tile;
+        best.gm = gm;
+        best.gn = gn;
+        best.chunk = chunk;
+        best.splits = splits;
+      }
+    }
+  }
+  return best;
 }
 
 template <typename T, int F, int TILE>
@@ -1131,13 +1224,7 @@ hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG,
   a.g.p1.D = A + NG * (int64_t)B * B;
   a.q[0] = rows;
   a.q[1] = cols;
-  if (fmt == DASH_MX_E4M3)
-    return B % 256 == 0   ? launch_stats<DASH_MX_E4M3, 256>(a, stream)
-           : B % 128 == 0 ? launch_stats<DASH_MX_E4M3, 128>(a, stream)
-                          : launch_stats<DASH_MX_E4M3, 64>(a, stream);
-  return B % 256 == 0   ? launch_stats<DASH_MX_E2M1, 256>(a, stream)
-         : B % 128 == 0 ? launch_stats<DASH_MX_E2M1, 128>(a, stream)
-                        : launch_stats<DASH_MX_E2M1, 64>(a, stream);
+  return fmt == DASH_MX_E4M3 ? stats_of_width<DASH_MX_E4M3>(a, stream) : stats_of_width<DASH_MX_E2M1>(a, stream);
 }
 
 hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream) {
@@ -1160,14 +1247,14 @@ hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream
                              : launch_apply_fmt<DASH_MX_E2M1>(a, p, stream);
 }
 
-size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in) {
-  const GradShape g = grad_shape(T, out, in);
+size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in, dash_prec type) {
+  const GradShape g = grad_shape(T, out, in, type);
   return g.splits > 1 ? (size_t)g.splits * g.gm * g.gn * g.tile * g.tile * sizeof(float) : 0;
 }
 
 hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
                           int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream) {
-  const GradShape g = grad_shape(T, out, in);
+  const GradShape g = grad_shape(T, out, in, type);
   GradArgs a;
   a.dy.p = dY;
   a.dy.ld = ldy;

@@ -303,6 +303,41 @@ def test_apply(B, fmt, diag):
     assert np.array_equal(f64(Gd), G.astype(np.float64))
 
 
+@pytest.mark.parametrize("diag", [False, True])
+@pytest.mark.parametrize("fmt", FMTS, ids=IDS)
+@pytest.mark.parametrize("N,B", [(60, 256), (50, 320), (40, 448), (130, 512)])
+def test_apply_wide(N, B, fmt, diag):
+    """Stacks that take 128- and 256-wide kernel tiles, whole and at the edges."""
+    rng = di.rng(110 + B)
+    ql, sl, L = random_codes(rng, N, B, B, fmt)
+    qr, sr, R = random_codes(rng, N, B, B, fmt)
+    L, R = torch.from_numpy(L).to(DEV), torch.from_numpy(R).to(DEV)
+    gen = torch.Generator(device=DEV).manual_seed(B)
+    dl = dr = None
+    if diag:
+        dl, dr = (50 * torch.randn((N, B), generator=gen, device=DEV) for _ in range(2))
+        L, R = L + torch.diag_embed(dl.double()), R + torch.diag_embed(dr.double())
+    G = torch.randn((N, B, B), generator=gen, device=DEV)
+    G *= torch.logspace(-6, 6, N, device=DEV)[:, None, None]  # blocks of their own magnitudes
+    got = torch.full((N, B, B), float("nan"), device=DEV)
+    ws = dash.workspace(dash.DASH_OP_APPLY, N, B, device=DEV)
+    ws.fill_(0xFF)
+    dash.dash_apply_mx(ql, sl, qr, sr, G, N, B, fmt, got, XL_diag=dl, XR_diag=dr, ws=ws)
+    Rt = R.transpose(1, 2).contiguous()
+    want = torch.bmm(torch.bmm(L, G.double()), Rt)
+    mag = torch.bmm(torch.bmm(L.abs(), G.double().abs()), Rt.abs())
+    err = (got.double() - want).abs()
+    assert bool((err <= 2 * (B + 4) * U * mag).all())
+    rel = err.flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    assert float(rel.max()) <= 2e-6
+    # each block as a call of its own makes it, to the products' rounding
+    one = torch.empty((1, B, B), device=DEV)
+    i = N // 2
+    dash.dash_apply_mx(ql[i:i + 1], sl[i:i + 1], qr[i:i + 1], sr[i:i + 1], G[i:i + 1], 1, B, fmt, one,
+                       XL_diag=dl[i:i + 1] if diag else None, XR_diag=dr[i:i + 1] if diag else None, ws=ws)
+    assert bool(((one[0].double() - want[i]).abs() <= 2 * (B + 4) * U * mag[i]).all())
+
+
 def test_apply_identity_and_ranges():
     """Unit roots give G back bit for bit; blocks of very different magnitudes do not touch each other."""
     fmt, N, B = dash.DASH_MX_E2M1, 4, 192
@@ -376,6 +411,35 @@ def test_grad_stack(dtype, fmt):
             assert np.linalg.norm(err) <= 3e-6 * np.linalg.norm(mag)
             again = grad(dY, q, s, fmt, T, out, inp, B, guard=64)
             assert torch.equal(again[:-64], G[:-64])  # equal calls, equal bits
+
+
+# tokens, out, in, B that take 128- and 256-wide kernel tiles, whole and at the edges, split and not
+WIDE_GRADS = [(200, 2070, 7000, 512), (90, 3000, 2100, 256), (7000, 600, 520, 192), (4100, 2050, 2048, 1024)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,out,inp,B", WIDE_GRADS)
+def test_grad_stack_wide(T, out, inp, B, dtype):
+    fmt = dash.DASH_MX_E4M3 if T % 200 else dash.DASH_MX_E2M1
+    rng = di.rng(135 + T)
+    q, s, X = random_codes(rng, 1, T, inp, fmt)
+    Xd = torch.from_numpy(X[0]).to(DEV)
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    for pad in (0, 6):
+        buf = torch.full((T, out + pad), float("nan"), dtype=dtype, device=DEV)
+        buf[:, :out] = torch.randn((T, out), generator=gen, device=DEV).to(dtype)
+        dY = buf[:, :out]
+        d = dY.double()
+        W, mag = (d.T.contiguous() @ Xd).cpu().numpy(), (d.abs().T.contiguous() @ Xd.abs()).cpu().numpy()
+        tol = ref.tiles((3 * T + 260) * U * mag, B)
+        G = grad(dY, q, s, fmt, T, out, inp, B)
+        err = np.abs(f64(G).reshape(-1, B, B) - ref.tiles(W, B))
+        assert np.all(err <= tol), (pad, np.nanmax(err - tol))
+        assert np.linalg.norm(err) <= 3e-6 * np.linalg.norm(mag)
+        assert torch.equal(grad(dY, q, s, fmt, T, out, inp, B), G)
+        old = torch.randn(G.shape, generator=gen, device=DEV)
+        more = grad(dY, q, s, fmt, T, out, inp, B, True, old.clone())
+        assert torch.equal(more, old + G)  # one fp32 addition of the same sum
 
 
 @pytest.mark.parametrize("T", [0, 1, 40, 3000])
