@@ -37,18 +37,20 @@ class DashVec(ctypes.Structure):
 
 _lib = None
 _torch_module = None
+_Tensor = ()  # torch.Tensor
 _dtypes = {}  # element types by the names that _Args.ptr takes
 _precs = {}  # dash_prec by element type
 
 
 def _torch():
     """torch, imported at the first call that needs it."""
-    global _torch_module
+    global _torch_module, _Tensor
     if _torch_module is None:
         import torch
 
         _dtypes.update(float32=torch.float32, int32=torch.int32, uint8=torch.uint8)
         _precs.update({torch.float32: DASH_FP32, torch.float16: DASH_FP16, torch.bfloat16: DASH_BF16})
+        _Tensor = torch.Tensor
         _torch_module = torch
     return _torch_module
 
@@ -127,30 +129,32 @@ class _Args:
     expose ``data_ptr()`` pass through unchecked as raw device addresses (the ABI tests use them).
     """
 
+    __slots__ = ("call", "device", "index")
+
     def __init__(self, call: str):
         self.call = call
         self.device = None
         self.index = -1  # of that device
+        if _torch_module is None:
+            _torch()
 
     def _tensor(self, t, name):
-        if not isinstance(t, _torch().Tensor):
+        if not isinstance(t, _Tensor):
             return False
-        if not t.is_cuda:
-            raise ValueError("%s: %s must be a GPU tensor, got one on %s" % (self.call, name, t.device))
         index = t.get_device()
-        if self.device is None:
+        if index != self.index or index < 0:  # the call's first tensor, or one elsewhere
+            if index < 0:
+                raise ValueError("%s: %s must be a GPU tensor, got one on %s" % (self.call, name, t.device))
+            if self.device is not None:
+                raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, t.device,
+                                                                                      self.device))
             self.device, self.index = t.device, index
-        elif index != self.index:
-            raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, t.device,
-                                                                                  self.device))
         return True
 
     def ptr(self, t, name, dtype="float32", numel=0):
         """Pointer of tensor argument `name` of `dtype` ('float32', 'int32', 'uint8' or None for any) holding
         at least `numel` elements."""
-        if t is None:
-            return None
-        if isinstance(t, int):
+        if t is None or t.__class__ is int:
             return t
         if self._tensor(t, name):
             want = _dtypes.get(dtype)
@@ -161,6 +165,8 @@ class _Args:
             if t.numel() < numel:
                 raise ValueError("%s: %s holds %d elements, the call touches %d" % (self.call, name, t.numel(),
                                                                                      int(numel)))
+        elif isinstance(t, int):
+            return t
         return t.data_ptr()
 
     def ws(self, t):
@@ -191,10 +197,10 @@ class _Args:
         """(pointer, dash_prec type, row pitch) of N row-major matrices of rows x cols, one after the
         other: a tensor [rows, cols] (N = 1) or [N, rows, cols] of float32, float16 or bfloat16 with unit
         column stride and matrices rows * pitch apart, or a raw pointer with type and ld given."""
-        if t is None or isinstance(t, int) or not self._tensor(t, name):
+        if t is None or t.__class__ is int or not self._tensor(t, name):
             p = t if t is None or isinstance(t, int) else t.data_ptr()
             return p, DASH_FP32 if type is None else type, cols if ld is None else ld
-        have = _prec_of(t.dtype)
+        have = _precs.get(t.dtype)
         if have is None or type not in (None, have):
             raise ValueError("%s: %s must be float32, float16 or bfloat16, got %s" % (self.call, name, t.dtype))
         shape = tuple(t.shape)
@@ -231,19 +237,20 @@ class _Args:
     def stream(self, stream):
         if stream is not None:
             return stream if isinstance(stream, int) else stream.cuda_stream
-        torch = _torch()
         if self.device is None:
-            return torch.cuda.current_stream(None).cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.index)  # (current_stream(device) without its object)
+            return _torch_module.cuda.current_stream(None).cuda_stream
+        return _torch_module._C._cuda_getCurrentRawStream(self.index)  # (current_stream(device) without its object)
 
     def run(self, fn, *args):
         """fn(*args) with the tensors' device current, as a launch on that device's default stream needs;
         raises DashError on a non-OK status."""
-        if self.device is None or self.index == _torch().cuda.current_device():
-            _check(self.call, fn(*args))
+        if self.device is None or self.index == _torch_module._C._cuda_getDevice():
+            status = fn(*args)
         else:
-            with _torch().cuda.device(self.device):
-                _check(self.call, fn(*args))
+            with _torch_module.cuda.device(self.device):
+                status = fn(*args)
+        if status != DASH_OK:
+            raise DashError(self.call, status)
 
 
 def _check(name, status):

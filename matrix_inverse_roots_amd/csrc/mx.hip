@@ -163,21 +163,38 @@ __device__ __forceinline__ void take_diag(f32x8& x, int64_t r, int64_t c0, float
     }
 }
 
-// Rows only: 8 elements per thread, 4 threads per group; rows of all matrices are one list.
+// Rows a thread takes 8 elements of, their loads under way together: 2 from 16-bit sources (65536 x 4096
+// bfloat16 to E4M3 166 -> 151 us) and 1 from fp32 (192 x 1024 x 1024 160 us; 2: 163); 2 on the way back
+// (151 -> 134 and 187 -> 155 us; 4: 138 and 188).
+template <typename T>
+constexpr int ROWS_IN = sizeof(T) == 2 ? 2 : 1;
+constexpr int ROWS_BACK = 2;
+
+// Rows only: 4 threads per group; rows of all matrices are one list.
 template <typename T, int F>
 __global__ __launch_bounds__(256) void mx_rows_kernel(QuantArgs a) {
   const int64_t rb = blockIdx.x / a.col_wgs, cb = blockIdx.x - rb * a.col_wgs;
   const int per = 256 / a.lanes;
-  const int64_t r = rb * per + threadIdx.x / a.lanes;
+  const int64_t first = rb * per * ROWS_IN<T> + threadIdx.x / a.lanes;
   const int64_t c0 = 8 * (cb * a.lanes + threadIdx.x % a.lanes);
   const int64_t groups = (a.cols + GROUP - 1) / GROUP;
-  if (r >= a.N * a.rows || c0 >= groups * GROUP) return;  // (whole groups of 4 lanes leave together)
-  f32x8 x = load8((const T*)a.src + r * a.ld, c0, a.cols, a.vec);
-  if (a.diag) take_diag(x, r % a.rows, c0, a.diag + r);
-  unsigned byte;
-  const typename Codes<F>::type c = encode_group<F>(x, byte);
-  *(typename Codes<F>::type*)(a.codes + (r * groups * GROUP + c0) * Codes<F>::BITS / 8) = c;
-  if (threadIdx.x % 4 == 0) a.scales[r * groups + c0 / GROUP] = (uint8_t)byte;
+  if (c0 >= groups * GROUP) return;  // (the 4 lanes of a group leave together)
+  f32x8 x[ROWS_IN<T>];
+#pragma unroll
+  for (int i = 0; i < ROWS_IN<T>; ++i) {
+    const int64_t r = first + i * per;
+    x[i] = r < a.N * a.rows ? load8((const T*)a.src + r * a.ld, c0, a.cols, a.vec) : f32x8{};
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS_IN<T>; ++i) {
+    const int64_t r = first + i * per;
+    if (r >= a.N * a.rows) return;  // (as above)
+    if (a.diag) take_diag(x[i], r % a.rows, c0, a.diag + r);
+    unsigned byte;
+    const typename Codes<F>::type c = encode_group<F>(x[i], byte);
+    *(typename Codes<F>::type*)(a.codes + (r * groups * GROUP + c0) * Codes<F>::BITS / 8) = c;
+    if (threadIdx.x % 4 == 0) a.scales[r * groups + c0 / GROUP] = (uint8_t)byte;
+  }
 }
 
 // Columns, and rows from the same read: a 128 x 128 tile goes through LDS.  Four neighbouring lanes
@@ -258,23 +275,37 @@ template <typename T, int F>
 __global__ __launch_bounds__(256) void mx_values_kernel(DequantArgs a) {
   const int64_t rb = blockIdx.x / a.col_wgs, cb = blockIdx.x - rb * a.col_wgs;
   const int per = 256 / a.lanes;
-  const int64_t r = rb * per + threadIdx.x / a.lanes;
+  const int64_t first = rb * per * ROWS_BACK + threadIdx.x / a.lanes;
   const int64_t c0 = 8 * (cb * a.lanes + threadIdx.x % a.lanes);
-  if (r >= a.N * a.rows || c0 >= a.cols) return;
+  if (c0 >= a.cols) return;
   const int64_t groups = (a.cols + GROUP - 1) / GROUP;
-  const typename Codes<F>::type c =
-      *(const typename Codes<F>::type*)(a.codes + (r * groups * GROUP + c0) * Codes<F>::BITS / 8);
-  const int byte = a.scales[r * groups + c0 / GROUP];
-  f32x8 x = Codes<F>::decode(c);
+  typename Codes<F>::type c[ROWS_BACK];
+  int byte[ROWS_BACK];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) x[q] = byte == 255 ? __builtin_nanf("") : ldexpf(x[q], byte - 127);
-  if (a.diag) {
-    const int64_t d = r % a.rows;
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (c0 + q == d) x[q] += a.diag[r];
+  for (int i = 0; i < ROWS_BACK; ++i) {
+    const int64_t r = first + i * per;
+    c[i] = {};
+    byte[i] = 0;
+    if (r < a.N * a.rows) {
+      c[i] = *(const typename Codes<F>::type*)(a.codes + (r * groups * GROUP + c0) * Codes<F>::BITS / 8);
+      byte[i] = a.scales[r * groups + c0 / GROUP];
+    }
   }
-  store8((T*)a.dst + r * a.ld, c0, a.cols, a.vec, x);
+#pragma unroll
+  for (int i = 0; i < ROWS_BACK; ++i) {
+    const int64_t r = first + i * per;
+    if (r >= a.N * a.rows) return;
+    f32x8 x = Codes<F>::decode(c[i]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = byte[i] == 255 ? __builtin_nanf("") : ldexpf(x[q], byte[i] - 127);
+    if (a.diag) {
+      const int64_t d = r % a.rows;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c0 + q == d) x[q] += a.diag[r];
+    }
+    store8((T*)a.dst + r * a.ld, c0, a.cols, a.vec, x);
+  }
 }
 
 // Threads of a 256-thread workgroup on one row of `chunks` 8-element pieces, and workgroups along it
@@ -296,7 +327,7 @@ hipError_t quantize(QuantArgs& a, hipStream_t stream) {
     return hipGetLastError();
   }
   row_split((a.cols + GROUP - 1) / GROUP * 4, a.lanes, a.col_wgs);
-  const int per = 256 / a.lanes;
+  const int per = 256 / a.lanes * ROWS_IN<T>;
   const int64_t grid = (a.N * a.rows + per - 1) / per * a.col_wgs;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((mx_rows_kernel<T, F>), dim3((unsigned)grid), dim3(256), 0, stream, a);
@@ -306,7 +337,7 @@ hipError_t quantize(QuantArgs& a, hipStream_t stream) {
 template <typename T, int F>
 hipError_t dequantize(DequantArgs& a, hipStream_t stream) {
   row_split((a.cols + 7) / 8, a.lanes, a.col_wgs);
-  const int per = 256 / a.lanes;
+  const int per = 256 / a.lanes * ROWS_BACK;
   const int64_t grid = (a.N * a.rows + per - 1) / per * a.col_wgs;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((mx_values_kernel<T, F>), dim3((unsigned)grid), dim3(256), 0, stream, a);

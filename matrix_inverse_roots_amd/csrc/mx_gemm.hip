@@ -8,7 +8,7 @@
 // subnormals), scale included, and the 32x32x16 bfloat16 MFMA forms products of two elements exactly
 // and sums them in fp32.  (The scaled 8-bit MFMA, at twice the rate, drops bits below the largest
 // addend of its 64: sums of 4096 positive E4M3 products came out 7e-5 low, a hundred times fp32's own
-// error, so it is not used.)  A floating operand beside a microscaled one is cut into bfloat16
+// error, so it is not used; the 4-bit one sums exactly within a group and the E2M1 statistics use it.)  A floating operand beside a microscaled one is cut into bfloat16
 // pieces that add up to it exactly (one for bfloat16, two for binary16, three for fp32), and each
 // piece multiplies the one microscaled piece: exact products again, accumulated in fp32.
 //
@@ -539,6 +539,21 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
     load(slot_c, IC<0>{}, kt + DEPTH);
     store(IC<(slot + 1) % DEPTH>{});
     compute(slot & 1 ? stage1 : stage0);
+    // two binary16 pieces: asks for the split's arithmetic between the products instead of before them
+    // (384 x 1024 4.19 -> 4.03 ms; the gradient tiles came out level or 1 % slower)
+    if constexpr (TILE == 256 && std::is_same<TE, _Float16>::value) {
+      constexpr int PRODUCTS = 2 * PA * PB * Shape<TILE>::MTM * Shape<TILE>::MTN;
+      constexpr int VALU = 0x2, MFMA = 0x8, VMEM_READ = 0x20, DS_READ = 0x100, DS_WRITE = 0x200;
+      __builtin_amdgcn_sched_group_barrier(VMEM_READ, 16, 0);
+      __builtin_amdgcn_sched_group_barrier(DS_READ, 6, 0);
+#pragma unroll
+      for (int m = 0; m < PRODUCTS; ++m) {
+        __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(VALU, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(DS_READ, 1, 0);
+        if (m >= PRODUCTS / 4) __builtin_amdgcn_sched_group_barrier(DS_WRITE, 1, 0);
+      }
+    }
     __syncthreads();
   };
   auto last_step = [&](auto slot_c, int64_t kt) {
@@ -577,23 +592,22 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
 }
 
 // ------------------------------------------------------------------------------------------------
-// Two microscaled operands, k contiguous in both
+// Two E4M3 operands, k contiguous in both
 // ------------------------------------------------------------------------------------------------
 //
-// A 32-k slice of a row is 16 or 32 bytes: loaded slice by slice, every load touches one cache line per
-// row and uses a quarter of it or less, and the lines per load bounded the product.  So 128 k of a row
+// A 32-k slice of a row is 32 bytes: loaded slice by slice, every load touches one cache line per row
+// and uses a quarter of it, and the lines per load bounded the product.  So 128 k of a row
 // are loaded at once, 16 consecutive k by each of 8 neighbouring lanes, and slice s of the four takes
 // k = 4 s .. 4 s + 3 of every lane's 16: any 32 k make a slice as long as both operands agree.  A thread
 // holds such pieces of four rows, TILE / 4 = 32 apart.  Rows and k beyond B (a multiple of 64) are zero.
 // EDGE: B is not a multiple of 128.
-template <int F, int TILE, bool EDGE>
+template <int TILE, bool EDGE>
 struct CodesWide {
   static_assert(TILE == 128, "the passes of 32 rows lie inside or outside B as a whole");
-  typedef unsigned raw16 __attribute__((ext_vector_type(F == DASH_MX_E4M3 ? 4 : 2)));
   const uint8_t *c, *s;
   unsigned off_c, off_s;
   int64_t row_c, row_s;  // 32 rows
-  raw16 r[4];
+  u32x4 r[4];
   unsigned sc[4];
   int row, lane8, B, rows;  // rows: of the tile that exist
   __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int r0, int B_, int tid) {
@@ -606,12 +620,12 @@ struct CodesWide {
     s = q.scales + at * q.row_groups;
     row_c = q.row_bytes * 32;
     row_s = q.row_groups * 32;
-    off_c = (unsigned)row * (unsigned)q.row_bytes + lane8 * (2 * Elem<F>::BITS);
+    off_c = (unsigned)row * (unsigned)q.row_bytes + 16 * lane8;
     off_s = (unsigned)row * (unsigned)q.row_groups + lane8 / 2;
   }
   __device__ __forceinline__ void load(int quad) {  // k = 128 quad .. 128 quad + 127
     auto piece = [&](int i) {
-      r[i] = *(const raw16*)(c + i * row_c + quad * (16 * Elem<F>::BITS) + off_c);
+      r[i] = *(const u32x4*)(c + i * row_c + quad * 128 + off_c);
       sc[i] = (s + i * row_s + quad * 4)[off_s];
     };
     if (!EDGE || (rows >= TILE && 128 * quad + 128 <= B)) {
@@ -620,7 +634,7 @@ struct CodesWide {
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        r[i] = raw16{};
+        r[i] = u32x4{};
         sc[i] = 0;
         if (32 * i < rows && 128 * quad + 16 * lane8 < B) piece(i);
       }
@@ -632,22 +646,15 @@ struct CodesWide {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float f = scale_of(sc[i]);
-      bf16x2 lo, hi;
-      if constexpr (F == DASH_MX_E4M3) {
-        lo = Pair<__bf16>::e4m3<0>(r[i][SLICE], f);
-        hi = Pair<__bf16>::e4m3<1>(r[i][SLICE], f);
-      } else {
-        lo = Pair<__bf16>::e2m1<2 * (SLICE & 1)>(r[i][SLICE / 2], f);
-        hi = Pair<__bf16>::e2m1<2 * (SLICE & 1) + 1>(r[i][SLICE / 2], f);
-      }
+      const bf16x2 lo = Pair<__bf16>::e4m3<0>(r[i][SLICE], f), hi = Pair<__bf16>::e4m3<1>(r[i][SLICE], f);
       *(v4*)&plane[kc_at(row + i * 32, lane8 >> 1) + 4 * (lane8 & 1)] = v4{lo[0], lo[1], hi[0], hi[1]};
     }
   }
 };
 
 // quads: of 128 k.  same: both operands are the same rows (B's plane is then A's)
-template <int F, int TILE, bool EDGE>
-__device__ __forceinline__ void multiply_wide(CodesWide<F, TILE, EDGE>& la, CodesWide<F, TILE, EDGE>& lb, bool same, int quads,
+template <int TILE, bool EDGE>
+__device__ __forceinline__ void multiply_wide(CodesWide<TILE, EDGE>& la, CodesWide<TILE, EDGE>& lb, bool same, int quads,
                                               __bf16* stage0, __bf16* stage1, int wm, int wn, int lane,
                                               f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN]) {
   constexpr int PLANE = TILE * BK;
@@ -778,10 +785,10 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
   }
 }
 
-// 128-wide tiles, three workgroups to a compute unit: one's loads and stores of A run under the others'
+// E4M3: 128-wide tiles, three workgroups to a compute unit: one's loads and stores of A run under the others'
 // products.  (256-wide ones, one to a unit, took 1.50 ms where these take 1.37 at B = 1024, 394 us against
 // 327 at 200 x 768, and 3 % less at B = 4096; with B an odd multiple of 64, 64-wide tiles took 6 % more at
-// B = 192 and 86 % more at 1600.)  B = 64: one 64-wide tile.
+// B = 192 and 86 % more at 1600.)  Both formats at B = 64: one 64-wide tile.
 template <int F, int TILE, bool EDGE>
 __global__ __launch_bounds__(2 * TILE, 3) void mx_stats_kernel(StatsArgs a) {
   constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, WAVES = TILE / 32;
@@ -794,7 +801,7 @@ __global__ __launch_bounds__(2 * TILE, 3) void mx_stats_kernel(StatsArgs a) {
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
   f32x16 acc[MTM][MTN];
   if constexpr (TILE == 128) {
-    CodesWide<F, TILE, EDGE> la, lb;
+    CodesWide<TILE, EDGE> la, lb;
     la.init(q, tc.b, tc.ti * TILE, a.g.B, tid);
     lb.init(q, tc.b, tc.tj * TILE, a.g.B, tid);
     multiply_wide(la, lb, tc.ti == tc.tj, (a.g.B + 127) / 128, stage0, stage1, wm, wn, lane, acc);
@@ -810,21 +817,143 @@ __global__ __launch_bounds__(2 * TILE, 3) void mx_stats_kernel(StatsArgs a) {
   stats_epilogue<TILE, EDGE>(a, tc, (float*)(tc.prob ? a.g.p1.D : a.g.p0.D), acc, wm, wn, lane, mlds);
 }
 
-template <int F, int TILE, bool EDGE>
-hipError_t launch_stats(StatsArgs& a, hipStream_t stream) {
+// ------------------------------------------------------------------------------------------------
+// E2M1 statistics: the scaled 4-bit MFMA
+// ------------------------------------------------------------------------------------------------
+//
+// The 32x32x64 scaled MFMA multiplies E2M1 codes as they are stored, at four times the bfloat16 rate: lane l
+// takes row l % 32, k = 32 (l / 32) .. + 31, one scale group, and its scale byte.  Products of two E2M1
+// values are whole quarters up to 36, so its sum of a group is exact; the sums across groups are fp32's
+// (against 64 bits as near as the bfloat16 kernel's).  Stages hold codes, 128 k of a row in its 64
+// bytes, laid out like 32 bfloat16 k; a thread loads one group of a row and its scale.  Three workgroups
+// of 128-wide tiles to a compute unit (four, in 128 registers, took 1.24 ms where these take 1.06 at
+// B = 1024).  Against the bfloat16 kernel on the same codes: B = 1024 1450 -> 1062 us (4.96 TB/s), 2048 1140
+// -> 717, 4096 915 -> 574, 256 593 -> 588; at B = 64 49 -> 53, so that stays with the bfloat16 one.
+template <bool EDGE>
+struct Codes4 {
+  static constexpr int TILE = 128;
+  const uint8_t *c, *s;
+  unsigned off_c, off_s;
+  int64_t row_c, row_s;  // TILE / 2 rows
+  u32x4 r[2];
+  unsigned sc[2];
+  int row, group, B, rows;
+  __device__ __forceinline__ void init(const MxCodes& q, int64_t b, int r0, int B_, int tid) {
+    row = tid >> 2;
+    group = tid & 3;
+    B = B_;
+    rows = B - r0;
+    const int64_t at = b * q.rows + r0;
+    c = q.codes + at * q.row_bytes;
+    s = q.scales + at * q.row_groups;
+    row_c = q.row_bytes * (TILE / 2);
+    row_s = q.row_groups * (TILE / 2);
+    off_c = (unsigned)row * (unsigned)q.row_bytes + 16 * group;
+    off_s = (unsigned)row * (unsigned)q.row_groups + group;
+  }
+  __device__ __forceinline__ void load(int slice) {  // k = 128 slice .. 128 slice + 127
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (EDGE) {
+        r[i] = u32x4{};
+        sc[i] = 0;
+        if (row + i * (TILE / 2) >= rows || 128 * slice + 32 * group >= B) continue;
+      }
+      r[i] = *(const u32x4*)(c + i * row_c + slice * 64 + off_c);
+      sc[i] = (s + i * row_s + slice * 4)[off_s];
+    }
+  }
+  __device__ __forceinline__ void store(__bf16* plane, uint8_t* scales) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *(u32x4*)&plane[kc_at(row + i * (TILE / 2), group)] = r[i];
+      scales[4 * (row + i * (TILE / 2)) + group] = (uint8_t)sc[i];
+    }
+  }
+};
+
+template <bool EDGE>
+__global__ __launch_bounds__(256, 3) void mx_stats4_kernel(StatsArgs a) {
+  constexpr int TILE = 128;
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, WAVES = TILE / 32;
+  constexpr int PLANE = TILE * BK, STAGE = 2 * PLANE;
+  typedef int v8i __attribute__((ext_vector_type(8)));
+  __shared__ __attribute__((aligned(16))) __bf16 stage[2][STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t scale[2][2][4 * TILE];
+  const TileCoord tc = decode_tile(a.g, true);
+  const MxCodes q = tc.prob ? a.q[1] : a.q[0];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
+  const bool same = tc.ti == tc.tj;
+  const int sb = same ? 0 : 1;  // B's plane
+  Codes4<EDGE> la, lb;
+  la.init(q, tc.b, tc.ti * TILE, a.g.B, tid);
+  lb.init(q, tc.b, tc.tj * TILE, a.g.B, tid);
+  f32x16 acc[MTM][MTN];
+  clear(acc);
+  auto load = [&](int slice) {
+    la.load(slice);
+    if (!same) lb.load(slice);
+  };
+  auto store = [&](int to) {
+    la.store(stage[to], scale[to][0]);
+    if (!same) lb.store(stage[to] + PLANE, scale[to][1]);
+  };
+  auto operand = [&](const __bf16* plane, int base, int ks) {
+    const u32x4 x = *(const u32x4*)&plane[kc_at(base + (lane & 31), 2 * ks + (lane >> 5))];
+    return v8i{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+  };
+  // the row's four scale bytes, moved so that byte 2 ks is the lane's
+  auto scales = [&](const uint8_t* s, int base) {
+    return (int)(*(const unsigned*)&s[4 * (base + (lane & 31))] >> (8 * (lane >> 5)));
+  };
+  auto compute = [&](int from) {
+    const __bf16 *pa = stage[from], *pb = stage[from] + sb * PLANE;
+    int xa[MTM], xb[MTN];
+#pragma unroll
+    for (int mt = 0; mt < MTM; ++mt) xa[mt] = scales(scale[from][0], (wm * MTM + mt) * 32);
+#pragma unroll
+    for (int nt = 0; nt < MTN; ++nt) xb[nt] = scales(scale[from][sb], (wn * MTN + nt) * 32);
+    constexpr int FP4 = 4;
+#pragma unroll
+    for (int mt = 0; mt < MTM; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < MTN; ++nt)
+        acc[mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            operand(pa, (wm * MTM + mt) * 32, 0), operand(pb, (wn * MTN + nt) * 32, 0), acc[mt][nt], FP4, FP4, 0, xa[mt],
+            0, xb[nt]);
+#pragma unroll
+    for (int mt = 0; mt < MTM; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < MTN; ++nt)
+        acc[mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            operand(pa, (wm * MTM + mt) * 32, 1), operand(pb, (wn * MTN + nt) * 32, 1), acc[mt][nt], FP4, FP4, 2, xa[mt],
+            2, xb[nt]);
+  };
+  const int slices = (a.g.B + 127) / 128;
+  load(0);
+  store(0);
+  if (slices > 1) load(1);
+  __syncthreads();
+  for (int k = 0; k < slices; ++k) {
+    if (k + 1 < slices) store((k + 1) & 1);
+    if (k + 2 < slices) load(k + 2);
+    compute(k & 1);
+    __syncthreads();
+  }
+  static_assert(WAVES / 2 * MLDS_FLOATS * 4 <= STAGE * 2, "LDS for the mirror");
+  float* mlds = (float*)stage[wave < WAVES / 2 ? 0 : 1] + (wave % (WAVES / 2)) * MLDS_FLOATS;
+  stats_epilogue<TILE, EDGE>(a, tc, (float*)(tc.prob ? a.g.p1.D : a.g.p0.D), acc, wm, wn, lane, mlds);
+}
+
+template <int TILE, typename K>
+hipError_t launch_stats(K kernel, StatsArgs& a, hipStream_t stream) {
   a.g.tdim = (a.g.B + TILE - 1) / TILE;
   a.g.tiles = a.g.tdim * (a.g.tdim + 1) / 2;
   const int64_t grid = 2 * a.g.N * a.g.tiles;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_stats_kernel<F, TILE, EDGE>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   return hipGetLastError();
-}
-
-template <int F>
-hipError_t stats_of_width(StatsArgs& a, hipStream_t stream) {
-  return a.g.B == 64         ? launch_stats<F, 64, false>(a, stream)
-         : a.g.B % 128 == 0 ? launch_stats<F, 128, false>(a, stream)
-                            : launch_stats<F, 128, true>(a, stream);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1224,7 +1353,14 @@ hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG,
   a.g.p1.D = A + NG * (int64_t)B * B;
   a.q[0] = rows;
   a.q[1] = cols;
-  return fmt == DASH_MX_E4M3 ? stats_of_width<DASH_MX_E4M3>(a, stream) : stats_of_width<DASH_MX_E2M1>(a, stream);
+  const bool edge = B % 128 != 0;
+  if (fmt == DASH_MX_E4M3)
+    return B == 64 ? launch_stats<64>(mx_stats_kernel<DASH_MX_E4M3, 64, false>, a, stream)
+           : edge  ? launch_stats<128>(mx_stats_kernel<DASH_MX_E4M3, 128, true>, a, stream)
+                   : launch_stats<128>(mx_stats_kernel<DASH_MX_E4M3, 128, false>, a, stream);
+  return B == 64 ? launch_stats<64>(mx_stats_kernel<DASH_MX_E2M1, 64, false>, a, stream)
+         : edge  ? launch_stats<128>(mx_stats4_kernel<true>, a, stream)
+                 : launch_stats<128>(mx_stats4_kernel<false>, a, stream);
 }
 
 hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream) {
