@@ -22,6 +22,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int GROUP = MX_GROUP;
 
@@ -55,18 +56,12 @@ struct Codes<DASH_MX_E4M3> {
     }
     return c;
   }
-  static __device__ __forceinline__ f32x8 decode(type c) {
-    f32x8 v;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[w], 1.f, false);
-      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c[w], 1.f, true);
-      v[4 * w] = a[0];
-      v[4 * w + 1] = a[1];
-      v[4 * w + 2] = b[0];
-      v[4 * w + 3] = b[1];
-    }
-    return v;
+  // the values of 4 codes
+  typedef unsigned raw4;
+  static __device__ __forceinline__ f32x4 decode(raw4 c) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, 1.f, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, 1.f, true);
+    return f32x4{a[0], a[1], b[0], b[1]};
   }
 };
 template <>
@@ -84,12 +79,11 @@ struct Codes<DASH_MX_E2M1> {
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], 1.f, 3);
     return c;
   }
-  static __device__ __forceinline__ f32x8 decode(type c) {
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 1);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 2);
-    const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 3);
-    return f32x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+  typedef uint16_t raw4;
+  static __device__ __forceinline__ f32x4 decode(raw4 c) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((unsigned)c, 1.f, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((unsigned)c, 1.f, 1);
+    return f32x4{a[0], a[1], b[0], b[1]};
   }
 };
 
@@ -114,20 +108,6 @@ __device__ __forceinline__ f32x8 load8(const T* row, int64_t c0, int64_t cols, b
     for (int q = 0; q < 8; ++q) x[q] = c0 + q < cols ? (float)row[c0 + q] : 0.f;
   }
   return x;
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int64_t c0, int64_t cols, bool vec, const f32x8& x) {
-  if (vec && c0 + 8 <= cols) {
-    v8<T> r;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) r[q] = (T)x[q];
-    *(v8<T>*)(row + c0) = r;
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (c0 + q < cols) row[c0 + q] = (T)x[q];
-  }
 }
 
 struct QuantArgs {
@@ -163,9 +143,10 @@ __device__ __forceinline__ void take_diag(f32x8& x, int64_t r, int64_t c0, float
     }
 }
 
-// Rows a thread takes 8 elements of, their loads under way together: 2 from 16-bit sources (65536 x 4096
-// bfloat16 to E4M3 166 -> 151 us) and 1 from fp32 (192 x 1024 x 1024 160 us; 2: 163); 2 on the way back
-// (151 -> 134 and 187 -> 155 us; 4: 138 and 188).
+// Rows a thread takes a piece of, their loads under way together: 2 from 16-bit sources (65536 x 4096
+// bfloat16 to E4M3 166 -> 151 us) and 1 from fp32 (192 x 1024 x 1024 to E2M1 160 us; 2: 163); on the way
+// back 2 (65536 x 4096 to bfloat16 with 1 / 2 / 4 154 / 130 / 139 us, 192 x 1024 x 1024 E4M3 to fp32
+// 219 / 162 / 170).
 template <typename T>
 constexpr int ROWS_IN = sizeof(T) == 2 ? 2 : 1;
 constexpr int ROWS_BACK = 2;
@@ -269,25 +250,32 @@ struct DequantArgs {
   int64_t col_wgs;
 };
 
-// The values: element times 2^e in fp32 (two exact steps where 2^e alone leaves the normal range), the
-// diagonal's own value in its place, rounded to the output type once.
+// The values: element times 2^e in fp32 (ldexp is exact down to fp32's subnormals), the diagonal's own
+// value in its place, rounded to the output type once.  A thread makes 16 bytes of output per row, so
+// that a wave's store is one run of whole lines.
 template <typename T, int F>
 __global__ __launch_bounds__(256) void mx_values_kernel(DequantArgs a) {
+  constexpr int EACH = 16 / sizeof(T), QUADS = EACH / 4;
+  typedef typename Codes<F>::raw4 raw4;
+  typedef T out_t __attribute__((ext_vector_type(EACH)));
+  struct alignas(sizeof(raw4) * QUADS) Raw {
+    raw4 q[QUADS];
+  };
   const int64_t rb = blockIdx.x / a.col_wgs, cb = blockIdx.x - rb * a.col_wgs;
   const int per = 256 / a.lanes;
   const int64_t first = rb * per * ROWS_BACK + threadIdx.x / a.lanes;
-  const int64_t c0 = 8 * (cb * a.lanes + threadIdx.x % a.lanes);
+  const int64_t c0 = EACH * (cb * a.lanes + threadIdx.x % a.lanes);
   if (c0 >= a.cols) return;
   const int64_t groups = (a.cols + GROUP - 1) / GROUP;
-  typename Codes<F>::type c[ROWS_BACK];
+  Raw c[ROWS_BACK];
   int byte[ROWS_BACK];
 #pragma unroll
   for (int i = 0; i < ROWS_BACK; ++i) {
     const int64_t r = first + i * per;
-    c[i] = {};
+    c[i] = Raw{};
     byte[i] = 0;
     if (r < a.N * a.rows) {
-      c[i] = *(const typename Codes<F>::type*)(a.codes + (r * groups * GROUP + c0) * Codes<F>::BITS / 8);
+      c[i] = *(const Raw*)(a.codes + (r * groups * GROUP + c0) * Codes<F>::BITS / 8);
       byte[i] = a.scales[r * groups + c0 / GROUP];
     }
   }
@@ -295,20 +283,34 @@ __global__ __launch_bounds__(256) void mx_values_kernel(DequantArgs a) {
   for (int i = 0; i < ROWS_BACK; ++i) {
     const int64_t r = first + i * per;
     if (r >= a.N * a.rows) return;
-    f32x8 x = Codes<F>::decode(c[i]);
+    float x[EACH];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = byte[i] == 255 ? __builtin_nanf("") : ldexpf(x[q], byte[i] - 127);
+    for (int w = 0; w < QUADS; ++w) {
+      const f32x4 v = Codes<F>::decode(c[i].q[w]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[4 * w + q] = byte[i] == 255 ? __builtin_nanf("") : ldexpf(v[q], byte[i] - 127);
+    }
     if (a.diag) {
       const int64_t d = r % a.rows;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int q = 0; q < EACH; ++q)
         if (c0 + q == d) x[q] += a.diag[r];
     }
-    store8((T*)a.dst + r * a.ld, c0, a.cols, a.vec, x);
+    T* out = (T*)a.dst + r * a.ld + c0;
+    if (a.vec && c0 + EACH <= a.cols) {
+      out_t v;
+#pragma unroll
+      for (int q = 0; q < EACH; ++q) v[q] = (T)x[q];
+      *(out_t*)out = v;
+    } else {
+#pragma unroll
+      for (int q = 0; q < EACH; ++q)
+        if (c0 + q < a.cols) out[q] = (T)x[q];
+    }
   }
 }
 
-// Threads of a 256-thread workgroup on one row of `chunks` 8-element pieces, and workgroups along it
+// Threads of a 256-thread workgroup on one row of `chunks` pieces, and workgroups along it
 void row_split(int64_t chunks, int& lanes, int64_t& col_wgs) {
   lanes = 4;
   while (lanes < 256 && lanes < chunks) lanes *= 2;
@@ -336,7 +338,8 @@ hipError_t quantize(QuantArgs& a, hipStream_t stream) {
 
 template <typename T, int F>
 hipError_t dequantize(DequantArgs& a, hipStream_t stream) {
-  row_split((a.cols + 7) / 8, a.lanes, a.col_wgs);
+  constexpr int EACH = 16 / sizeof(T);
+  row_split((a.cols + EACH - 1) / EACH, a.lanes, a.col_wgs);
   const int per = 256 / a.lanes * ROWS_BACK;
   const int64_t grid = (a.N * a.rows + per - 1) / per * a.col_wgs;
   if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
