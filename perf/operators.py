@@ -269,6 +269,7 @@ def _own(c, s):
         return s["U"]
     if "ws" not in s:
         s["ws"] = dash.grad_stack_mx_workspace(c["T"], c["out"], c["in"], s["dY"].dtype, device=DEV)
+        s["G"] = s["G"].contiguous()  # (one row of tiles may have come as a strided view)
     dash.dash_grad_stack_mx(s["dY"], s["codes"], s["scales"], fmt, c["T"], c["out"], c["in"], c["B"], s["G"],
                             accumulate=c["accumulate"], ws=s["ws"])
     return s["G"]
