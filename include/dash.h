@@ -496,8 +496,11 @@ dash_status dash_update_stats_mx(const void* codes, const void* scales, const vo
 /* dash_apply with microscaled roots: U_t = (XL_t G_t) XR_t^T for t < NG, where XL_t and XR_t are the values
  * of the row codes XL / XR [NG, B, B] plus, when given, their fp32 diagonals XL_diag / XR_diag [NG, B].
  * (The roots are symmetric; the right one is read by rows, as stored, so that it enters transposed:
- * the groups' rounding makes the two differ.)  G_stack, U_stack fp32, results to fp32 accuracy in the
- * given root values.  ws: dash_workspace_size(DASH_OP_APPLY, NG, B, ...), as dash_apply. */
+ * the groups' rounding makes the two differ.)  G_stack and U_stack fp32.  The root values
+ * enter with all their bits, G and XL G with 22, each down to 2^-38 of its block's largest element (as
+ * DASH_FP32_SPLIT16): the error against fp64 is that of fp32 products.  A non-finite element makes
+ * results of its block non-finite, and of no other.
+ * ws: dash_workspace_size(DASH_OP_APPLY, NG, B, ...), as dash_apply. */
 dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL_diag, const void* XR,
                           const void* XR_scales, const float* XR_diag, const float* G_stack, int64_t NG, int32_t B,
                           dash_mx_fmt fmt, float* U_stack, void* ws, size_t ws_bytes, void* stream);
@@ -508,9 +511,9 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
  * in the forward pass), written as dash_stack would stack an out x in weight: ceil(out/B) x ceil(in/B)
  * tiles, the part of an edge tile outside the weight zero.  accumulate = 1 adds to the tiles that
  * G_stack holds (earlier micro-batches; the padding keeps what it holds), 0 overwrites them.  in, ldy at
- * most 2^26.  dY
- * enters exactly in every type, sums are fp32, and equal calls give equal bits.  T = 0 (dY, codes and
- * scales may be NULL): an empty sum.
+ * most 2^26.  dY enters exactly (fp32 magnitudes from 2^-100 to 3.38e38; smaller ones lose low bits, larger
+ * ones count as Inf), sums are fp32, and equal calls give equal bits.  T = 0 (dY, codes and scales may
+ * be NULL): an empty sum.
  * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned. */
 dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, const void* codes, const void* scales,
                                dash_mx_fmt fmt, int64_t T, int64_t out, int64_t in, int32_t B, int32_t accumulate,

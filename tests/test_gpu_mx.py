@@ -480,6 +480,35 @@ def test_grad_stack_nonfinite_rows(dtype):
     assert np.array_equal(~np.isfinite(G), bad)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=["fp32", "bf16", "fp16"])
+def test_unaligned_views(dtype):
+    """Views that start on their element only, at every offset within 16 bytes: as their aligned copies."""
+    fmt, T, out, inp, B = dash.DASH_MX_E4M3, 130, 300, 77, 128
+    rng = di.rng(155)
+    q, s, _ = random_codes(rng, 1, T, inp, fmt)
+    buf = torch.from_numpy(rng.standard_normal((T, out + 24))).to(DEV).to(dtype)
+    for shift in range(1, 9):
+        view = buf[:, shift:shift + out]
+        copy = torch.empty((T, out + 12), dtype=dtype, device=DEV)[:, :out]  # rows of another pitch
+        copy.copy_(view)
+        assert torch.equal(grad(view, q, s, fmt, T, out, inp, B), grad(copy, q, s, fmt, T, out, inp, B))
+        for sides in (("rows",), ("cols",), ("rows", "cols")):
+            got = []
+            for src in (view, copy.contiguous()):
+                pair = [dash.mx_buffers(1, T, out, fmt, device=DEV), dash.mx_buffers(1, out, T, fmt, device=DEV)]
+                args = [x if side in sides else (None, None) for side, x in zip(("rows", "cols"), pair)]
+                dash.dash_mx_quantize(src, 1, T, out, fmt, *args[0], *args[1])
+                got.append([x for a in args for x in a if x is not None])
+            assert all(torch.equal(x, y) for x, y in zip(*got))
+        c, sc = dash.mx_buffers(1, T, out, fmt, device=DEV)
+        dash.dash_mx_quantize(view, 1, T, out, fmt, c, sc)
+        back, wide = torch.zeros_like(buf), torch.empty((T, out), dtype=dtype, device=DEV)
+        dash.dash_mx_dequantize(c, sc, 1, T, out, fmt, back[:, shift:shift + out])
+        dash.dash_mx_dequantize(c, sc, 1, T, out, fmt, wide)
+        assert torch.equal(back[:, shift:shift + out], wide)
+        assert not back[:, :shift].any() and not back[:, shift + out:].any()
+
+
 def test_grad_stack_past_32_bit_offsets():
     """Rows of dY beyond 2^31 elements, codes beyond 2^32 bytes."""
     fmt = dash.DASH_MX_E4M3

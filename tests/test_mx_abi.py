@@ -163,3 +163,32 @@ def test_reference_format(fmt, top, code):
     assert s[0, 0] == 255 and not c.any()
     c, s = mx_ref.quantize(np.zeros((1, 5)), fmt)
     assert s[0, 0] == 0 and not c.any() and c.shape == (1, 32)
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """A launch whose tensors live on another device than the current one makes theirs current."""
+    a = _lib._Args("call")
+    entered = []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *exc):
+            entered.append(None)
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    a.device, a.index = torch.device("cuda:1"), 1
+    a.run(lambda: entered.append("ran") or 0)
+    assert entered == [torch.device("cuda:1"), "ran", None]
+    a.device, a.index = torch.device("cuda:0"), 0
+    del entered[:]
+    a.run(lambda: entered.append("ran") or 0)
+    assert entered == ["ran"]
+    with pytest.raises(dash.DashError) as e:
+        a.run(lambda: INVALID)
+    assert e.value.status == INVALID
