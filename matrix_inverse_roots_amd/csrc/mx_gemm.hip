@@ -8,14 +8,15 @@
 // subnormals), scale included, and the 32x32x16 bfloat16 MFMA forms products of two elements exactly
 // and sums them in fp32.  (The scaled 8-bit MFMA, at twice the rate, drops bits below the largest
 // addend of its 64: sums of 4096 positive E4M3 products came out 7e-5 low, a hundred times fp32's own
-// error, so it is not used; the 4-bit one sums exactly within a group and the E2M1 statistics use it.)  A floating operand beside a microscaled one is cut into bfloat16
-// pieces that add up to it exactly (one for bfloat16, two for binary16, three for fp32), and each
-// piece multiplies the one microscaled piece: exact products again, accumulated in fp32.
+// error, so it is not used; the 4-bit one sums exactly within a group, and the E2M1 statistics use it.)
+// A floating operand beside a microscaled one is cut into bfloat16 pieces that add up to it exactly
+// (one for bfloat16, two for binary16, three for fp32), or into two binary16 pieces (the update), and
+// each piece multiplies the one microscaled piece: exact products again, accumulated in fp32.
 //
-// One kernel frame: an output tile of TILE x TILE, 2 TILE threads, k-slices of 32 (one scale group
-// along k), a register ring of two slices and an LDS double buffer of bfloat16 planes, one per
-// piece.  An operand whose k is contiguous in memory sits in LDS as [row][32 k], one whose k is the
-// slow axis as [k][TILE], read back k-major by the transposing LDS load.
+// One frame: an output tile of TILE x TILE, 2 TILE threads, k-slices of 32 (one scale group along k), a
+// register ring of slices under way and an LDS double buffer of 16-bit planes, one per piece.  An operand
+// whose k is contiguous in memory sits in LDS as [row][32 k], one whose k is the slow axis as [k][TILE],
+// read back k-major by the transposing LDS load.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -118,7 +119,7 @@ __device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&p)[P]) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// LDS planes: TILE x 32 bfloat16
+// LDS planes: TILE x 32 elements of 16 bits
 // ------------------------------------------------------------------------------------------------
 
 // [row][32 k]: rows of four 16-byte chunks; the chunk index is xored with bits 2-3 and bit 1 of the row.
@@ -161,8 +162,10 @@ __device__ __forceinline__ typename Half<TE>::v8 fragment(const TE* plane, int b
 // into LDS planes.  An address is a wave-uniform base that moves with kt plus a 32-bit lane offset.
 // ------------------------------------------------------------------------------------------------
 
-// D: slices in the register ring, 4, but 2 beside fp32 in 256 x 256 tiles (where four spill)
-// Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows beyond `rows` are zero.
+// DEPTH: slices in the register ring, 4, but 2 beside an fp32 operand in 256 x 256 tiles (where four
+// spill) and in the update (where four changed nothing at any width).
+
+// Microscaled, k contiguous: thread t holds 16 k of row t / 2.  Rows beyond the matrix are zero.
 // shift: added to the scale bytes (a power of two on every element).
 template <int F, int TILE, int D, typename E>
 struct CodesK {
@@ -266,15 +269,15 @@ struct CodesCol {
 // fp32, k contiguous, two binary16 pieces of 2^e x: thread t holds 8 k of rows t / 4 and t / 4 + TILE / 2
 // (four lanes read a row's 128 bytes).  Rows from x.cols on (the matrices are square) are zero.  m1 is
 // -1 (see split2).
-template <int TILE, int D>
+template <int TILE>
 struct FloatK {
   typedef _Float16 TE;
-  static constexpr int DEPTH = D;
+  static constexpr int DEPTH = 2;
   static constexpr int PIECES = 2;
   static constexpr bool KS = false;
   const float* p;
   unsigned off;
-  f32x4 r[D][2][2];
+  f32x4 r[DEPTH][2][2];
   int64_t half;  // elements from one of the thread's rows to the other
   int row, chunk, e;
   bool in[2];
@@ -318,15 +321,15 @@ struct FloatK {
 
 // fp32, k the slow axis, two binary16 pieces of 2^e x: thread t holds 8 columns of two of the slice's
 // rows, 16 apart.  Columns beyond the matrix are zero; the slices' rows all exist.
-template <int TILE, int D>
+template <int TILE>
 struct FloatCol16 {
   typedef _Float16 TE;
-  static constexpr int DEPTH = D;
+  static constexpr int DEPTH = 2;
   static constexpr int PIECES = 2;
   static constexpr bool KS = true;
   const float* p;
   unsigned off;
-  f32x4 r[D][2][2];
+  f32x4 r[DEPTH][2][2];
   int64_t ld;
   int k, col, e;
   bool in;
@@ -596,10 +599,10 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, int64_t slices, int64_t
 // ------------------------------------------------------------------------------------------------
 //
 // A 32-k slice of a row is 32 bytes: loaded slice by slice, every load touches one cache line per row
-// and uses a quarter of it, and the lines per load bounded the product.  So 128 k of a row
-// are loaded at once, 16 consecutive k by each of 8 neighbouring lanes, and slice s of the four takes
-// k = 4 s .. 4 s + 3 of every lane's 16: any 32 k make a slice as long as both operands agree.  A thread
-// holds such pieces of four rows, TILE / 4 = 32 apart.  Rows and k beyond B (a multiple of 64) are zero.
+// and uses a quarter of it, and the lines per load bounded the product.  So 128 k of a row are loaded at
+// once, 16 consecutive k by each of 8 neighbouring lanes, and slice s of the four takes k = 4 s .. 4 s + 3
+// of every lane's 16: any 32 k make a slice as long as both operands agree.  A thread holds such pieces
+// of four rows, 32 apart.  Rows and k beyond B (a multiple of 64) are zero.
 // EDGE: B is not a multiple of 128.
 template <int TILE, bool EDGE>
 struct CodesWide {
@@ -707,14 +710,14 @@ struct StatsArgs {
 
 // A <- beta A + (1 - beta) acc for the tile and its mirror, the arithmetic and the accesses of epilogue_split
 // (32 x 32 sub-blocks; on a diagonal tile those below the diagonal store nothing and those on it their
-// upper part and its mirror).  The old values of AHEAD sub-blocks are under way at a time: loaded one
-// sub-block at a time, their latency was a third of the launch.
+// upper part and its mirror).  The old values of AHEAD sub-blocks are under way at a time (256-wide tiles,
+// B = 1024 1620 -> 1551 us).
 template <int TILE, bool EDGE>
 __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoord& tc, float* A,
                                                const f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN], int wm, int wn,
                                                int lane, float* mlds) {
   constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, SUBS = MTM * MTN, AHEAD = SUBS < 4 ? SUBS : 4;
-  constexpr int NT = 2;  // non-temporal: A passes through once (B = 1024 1551 -> 1514 us, 256 600 -> 620 us)
+  constexpr int NT = 2;  // non-temporal: A passes through once (256-wide tiles, B = 1024 1551 -> 1514 us)
   const int B = a.g.B;
   const float al = a.g.epi.alpha, be = a.g.epi.delta;
   const uint64_t at = (uint64_t)(A + tc.b * (int64_t)B * B);  // (the same in every lane: say so)
@@ -1013,11 +1016,11 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
   CodesK<F, TILE, 2, _Float16> lq;
   lq.init(a.q, tc.b, (LEFT ? tc.ti : tc.tj) * TILE, tid, shift);
   if constexpr (LEFT) {
-    FloatCol16<TILE, 2> lx;
+    FloatCol16<TILE> lx;
     lx.init(a.x, tc.b, tc.tj * TILE, tid, ex, m1);
     multiply<TILE>(lq, lx, B / BK, whole, stage0, stage1, wm, wn, lane, acc);
   } else {
-    FloatK<TILE, 2> lx;
+    FloatK<TILE> lx;
     lx.init(a.x, tc.b, tc.ti * TILE, tid, ex, m1);
     multiply<TILE>(lx, lq, B / BK, whole, stage0, stage1, wm, wn, lane, acc);
   }
