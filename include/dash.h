@@ -464,8 +464,9 @@ dash_status dash_apply_vec(const float* X, const float* g_pieces, int64_t P, int
  * after the other. */
 typedef enum { DASH_MX_E2M1 = 0, DASH_MX_E4M3 = 1 } dash_mx_fmt;
 
-/* Quantise N matrices of rows x cols, row-major with row pitch ld >= cols, matrix n at src + n rows ld
- * (elements of `type`: DASH_FP32, DASH_FP16 or DASH_BF16, aligned to their size; any ld).
+/* Quantise N >= 1 matrices of rows x cols (both >= 1, else DASH_ERR_SHAPE), row-major with row pitch ld >=
+ * cols, matrix n at src + n rows ld (elements of `type`: DASH_FP32, DASH_FP16 or DASH_BF16, aligned to
+ * their size; any ld).
  *   codes, scales:     the rows in groups along cols, or both NULL;
  *   codes_t, scales_t: the columns in groups along rows, i.e. the transpose (cols x rows) of each
  *                      matrix quantised by rows, or both NULL; at least one pair is given.  Both pairs

@@ -178,27 +178,28 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(QuantArgs a) {
   }
 }
 
-// Columns, and rows from the same read: a 128 x 128 tile goes through LDS.  Four neighbouring lanes
-// take the four 32-row groups of one column, so that a wave writes 16 columns' 128 (64) contiguous
-// bytes; a row's columns are xored with 16 (row / 32), which puts the four groups on different banks.
-constexpr int QT = 128;
-template <typename T, int F, bool ROWS>
+// Columns, and rows from the same read: a QT x QT tile goes through LDS.  QT / 32 neighbouring lanes take
+// the 32-row groups of one column, so that with QT = 128 a wave writes 16 columns' 128 (64) contiguous
+// bytes; a row's columns are xored with 16 (row / 32), which puts the groups on different banks.
+template <typename T, int F, bool ROWS, int QT>
 __global__ __launch_bounds__(256) void mx_cols_kernel(QuantArgs a) {
+  constexpr int CHUNKS = QT / 8, STEP = 256 / CHUNKS, EACH = QT / STEP;  // 8-column pieces per row; a thread's rows
+  constexpr int GROUPS = QT / GROUP;
   __shared__ __attribute__((aligned(16))) float tile[QT * QT];
   const int64_t tr = (a.rows + QT - 1) / QT, tc = (a.cols + QT - 1) / QT;
   const int64_t n = blockIdx.x / (tr * tc), t = blockIdx.x - n * (tr * tc);
   const int64_t r0 = t / tc * QT, c0 = t % tc * QT;
   const T* src = (const T*)a.src + n * a.rows * a.ld;
   const int64_t gc = (a.cols + GROUP - 1) / GROUP, gr = (a.rows + GROUP - 1) / GROUP;
-  f32x8 x[8];
+  f32x8 x[EACH];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // row threadIdx.x / 16 + 16 i, columns 8 (threadIdx.x % 16) ..
-    const int64_t r = r0 + threadIdx.x / 16 + 16 * i, c = c0 + 8 * (threadIdx.x % 16);
+  for (int i = 0; i < EACH; ++i) {
+    const int64_t r = r0 + threadIdx.x / CHUNKS + STEP * i, c = c0 + 8 * (threadIdx.x % CHUNKS);
     x[i] = r < a.rows ? load8(src + r * a.ld, c, a.cols, a.vec) : f32x8{};
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int lr = threadIdx.x / 16 + 16 * i, lc = 8 * (threadIdx.x % 16);
+  for (int i = 0; i < EACH; ++i) {
+    const int lr = threadIdx.x / CHUNKS + STEP * i, lc = 8 * (threadIdx.x % CHUNKS);
     const int64_t r = r0 + lr, c = c0 + lc;
     if (a.diag && r < a.rows) take_diag(x[i], r, c, a.diag + n * a.rows + r);
     *(f32x8*)&tile[lr * QT + (lc ^ (16 * (lr >> 5)))] = x[i];
@@ -213,8 +214,8 @@ __global__ __launch_bounds__(256) void mx_cols_kernel(QuantArgs a) {
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int g = threadIdx.x & 3, lc = (threadIdx.x >> 2) + 64 * i;
+  for (int task = threadIdx.x; task < QT * GROUPS; task += 256) {
+    const int g = task % GROUPS, lc = task / GROUPS;
     const int64_t c = c0 + lc, r = r0 + GROUP * g;
     if (c >= a.cols || r >= a.rows) continue;
     f32x8 y[4];
@@ -317,16 +318,29 @@ void row_split(int64_t chunks, int& lanes, int64_t& col_wgs) {
   col_wgs = (chunks + lanes - 1) / lanes;
 }
 
+template <typename K>
+hipError_t launch_cols(K kernel, int64_t side, QuantArgs& a, hipStream_t stream) {
+  const int64_t grid = a.N * ((a.rows + side - 1) / side) * ((a.cols + side - 1) / side);
+  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
 template <typename T, int F>
 hipError_t quantize(QuantArgs& a, hipStream_t stream) {
   if (a.codes_t) {
-    const int64_t grid = a.N * ((a.rows + QT - 1) / QT) * ((a.cols + QT - 1) / QT);
-    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    if (a.codes)
-      hipLaunchKernelGGL((mx_cols_kernel<T, F, true>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((mx_cols_kernel<T, F, false>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    // 64-wide tiles, but 128-wide ones (whole lines written per column) for large stacks of fp32 that fill
+    // them.  Both measured (us, 64 / 128): 1777 x 1001 fp16 10 / 12, 60 x 320 x 320 8 / 13, 48 x 1024 x 1024
+    // 61 / 70, 96 x 1024 x 1024 128 / 114, 192 x 1024 x 1024 269 / 218, 4000 x 192 x 192 172 / 255, 20000 x 6437
+    // 316 / 283 (fp32 to E4M3); 16384 x 16384 bfloat16 328 / 372.
+    if constexpr (sizeof(T) == 4) {
+      const int64_t tiles = a.N * ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
+      if (tiles >= 4096 && (double)tiles * (128 * 128) <= 1.1 * (double)a.N * (double)a.rows * (double)a.cols)
+        return a.codes ? launch_cols(mx_cols_kernel<T, F, true, 128>, 128, a, stream)
+                       : launch_cols(mx_cols_kernel<T, F, false, 128>, 128, a, stream);
+    }
+    return a.codes ? launch_cols(mx_cols_kernel<T, F, true, 64>, 64, a, stream)
+                   : launch_cols(mx_cols_kernel<T, F, false, 64>, 64, a, stream);
   }
   row_split((a.cols + GROUP - 1) / GROUP * 4, a.lanes, a.col_wgs);
   const int per = 256 / a.lanes * ROWS_IN<T>;

@@ -117,6 +117,29 @@ def test_quantize_equals_the_definition(dtype, fmt, sides):
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=IDS)
+@pytest.mark.parametrize("N,rows,cols", [(66, 1024, 1024), (1, 8300, 8191)])
+def test_quantize_large_stacks(N, rows, cols, fmt):
+    """Sizes that take the wide column tiles: as the rows of the matrices and of their transposes."""
+    gen = torch.Generator(device=DEV).manual_seed(N)
+    x = torch.randn((N, rows, cols), generator=gen, device=DEV)
+    x *= torch.exp2(torch.randint(-20, 20, (N, rows, 1), generator=gen, device=DEV).float())
+    x[0, 5, 7], x[-1, -1, -1] = float("inf"), float("nan")
+    both = [dash.mx_buffers(N, rows, cols, fmt, device=DEV), dash.mx_buffers(N, cols, rows, fmt, device=DEV)]
+    dash.dash_mx_quantize(x, N, rows, cols, fmt, *both[0], *both[1])
+    alone = dash.mx_buffers(N, cols, rows, fmt, device=DEV)
+    dash.dash_mx_quantize(x, N, rows, cols, fmt, None, None, *alone)
+    for m, got in ((x, both[0]), (x.transpose(1, 2).contiguous(), both[1])):
+        want = dash.mx_buffers(*m.shape, fmt, device=DEV)
+        dash.dash_mx_quantize(m, *m.shape, fmt, *want)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(alone[0], both[1][0]) and torch.equal(alone[1], both[1][1])
+    # and a few rows of it against the definition
+    code, byte = ref.quantize(x[0, :9].double().cpu().numpy(), fmt)
+    assert np.array_equal(host(both[0][0][0, :9]).numpy(), ref.pack(code, fmt))
+    assert np.array_equal(host(both[0][1][0, :9]).numpy(), byte)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=IDS)
 @pytest.mark.parametrize("sides", ["rows", "both"])
 def test_quantize_diagonal(fmt, sides):
     rng = di.rng(75)
