@@ -982,8 +982,33 @@ struct ApplyArgs {
   float* amax_out;        // LEFT: [N, tiles, waves]: the largest |out| each wave stored
 };
 
-// LEFT: out = Q X (Q's rows, X's columns); else out = X Q^T (X's rows, Q's rows as columns)
-template <int F, int TILE, bool LEFT>
+// The largest v (NaN passed over) and c over a workgroup's threads, in all of them
+template <int WAVES>
+__device__ __forceinline__ void block_max(float& v, unsigned& c) {
+  __shared__ float vs[WAVES];
+  __shared__ unsigned cs[WAVES];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned x = __shfl_xor(c, o, 64);
+    v = fmaxf(v, __shfl_xor(v, o, 64));
+    c = x > c ? x : c;
+  }
+  if ((threadIdx.x & 63) == 0) {
+    vs[threadIdx.x >> 6] = v;
+    cs[threadIdx.x >> 6] = c;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    v = fmaxf(v, vs[w]);
+    c = cs[w] > c ? cs[w] : c;
+  }
+}
+
+// LEFT: out = Q X (Q's rows, X's columns); else out = X Q^T (X's rows, Q's rows as columns).  OWN: no launch
+// went before for the bounds; each workgroup takes G's (LEFT) and the root's scale bytes' from the block
+// itself
+template <int F, int TILE, bool LEFT, bool OWN>
 __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
   constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, WAVES = TILE / 32;
   constexpr int STAGE = 3 * TILE * BK;
@@ -995,17 +1020,35 @@ __global__ __launch_bounds__(2 * TILE) void mx_apply_kernel(ApplyArgs a) {
   const int wm = wave / Shape<TILE>::WN, wn = wave % Shape<TILE>::WN;
   float m = 0.f;
   unsigned top = 0;
-  for (int p = lane; p < a.parts; p += 64) m = fmaxf(m, a.amax[tc.b * a.parts + p]);
-  for (int p = lane; p < a.byte_parts; p += 64) {
-    const unsigned v = a.bytes[tc.b * a.byte_parts + p];
-    const unsigned c = LEFT ? v & 255u : v >> 8;
-    top = c > top ? c : top;
-  }
+  if (!(OWN && LEFT))
+    for (int p = lane; p < a.parts; p += 64) m = fmaxf(m, a.amax[tc.b * a.parts + p]);
+  if constexpr (OWN) {
+    const int n = B * B;
+    if (LEFT) {
+      const f32x4* g = (const f32x4*)((const float*)a.x.p + tc.b * n);
+#pragma unroll 4
+      for (int i = tid; i < n / 4; i += 2 * TILE) {
+        const f32x4 v = g[i];
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+      }
+    }
+    for (int i = tid; i < n / MX_GROUP; i += 2 * TILE) {
+      const unsigned c = a.q.scales[tc.b * (n / MX_GROUP) + i];
+      top = c != 255u && c > top ? c : top;
+    }
+    block_max<WAVES>(m, top);
+  } else {
+    for (int p = lane; p < a.byte_parts; p += 64) {
+      const unsigned v = a.bytes[tc.b * a.byte_parts + p];
+      const unsigned c = LEFT ? v & 255u : v >> 8;
+      top = c > top ? c : top;
+    }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const unsigned c = __shfl_xor(top, o, 64);
-    m = fmaxf(m, __shfl_xor(m, o, 64));
-    top = c > top ? c : top;
+    for (int o = 32; o > 0; o >>= 1) {
+      const unsigned c = __shfl_xor(top, o, 64);
+      m = fmaxf(m, __shfl_xor(m, o, 64));
+      top = c > top ? c : top;
+    }
   }
   const int ex = __builtin_amdgcn_readfirstlane(top_exp(m));
   const int shift = __builtin_amdgcn_readfirstlane(127 + Elem<F>::TOP - (int)top);
@@ -1111,7 +1154,7 @@ __global__ __launch_bounds__(256) void mx_bounds_kernel(const float* G, const ui
   }
 }
 
-template <int F, int TILE>
+template <int F, int TILE, bool OWN>
 hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream) {
   a.g.tdim = (p.B + TILE - 1) / TILE;
   a.g.tiles = a.g.tdim * a.g.tdim;
@@ -1124,7 +1167,7 @@ hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream)
   a.amax = p.amax_g;
   a.parts = p.parts;
   a.amax_out = p.amax_t;
-  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, true>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, true, OWN>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.q = p.xr;
@@ -1133,7 +1176,7 @@ hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream)
   a.out = p.U;
   a.amax = p.amax_t;
   a.parts = a.g.tiles * (TILE / 32);
-  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, false>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
+  hipLaunchKernelGGL((mx_apply_kernel<F, TILE, false, OWN>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -1154,12 +1197,18 @@ int apply_tile(int64_t N, int B) {
   return best;
 }
 
+// Up to this B a block is 64 KiB or less, and its workgroups find the bounds themselves: with / without a
+// launch for them, 2 x 128 22 / 19 us, 3000 x 128 258 / 240, 20000 x 64 403 / 357; but 1000 x 192 257 / 323.
+constexpr int APPLY_OWN_BOUNDS = 128;
+
 template <int F>
 hipError_t launch_apply_fmt(ApplyArgs& a, const MxApply& p, hipStream_t stream) {
   const int tile = apply_tile(p.N, p.B);
-  return tile == 256   ? launch_apply_tile<F, 256>(a, p, stream)
-         : tile == 128 ? launch_apply_tile<F, 128>(a, p, stream)
-                       : launch_apply_tile<F, 64>(a, p, stream);
+  if (p.B <= APPLY_OWN_BOUNDS)  // (a 256-wide tile is never the cheapest there)
+    return tile > 64 ? launch_apply_tile<F, 128, true>(a, p, stream) : launch_apply_tile<F, 64, true>(a, p, stream);
+  return tile == 256   ? launch_apply_tile<F, 256, false>(a, p, stream)
+         : tile == 128 ? launch_apply_tile<F, 128, false>(a, p, stream)
+                       : launch_apply_tile<F, 64, false>(a, p, stream);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1367,12 +1416,14 @@ hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG,
 }
 
 hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream) {
-  const int64_t grid = p.N * p.parts;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(mx_bounds_kernel, dim3((unsigned)grid), dim3(256), 0, stream, p.G, p.xl.scales, p.xr.scales, p.B,
-                     p.parts, p.amax_g, p.bytes);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (p.B > APPLY_OWN_BOUNDS) {
+    const int64_t grid = p.N * p.parts;
+    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(mx_bounds_kernel, dim3((unsigned)grid), dim3(256), 0, stream, p.G, p.xl.scales, p.xr.scales,
+                       p.B, p.parts, p.amax_g, p.bytes);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   ApplyArgs a;
   a.g.N = p.N;
   a.g.B = p.B;

@@ -328,7 +328,7 @@ def test_apply(B, fmt, diag):
 
 @pytest.mark.parametrize("diag", [False, True])
 @pytest.mark.parametrize("fmt", FMTS, ids=IDS)
-@pytest.mark.parametrize("N,B", [(60, 256), (50, 320), (40, 448), (130, 512)])
+@pytest.mark.parametrize("N,B", [(500, 64), (300, 128), (60, 256), (50, 320), (40, 448), (130, 512)])
 def test_apply_wide(N, B, fmt, diag):
     """Stacks that take 128- and 256-wide kernel tiles, whole and at the edges."""
     rng = di.rng(110 + B)
