@@ -697,6 +697,101 @@ def test_captured_step_replays():
             assert torch.equal(b[k], e[k]), (seed, k)
 
 
+@pytest.mark.parametrize("B", [64, 128, 192, 320, 448])
+@pytest.mark.parametrize("N", [1, 50])
+def test_nothing_is_written_past_the_buffers(N, B):
+    """Outputs and exactly sized workspaces end where they say, for every tile width and edge."""
+    fmt8, fmt4 = dash.DASH_MX_E4M3, dash.DASH_MX_E2M1
+    rng = di.rng(180 + B)
+
+    def guarded(n, dtype=torch.float32):
+        buf = torch.full((n + 4096,), 77, dtype=dtype, device=DEV)
+        return buf, buf[:n]
+
+    tails = []
+    for fmt in (fmt8, fmt4):
+        q, s, _ = random_codes(rng, 1, B, B, fmt)
+        q, s = q.expand(N, -1, -1).contiguous(), s.expand(N, -1, -1).contiguous()
+        G = torch.randn((N, B, B), generator=torch.Generator(device=DEV).manual_seed(B), device=DEV)
+        buf, Ud = guarded(N * B * B)
+        wbuf, ws = guarded(dash.dash_workspace_size(dash.DASH_OP_APPLY, N, B), torch.uint8)
+        dash.dash_apply_mx(q, s, q, s, G, N, B, fmt, Ud, ws=ws)
+        tails += [buf[N * B * B:], wbuf[ws.numel():]]
+        assert bool(torch.isfinite(Ud).all())
+        buf, A = guarded(2 * N * B * B)
+        A.zero_()
+        dash.dash_update_stats_mx(q, s, q, s, N, B, fmt, 0.5, A)
+        tails.append(buf[2 * N * B * B:])
+        T, out, inp = 40 * N + 700, B + 9, B - 5
+        x, xs, _ = random_codes(rng, 1, T, inp, fmt)
+        n = 4 * B * B if inp > B else 2 * B * B
+        buf, Gd = guarded(n)
+        for dtype in TYPES:
+            dY = torch.ones((T, out), dtype=dtype, device=DEV)
+            need = dash.dash_grad_stack_mx_workspace(T, out, inp, dash._lib._prec_of(dtype))
+            wbuf, ws = guarded(need, torch.uint8)
+            dash.dash_grad_stack_mx(dY, x, xs, fmt, T, out, inp, B, Gd, ws=ws if need else None)
+            tails += [buf[n:], wbuf[need:]]
+    torch.cuda.synchronize()
+    for tail in tails:
+        assert bool((tail == 77).all())
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own buffers, equal the same calls in turn."""
+    fmt8, fmt4 = dash.DASH_MX_E4M3, dash.DASH_MX_E2M1
+    T, out, inp, B = 3000, 300, 400, 128
+    data = [pipeline_inputs(190 + i, T, out, inp) for i in range(2)]
+    ref_b, b = ([pipeline_buffers(T, fmt8, fmt4, out, inp, B) for _ in range(2)] for _ in range(2))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        pipeline(*data[i], fmt8, fmt4, out, inp, B, ref_b[i])
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in range(2):
+            b[i]["A"].copy_((torch.eye(B, device=DEV) * 40.0).expand_as(b[i]["A"]))
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                pipeline(*data[i], fmt8, fmt4, out, inp, B, b[i])
+        torch.cuda.synchronize()
+        for i in range(2):
+            for k in ("x", "G", "g", "gt", "A", "r", "d", "U"):
+                assert torch.equal(b[i][k], ref_b[i][k]), (i, k)
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls with one workspace, replayed in turn: each equals its eager call every time."""
+    fmt, B = dash.DASH_MX_E4M3, 64
+    rng = di.rng(195)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    calls = []
+    for T, out, inp in ((5000, 72, 40), (3000, 100, 130)):
+        q, s, _ = random_codes(rng, 1, T, inp, fmt)
+        dY = torch.from_numpy(rng.standard_normal((T, out)).astype(np.float32)).to(DEV)
+        assert 0 < dash.dash_grad_stack_mx_workspace(T, out, inp, dash.DASH_FP32) <= ws.numel()
+        G = torch.empty((-(-out // B) * -(-inp // B), B, B), device=DEV)
+        calls.append((lambda dY=dY, q=q, s=s, T=T, out=out, inp=inp, G=G: dash.dash_grad_stack_mx(
+            dY, q, s, fmt, T, out, inp, B, G, ws=ws), G, dY))
+    graphs = []
+    for call, G, _ in calls:
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for i in range(4):
+        for (call, G, dY), g in zip(calls, graphs):
+            dY.mul_(-0.5)
+            G.fill_(float("nan"))
+            g.replay()
+            got = G.clone()
+            call()
+            torch.cuda.synchronize()
+            assert torch.equal(G, got), i
+
+
 def test_wrong_tensors_are_refused():
     x = torch.zeros((64, 64), device=DEV)
     c, s = dash.mx_buffers(1, 64, 64, dash.DASH_MX_E4M3, device=DEV)
