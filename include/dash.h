@@ -499,8 +499,9 @@ dash_status dash_update_stats_mx(const void* codes, const void* scales, const vo
  * (The roots are symmetric; the right one is read by rows, as stored, so that it enters transposed:
  * the groups' rounding makes the two differ.)  G_stack and U_stack fp32.  The root values
  * enter with all their bits, G and XL G with 22, each down to 2^-38 of its block's largest element (as
- * DASH_FP32_SPLIT16): the error against fp64 is that of fp32 products.  A non-finite element makes
- * results of its block non-finite, and of no other.
+ * DASH_FP32_SPLIT16): the error against fp64 is that of fp32 products.  A NaN group or a non-finite
+ * diagonal element of a root makes its row (XL) or column (XR) of U non-finite, a non-finite element of G
+ * its whole block; bounds are taken over finite elements, so nothing else changes.
  * ws: dash_workspace_size(DASH_OP_APPLY, NG, B, ...), as dash_apply. */
 dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL_diag, const void* XR,
                           const void* XR_scales, const float* XR_diag, const float* G_stack, int64_t NG, int32_t B,

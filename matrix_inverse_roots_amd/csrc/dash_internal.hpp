@@ -328,8 +328,8 @@ hipError_t launch_mx_dequantize(const void* codes, const void* scales, const flo
 hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG, int B, dash_mx_fmt fmt, float beta,
                            float* A, hipStream_t stream);
 // U = (XL G) XR^T: the roots' row codes and fp32 diagonals (or null), the intermediate T [N, B, B], and
-// bounds per block: max|G| and both roots' largest scale bytes in mx_apply_parts(B) pieces, max|T| in at
-// most mx_apply_waves(B) pieces
+// bounds per block, over finite elements: max|G| and both roots' largest scale bytes in mx_apply_parts(B)
+// pieces, max|T| in at most mx_apply_waves(B) pieces
 struct MxApply {
   int64_t N;
   int B;
