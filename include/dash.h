@@ -404,7 +404,8 @@ dash_status dash_inverse_root_evd_prec(const float* A, int64_t N, int32_t B, int
 /* Preconditioned update U_t = (XL_t G_t) XR_t for t < NG ([TG] body: the -1/4 powers of L and R
  * precondition the gradient).  XL, XR, G_stack, U_stack are [NG,B,B]; U_stack must not alias the
  * inputs.  ws holds one [NG,B,B] intermediate and the magnitude bounds that DASH_FP32_SPLIT16
- * uses (dash_workspace_size(DASH_OP_APPLY), the same for every prec). */
+ * uses (dash_workspace_size(DASH_OP_APPLY), the same for every prec; that size serves dash_apply_mx too,
+ * whose bounds can take more, and this call accepts one without them). */
 dash_status dash_apply(const float* XL, const float* XR, const float* G_stack, int64_t NG, int32_t B, float* U_stack,
                        void* ws, size_t ws_bytes, void* stream);
 

@@ -99,14 +99,16 @@ dash_status grad_shape_check(int64_t T, int64_t out, int64_t in, int64_t ldy, da
   return most > MX_MAX_ELEMENTS ? DASH_ERR_SHAPE : DASH_OK;
 }
 // apply: the intermediate stack T = XL G, and for two-piece binary16 products the bounds of XL, G
-// and XR per block and T's per-wave maxima (with microscaled roots G's bound and the roots' scale bytes
-// in mx_apply_parts pieces, and T's maxima at up to mx_apply_waves)
+// and XR per block and T's per-wave maxima
 size_t ws_apply(int64_t N, int B) {
-  const size_t fp32 = 3 * align_up((size_t)N * sizeof(float), 256) +
-                      align_up((size_t)N * ndb_parts(B) * sizeof(float), 256);
-  const size_t mx = 2 * align_up((size_t)N * mx_apply_parts(B) * sizeof(float), 256) +
-                    align_up((size_t)N * mx_apply_waves(B) * sizeof(float), 256);
-  return stack_bytes(N, B, DASH_FP32) + (fp32 > mx ? fp32 : mx);
+  return stack_bytes(N, B, DASH_FP32) + 3 * align_up((size_t)N * sizeof(float), 256) +
+         align_up((size_t)N * ndb_parts(B) * sizeof(float), 256);
+}
+// with microscaled roots: T, G's bound and the roots' scale bytes in mx_apply_parts pieces, and T's maxima at up
+// to mx_apply_waves
+size_t ws_apply_mx(int64_t N, int B) {
+  return stack_bytes(N, B, DASH_FP32) + 2 * align_up((size_t)N * mx_apply_parts(B) * sizeof(float), 256) +
+         align_up((size_t)N * mx_apply_waves(B) * sizeof(float), 256);
 }
 size_t ndb_bound_bytes(int64_t N, int B) {
   return align_up((size_t)N * sizeof(float), 256) + 5 * align_up((size_t)N * ndb_parts(B) * sizeof(float), 256);
@@ -783,7 +785,11 @@ dash_status dash_workspace_size(dash_op op, int64_t N, int32_t B, dash_prec prec
     case DASH_OP_CN: *bytes = ws_cn(N, B, prec); return DASH_OK;
     case DASH_OP_CHEB: *bytes = ws_cheb(N, B); return DASH_OK;
     case DASH_OP_ROUTED: *bytes = ws_routed(N, B); return DASH_OK;
-    case DASH_OP_APPLY: *bytes = ws_apply(N, B); return DASH_OK;
+    case DASH_OP_APPLY: {  // either call's
+      const size_t fp32 = ws_apply(N, B), mx = ws_apply_mx(N, B);
+      *bytes = fp32 > mx ? fp32 : mx;
+      return DASH_OK;
+    }
     case DASH_OP_STATS: *bytes = split16 ? ws_stats16(N) : 0; return DASH_OK;
     case DASH_OP_EVD: *bytes = ws_evd(N, B); return DASH_OK;
   }
@@ -1767,7 +1773,7 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
   if ((XL_diag && !aligned(XL_diag, 4)) || (XR_diag && !aligned(XR_diag, 4)))
     return DASH_ERR_INVALID_ARG;
   if (!valid_B(B)) return DASH_ERR_SHAPE;
-  if (!ws || !aligned(ws, 256) || ws_bytes < ws_apply(NG, B)) return DASH_ERR_WORKSPACE;
+  if (!ws || !aligned(ws, 256) || ws_bytes < ws_apply_mx(NG, B)) return DASH_ERR_WORKSPACE;
   Carver cv{(char*)ws, ws_bytes};
   MxApply p;
   p.N = NG;

@@ -1,0 +1,28 @@
+"""Host-side tests of the update's and the gradient tiles' workspace sizes (no GPU): nothing is launched."""
+import pytest
+
+import matrix_inverse_roots_amd as dash
+from matrix_inverse_roots_amd import _lib
+from test_mx_abi import E2, P, WS, Ws, status
+
+
+def up(n):
+    return -(-n // 256) * 256
+
+
+def apply_bytes(N, B):
+    """dash_apply: T, a bound per block of XL, G and XR, and T's per-wave maxima."""
+    return up(4 * N * B * B) + 3 * up(4 * N) + up(4 * N * 8 * (B // 256) ** 2)
+
+
+def test_the_sizes_that_dash_apply_takes():
+    assert apply_bytes(1536, 1024) == 6443255808 and apply_bytes(100, 64) == 1639936
+    for N, B in ((1536, 1024), (100, 64), (3, 192), (50, 448)):
+        reported = dash.dash_workspace_size(dash.DASH_OP_APPLY, N, B)
+        assert reported >= apply_bytes(N, B)  # (dash_apply_mx's bounds can take more)
+        for prec in (dash.DASH_FP32, dash.DASH_FP32_SPLIT, dash.DASH_FP32_SPLIT16):
+            assert status(dash.dash_apply_prec, P[0], P[1], P[2], N, B, prec, P[3],
+                          ws=Ws(P[8], apply_bytes(N, B) - 1)) == WS
+        # and the microscaled update wants all of its own: T and more than one bound per block
+        assert status(dash.dash_apply_mx, P[0], P[1], P[2], P[3], P[4], N, B, E2, P[5],
+                      ws=Ws(P[8], up(4 * N * B * B) + 3 * up(4 * N) - 1)) == WS
