@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libdash.so")
@@ -40,6 +41,11 @@ _torch_module = None
 _Tensor = ()  # torch.Tensor
 _dtypes = {}  # element types by the names that _Args.ptr takes
 _precs = {}  # dash_prec by element type
+
+
+def _torch_loaded():
+    """Whether the program has torch (only then can an argument be a tensor); takes it up if so."""
+    return sys.modules.get("torch") is not None and _torch() is not None
 
 
 def _torch():
@@ -135,10 +141,10 @@ class _Args:
         self.call = call
         self.device = None
         self.index = -1  # of that device
-        if _torch_module is None:
-            _torch()
 
     def _tensor(self, t, name):
+        if _torch_module is None and not _torch_loaded():  # (raw addresses need no torch)
+            return False
         if not isinstance(t, _Tensor):
             return False
         index = t.get_device()
@@ -238,7 +244,7 @@ class _Args:
         if stream is not None:
             return stream if isinstance(stream, int) else stream.cuda_stream
         if self.device is None:
-            return _torch_module.cuda.current_stream(None).cuda_stream
+            return _torch().cuda.current_stream(None).cuda_stream
         return _torch_module._C._cuda_getCurrentRawStream(self.index)  # (current_stream(device) without its object)
 
     def run(self, fn, *args):
