@@ -509,14 +509,15 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
                           dash_mx_fmt fmt, float* U_stack, void* ws, size_t ws_bytes, void* stream);
 
 /* A linear layer's weight gradient from its microscaled input, as gradient tiles: for the input's T
- * tokens, W = dY^T Q with dY [T, out] (`type`, aligned to its element, any row pitch ldy >= out; rows
- * that start on 16 bytes load fastest) the gradient of the layer's output and Q [T, in] the values of codes/scales (the input quantised by rows
- * in the forward pass), written as dash_stack would stack an out x in weight: ceil(out/B) x ceil(in/B)
- * tiles, the part of an edge tile outside the weight zero.  accumulate = 1 adds to the tiles that
- * G_stack holds (earlier micro-batches; the padding keeps what it holds), 0 overwrites them.  in, ldy at
- * most 2^26.  dY enters exactly (fp32 magnitudes from 2^-100 to 3.38e38; smaller ones lose low bits, larger
- * ones count as Inf), sums are fp32, and equal calls give equal bits.  T = 0 (dY, codes and scales may
- * be NULL): an empty sum.
+ * tokens, W = dY^T Q with dY [T, out] the gradient of the layer's output (`type`, aligned to its element,
+ * any row pitch ldy >= out; rows that start on 16 bytes load fastest) and Q [T, in] the values of
+ * codes/scales (the input quantised by rows in the forward pass), written as dash_stack would stack an
+ * out x in weight: ceil(out/B) x ceil(in/B) tiles, the part of an edge tile outside the weight zero.
+ * accumulate = 1 adds to the tiles that G_stack holds (earlier micro-batches; the padding keeps what it
+ * holds), 0 overwrites them.  in, ldy at most 2^26.  dY enters exactly (fp32 magnitudes from 2^-100 to
+ * 3.38e38; smaller ones lose low bits, those above 3.39e38 count as Inf), sums are fp32, an Inf or a NaN in
+ * dY gives its row of W the infinities and NaN of those sums, and equal calls give equal bits.  T = 0 (dY,
+ * codes and scales may be NULL): an empty sum.
  * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned. */
 dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, const void* codes, const void* scales,
                                dash_mx_fmt fmt, int64_t T, int64_t out, int64_t in, int32_t B, int32_t accumulate,
