@@ -498,11 +498,16 @@ dash_status dash_update_stats_mx(const void* codes, const void* scales, const vo
 /* dash_apply with microscaled roots: U_t = (XL_t G_t) XR_t^T for t < NG, where XL_t and XR_t are the values
  * of the row codes XL / XR [NG, B, B] plus, when given, their fp32 diagonals XL_diag / XR_diag [NG, B].
  * (The roots are symmetric; the right one is read by rows, as stored, so that it enters transposed:
- * the groups' rounding makes the two differ.)  G_stack and U_stack fp32.  The root values
- * enter with all their bits, G and XL G with 22, each down to 2^-38 of its block's largest element (as
- * DASH_FP32_SPLIT16): the error against fp64 is that of fp32 products.  A NaN group or a non-finite
- * diagonal element of a root makes its row (XL) or column (XR) of U non-finite, a non-finite element of G
- * its whole block; bounds are taken over finite elements, so nothing else changes.
+ * the groups' rounding makes the two differ.)  G_stack and U_stack fp32.
+ * Precision, as DASH_FP32_SPLIT16: G and T = XL G enter their products with 22 bits, and not below 2^-38 of
+ * their block's largest finite element, i.e. an element m of a block with largest M is off by at most
+ * 2^-22 |m| + 2^-38 M; root values are exact down to 2^-38 of what the block's largest scale can hold;
+ * the diagonals enter in fp32; sums are fp32.  Against fp64, U is as near as fp32 products make it where
+ * a block's rows and columns of G (and of T) are within some 2^16 of each other; the error of a row or
+ * column 2^-20 of the largest is about 4e-6 of it, of one at 2^-30 5e-3, and below 2^-38 it is lost.
+ * (dash_apply on roots that dash_mx_dequantize made has no such limit.)
+ * A NaN group or a non-finite diagonal element of a root makes its row (XL) or column (XR) of U
+ * non-finite, a non-finite element of G its whole block; nothing else changes.
  * ws: dash_workspace_size(DASH_OP_APPLY, NG, B, ...), as dash_apply. */
 dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL_diag, const void* XR,
                           const void* XR_scales, const float* XR_diag, const float* G_stack, int64_t NG, int32_t B,
