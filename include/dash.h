@@ -523,7 +523,10 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
  * 3.38e38; smaller ones lose low bits, those above 3.39e38 count as Inf), sums are fp32, an Inf or a NaN in
  * dY gives its row of W the infinities and NaN of those sums, and equal calls give equal bits.  T = 0 (dY,
  * codes and scales may be NULL): an empty sum.
- * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned. */
+ * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned.  The size
+ * is that of one T: the split of the tokens is chosen by a measured cost, and a smaller T can need more
+ * (out = 256, in = 192, bfloat16: 4032 KiB at T = 2000, 3648 KiB at 4096).  One workspace for calls of
+ * several T takes the largest of their sizes. */
 dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, const void* codes, const void* scales,
                                dash_mx_fmt fmt, int64_t T, int64_t out, int64_t in, int32_t B, int32_t accumulate,
                                float* G_stack, void* ws, size_t ws_bytes, void* stream);

@@ -664,12 +664,13 @@ def dash_grad_stack_mx_workspace(T: int, out_features: int, in_features: int, ty
     return out.value
 
 
-def grad_stack_mx_workspace(T: int, out_features: int, in_features: int, dtype, device="cuda"):
+def grad_stack_mx_workspace(T, out_features: int, in_features: int, dtype, device="cuda"):
     """A byte tensor of the size dash_grad_stack_mx_workspace reports for dY of torch type `dtype` (None
-    when no workspace is needed)."""
-    import torch
-
-    n = dash_grad_stack_mx_workspace(T, out_features, in_features, _prec_of(dtype))
+    when no workspace is needed).  T: a token count, or several (a list, tuple or range) whose calls share
+    the workspace: a smaller count can need more than a larger one, so it holds the largest size of all."""
+    torch = _torch()
+    n = max(dash_grad_stack_mx_workspace(t, out_features, in_features, _prec_of(dtype))
+            for t in ((T,) if hasattr(T, "__index__") else T))
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 

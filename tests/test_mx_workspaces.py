@@ -1,9 +1,8 @@
 """Host-side tests of the update's and the gradient tiles' workspace sizes (no GPU): nothing is launched."""
-import pytest
+import torch
 
 import matrix_inverse_roots_amd as dash
-from matrix_inverse_roots_amd import _lib
-from test_mx_abi import E2, P, WS, Ws, status
+from test_mx_abi import E2, E4, P, WS, Ws, status
 
 
 def up(n):
@@ -26,3 +25,20 @@ def test_the_sizes_that_dash_apply_takes():
         # and the microscaled update wants all of its own: T and more than one bound per block
         assert status(dash.dash_apply_mx, P[0], P[1], P[2], P[3], P[4], N, B, E2, P[5],
                       ws=Ws(P[8], up(4 * N * B * B) + 3 * up(4 * N) - 1)) == WS
+
+
+def test_gradient_workspace_is_for_its_token_count():
+    """The size can fall as T grows: a workspace for one T alone is refused by another that needs more, and one
+    for several serves each."""
+    size = lambda T: dash.dash_grad_stack_mx_workspace(T, 256, 192, dash.DASH_BF16)
+    assert size(2000) == 4032 * 1024 > size(4096) == 3648 * 1024 > size(100) == 0
+    call = lambda T, n: status(dash.dash_grad_stack_mx, P[0], P[1], P[2], E4, T, 256, 192, 64, P[3], type=dash.DASH_BF16,
+                               ws=Ws(P[8], n))
+    assert call(2000, size(4096)) == WS
+    counts = [100, 1024, 2000, 4096]
+    for T in (counts, tuple(counts), range(1, 4097)):
+        ws = dash.grad_stack_mx_workspace(T, 256, 192, torch.bfloat16, device="cpu")
+        assert ws.numel() >= max(size(t) for t in counts)
+    assert ws.numel() == max(size(t) for t in range(1, 4097))
+    assert dash.grad_stack_mx_workspace(2000, 256, 192, torch.bfloat16, device="cpu").numel() == size(2000)
+    assert dash.grad_stack_mx_workspace([1, 100], 256, 192, torch.bfloat16, device="cpu") is None
