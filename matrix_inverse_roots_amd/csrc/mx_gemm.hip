@@ -711,14 +711,16 @@ struct StatsArgs {
 
 // A <- beta A + (1 - beta) acc for the tile and its mirror, the arithmetic and the accesses of epilogue_split
 // (32 x 32 sub-blocks; on a diagonal tile those below the diagonal store nothing and those on it their
-// upper part and its mirror).  The old values of AHEAD sub-blocks are under way at a time (256-wide tiles,
-// B = 1024 1620 -> 1551 us).
+// upper part and its mirror).  A wave's old values are all under way before its first store (each sub-block's
+// loaded at its turn, 384 x 1024 1272 -> 1299 us in E4M3 and 918 -> 963 in E2M1).
 template <int TILE, bool EDGE>
 __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoord& tc, float* A,
                                                const f32x16 (&acc)[Shape<TILE>::MTM][Shape<TILE>::MTN], int wm, int wn,
                                                int lane, float* mlds) {
-  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, SUBS = MTM * MTN, AHEAD = SUBS < 4 ? SUBS : 4;
-  constexpr int NT = 2;  // non-temporal: A passes through once (256-wide tiles, B = 1024 1551 -> 1514 us)
+  constexpr int MTM = Shape<TILE>::MTM, MTN = Shape<TILE>::MTN, SUBS = MTM * MTN;
+  // non-temporal: A passes through once (cached, 384 x 1024 1272 -> 1306 us in E4M3 and 918 -> 963 in E2M1,
+  // 60 x 1600 716 -> 759 and 426 -> 486; but 20000 x 64 469 -> 267)
+  constexpr int NT = 2;
   const int B = a.g.B;
   const float al = a.g.epi.alpha, be = a.g.epi.delta;
   const uint64_t at = (uint64_t)(A + tc.b * (int64_t)B * B);  // (the same in every lane: say so)
@@ -738,7 +740,7 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
     return !(diag && row_of(t) > col_of(t)) &&
            (!EDGE || (tc.ti * TILE + row_of(t) < B && tc.tj * TILE + col_of(t) < B));
   };
-  float old[AHEAD][16];
+  float old[SUBS][16];
   auto load = [&](int t, float (&ev)[16]) {
     if (!kept(t)) return;
 #pragma unroll
@@ -749,7 +751,7 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
     }
   };
 #pragma unroll
-  for (int t = 0; t < AHEAD; ++t) load(t, old[t]);
+  for (int t = 0; t < SUBS; ++t) load(t, old[t]);
 #pragma unroll
   for (int t = 0; t < SUBS; ++t) {
     const int ib = row_of(t), jb = col_of(t);
@@ -759,7 +761,7 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
       float v[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        v[r] = al * acc[t / MTN][t % MTN][r] + be * old[t % AHEAD][r];
+        v[r] = al * acc[t / MTN][t % MTN][r] + be * old[t][r];
         if (!masked || 8 * (r >> 2) + (r & 3) + 4 * h <= li)
           __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v[r]), rs, vlane,
                                                 ((row0 + 8 * (r >> 2) + (r & 3)) * B + col0) * 4, NT);
@@ -785,7 +787,6 @@ __device__ __forceinline__ void stats_epilogue(const StatsArgs& a, const TileCoo
         }
       }
     }
-    if (t + AHEAD < SUBS) load(t + AHEAD, old[t % AHEAD]);
   }
 }
 
