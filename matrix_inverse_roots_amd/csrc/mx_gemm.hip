@@ -102,20 +102,29 @@ struct Elem<DASH_MX_E2M1> {
   }
 };
 
-// x = p[0] + p[1] + ... for 8 elements: each piece the nearest bfloat16 to what is left, every
-// difference exact in fp32 (see split3).  Two pieces hold binary16's 11 significant bits.  INF: an Inf, or
-// a magnitude that rounds to one, is its first piece alone; without it the second is Inf - Inf, NaN.
+// x = p[0] + p[1] + ... for the 8 elements lo[0..3], hi[0..3]: each piece the nearest bfloat16 to what is
+// left, every difference exact in fp32.  Three pieces hold fp32's bits (split3), two binary16's 11.
+// INF: an Inf, or a magnitude that rounds to one, is its first piece alone; without it the second is
+// Inf - Inf, NaN.
 template <int P, bool INF>
-__device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&p)[P]) {
+__device__ __forceinline__ void pieces(const f32x4& lo, const f32x4& hi, bf16x8 (&p)[P]) {
+  static_assert(P == 2 || P == 3, "binary16 or fp32");
+  if constexpr (P == 3) {
+    split3(lo, hi, p[0], p[1], p[2]);
+  } else {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float left = x[q];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const __bf16 a = (__bf16)left;
-      p[i][q] = a;
-      left = INF && i == 0 && fabsf((float)a) == __builtin_inff() ? 0.f : left - (float)a;
+    for (int q = 0; q < 8; ++q) {
+      const float x = q < 4 ? lo[q] : hi[q - 4];
+      p[0][q] = (__bf16)x;
+      p[1][q] = (__bf16)(x - (float)p[0][q]);
     }
+  }
+  if constexpr (INF) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (fabsf((float)p[0][q]) == __builtin_inff())
+#pragma unroll
+        for (int i = 1; i < P; ++i) p[i][q] = (__bf16)0.f;
   }
 }
 
@@ -430,10 +439,13 @@ struct FloatCol {
       if constexpr (PIECES == 1) {
         v[0] = __builtin_bit_cast(bf16x8, r[SLOT][i]);
       } else {
-        float x[8];
+        f32x4 lo, hi;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = (float)r[SLOT][i][q];
-        pieces<PIECES, INF>(x, v);
+        for (int q = 0; q < 4; ++q) {
+          lo[q] = (float)r[SLOT][i][q];
+          hi[q] = (float)r[SLOT][i][4 + q];
+        }
+        pieces<PIECES, INF>(lo, hi, v);
       }
 #pragma unroll
       for (int q = 0; q < PIECES; ++q) *(bf16x8*)&planes[q * TILE * BK + ks_at<TILE>(k + 16 * i, col)] = v[q];
