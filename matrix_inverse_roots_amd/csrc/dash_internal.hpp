@@ -352,6 +352,10 @@ hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxC
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Workgroups that one launch can hold: its threads are counted in 32 bits, and a larger grid runs its remainder
+// by 2^32 threads alone, without an error.
+inline int64_t most_workgroups(int threads) { return 0xffffffffLL / threads; }
+
 // dash_scale's argument checks short of the workspace (DASH_OK or the status dash_scale returns).
 dash_status scale_args_check(const float* A, int64_t N, int32_t B, dash_scaling how, dash_prec prec, int32_t k,
                              int32_t steps, const float* V0, const float* s);

@@ -118,6 +118,7 @@ struct QuantArgs {
   bool vec;
   int lanes;         // rows kernel: threads of a workgroup on one row (a power of two, 4 .. 256)
   int64_t col_wgs;   // and workgroups along a row
+  int64_t first_wg;  // of this launch
 };
 
 // Quantises the thread's 8 values of a group held by 4 neighbouring lanes; the scale byte in every one.
@@ -154,7 +155,7 @@ constexpr int ROWS_BACK = 2;
 // Rows only: 4 threads per group; rows of all matrices are one list.
 template <typename T, int F>
 __global__ __launch_bounds__(256) void mx_rows_kernel(QuantArgs a) {
-  const int64_t rb = blockIdx.x / a.col_wgs, cb = blockIdx.x - rb * a.col_wgs;
+  const int64_t wg = a.first_wg + blockIdx.x, rb = wg / a.col_wgs, cb = wg - rb * a.col_wgs;
   const int per = 256 / a.lanes;
   const int64_t first = rb * per * ROWS_IN<T> + threadIdx.x / a.lanes;
   const int64_t c0 = 8 * (cb * a.lanes + threadIdx.x % a.lanes);
@@ -187,7 +188,7 @@ __global__ __launch_bounds__(256) void mx_cols_kernel(QuantArgs a) {
   constexpr int GROUPS = QT / GROUP;
   __shared__ __attribute__((aligned(16))) float tile[QT * QT];
   const int64_t tr = (a.rows + QT - 1) / QT, tc = (a.cols + QT - 1) / QT;
-  const int64_t n = blockIdx.x / (tr * tc), t = blockIdx.x - n * (tr * tc);
+  const int64_t wg = a.first_wg + blockIdx.x, n = wg / (tr * tc), t = wg - n * (tr * tc);
   const int64_t r0 = t / tc * QT, c0 = t % tc * QT;
   const T* src = (const T*)a.src + n * a.rows * a.ld;
   const int64_t gc = (a.cols + GROUP - 1) / GROUP, gr = (a.rows + GROUP - 1) / GROUP;
@@ -248,7 +249,7 @@ struct DequantArgs {
   void* dst;
   bool vec;
   int lanes;
-  int64_t col_wgs;
+  int64_t col_wgs, first_wg;
 };
 
 // The values: element times 2^e in fp32 (ldexp is exact down to fp32's subnormals), the diagonal's own
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(256) void mx_values_kernel(DequantArgs a) {
   struct alignas(sizeof(raw4) * QUADS) Raw {
     raw4 q[QUADS];
   };
-  const int64_t rb = blockIdx.x / a.col_wgs, cb = blockIdx.x - rb * a.col_wgs;
+  const int64_t wg = a.first_wg + blockIdx.x, rb = wg / a.col_wgs, cb = wg - rb * a.col_wgs;
   const int per = 256 / a.lanes;
   const int64_t first = rb * per * ROWS_BACK + threadIdx.x / a.lanes;
   const int64_t c0 = EACH * (cb * a.lanes + threadIdx.x % a.lanes);
@@ -318,12 +319,22 @@ void row_split(int64_t chunks, int& lanes, int64_t& col_wgs) {
   col_wgs = (chunks + lanes - 1) / lanes;
 }
 
+// `grid` workgroups of 256 threads, in as many launches as they take (one, below 2^24)
+template <typename K, typename A>
+hipError_t launch_all(K kernel, int64_t grid, A& a, hipStream_t stream) {
+  const int64_t most = most_workgroups(256);
+  for (a.first_wg = 0; a.first_wg < grid; a.first_wg += most) {
+    const int64_t n = grid - a.first_wg < most ? grid - a.first_wg : most;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(256), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <typename K>
 hipError_t launch_cols(K kernel, int64_t side, QuantArgs& a, hipStream_t stream) {
-  const int64_t grid = a.N * ((a.rows + side - 1) / side) * ((a.cols + side - 1) / side);
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  return launch_all(kernel, a.N * ((a.rows + side - 1) / side) * ((a.cols + side - 1) / side), a, stream);
 }
 
 template <typename T, int F>
@@ -344,10 +355,7 @@ hipError_t quantize(QuantArgs& a, hipStream_t stream) {
   }
   row_split((a.cols + GROUP - 1) / GROUP * 4, a.lanes, a.col_wgs);
   const int per = 256 / a.lanes * ROWS_IN<T>;
-  const int64_t grid = (a.N * a.rows + per - 1) / per * a.col_wgs;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_rows_kernel<T, F>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  return launch_all(mx_rows_kernel<T, F>, (a.N * a.rows + per - 1) / per * a.col_wgs, a, stream);
 }
 
 template <typename T, int F>
@@ -355,10 +363,7 @@ hipError_t dequantize(DequantArgs& a, hipStream_t stream) {
   constexpr int EACH = 16 / sizeof(T);
   row_split((a.cols + EACH - 1) / EACH, a.lanes, a.col_wgs);
   const int per = 256 / a.lanes * ROWS_BACK;
-  const int64_t grid = (a.N * a.rows + per - 1) / per * a.col_wgs;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_values_kernel<T, F>), dim3((unsigned)grid), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  return launch_all(mx_values_kernel<T, F>, (a.N * a.rows + per - 1) / per * a.col_wgs, a, stream);
 }
 
 bool row_aligned(const void* p, int64_t ld, size_t size) {
@@ -371,7 +376,7 @@ hipError_t launch_mx_quantize(const void* src, dash_prec type, int64_t N, int64_
                               dash_mx_fmt fmt, void* codes, void* scales, void* codes_t, void* scales_t, float* diag,
                               hipStream_t stream) {
   QuantArgs a{src, N, rows, cols, ld, (uint8_t*)codes, (uint8_t*)scales, (uint8_t*)codes_t, (uint8_t*)scales_t, diag,
-              row_aligned(src, ld, type == DASH_FP32 ? 4 : 2), 0, 0};
+              row_aligned(src, ld, type == DASH_FP32 ? 4 : 2), 0, 0, 0};
   const bool e4 = fmt == DASH_MX_E4M3;
   if (type == DASH_FP32)
     return e4 ? quantize<float, DASH_MX_E4M3>(a, stream) : quantize<float, DASH_MX_E2M1>(a, stream);
@@ -384,7 +389,7 @@ hipError_t launch_mx_dequantize(const void* codes, const void* scales, const flo
                                 int64_t cols, dash_mx_fmt fmt, dash_prec type, int64_t ld, void* dst,
                                 hipStream_t stream) {
   DequantArgs a{(const uint8_t*)codes, (const uint8_t*)scales, diag, N, rows, cols, ld, dst,
-                row_aligned(dst, ld, type == DASH_FP32 ? 4 : 2), 0, 0};
+                row_aligned(dst, ld, type == DASH_FP32 ? 4 : 2), 0, 0, 0};
   const bool e4 = fmt == DASH_MX_E4M3;
   if (type == DASH_FP32)
     return e4 ? dequantize<float, DASH_MX_E4M3>(a, stream) : dequantize<float, DASH_MX_E2M1>(a, stream);

@@ -968,7 +968,7 @@ hipError_t launch_stats(K kernel, StatsArgs& a, hipStream_t stream) {
   a.g.tdim = (a.g.B + TILE - 1) / TILE;
   a.g.tiles = a.g.tdim * (a.g.tdim + 1) / 2;
   const int64_t grid = 2 * a.g.N * a.g.tiles;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  if (grid > most_workgroups(2 * TILE)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   return hipGetLastError();
 }
@@ -1195,7 +1195,7 @@ hipError_t launch_apply_tile(ApplyArgs& a, const MxApply& p, hipStream_t stream)
   a.g.tdim = (p.B + TILE - 1) / TILE;
   a.g.tiles = a.g.tdim * a.g.tdim;
   const int64_t grid = p.N * a.g.tiles;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  if (grid > most_workgroups(2 * TILE)) return hipErrorInvalidConfiguration;
   a.q = p.xl;
   a.diag = p.xl_diag;
   a.x.p = p.G;
@@ -1430,12 +1430,12 @@ hipError_t launch_grad_one(GradArgs& a, const GradShape& g, hipStream_t stream) 
     a.gn = g.gn;
   }
   const int64_t grid = a.gm * a.gn * g.splits;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  if (grid > most_workgroups(2 * TILE)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((mx_grad_kernel<T, F, TILE>), dim3((unsigned)grid), dim3(2 * TILE), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
   const int64_t joins = (a.tr * a.B * (a.tc * a.B / 4) + 255) / 256;
-  if (joins > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  if (joins > most_workgroups(256)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(mx_grad_join_kernel, dim3((unsigned)joins), dim3(256), 0, stream, a, g.gm * TILE, g.gn * TILE);
   return hipGetLastError();
 }
@@ -1483,7 +1483,7 @@ hipError_t launch_mx_stats(const MxCodes& rows, const MxCodes& cols, int64_t NG,
 hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream) {
   if (p.B > APPLY_OWN_BOUNDS) {
     const int64_t grid = p.N * p.parts;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    if (grid > most_workgroups(256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(mx_bounds_kernel, dim3((unsigned)grid), dim3(256), 0, stream, p.G, p.xl.scales, p.xr.scales,
                        p.B, p.parts, p.amax_g, p.bytes);
     const hipError_t e = hipGetLastError();
