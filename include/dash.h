@@ -474,7 +474,8 @@ typedef enum { DASH_MX_E2M1 = 0, DASH_MX_E4M3 = 1 } dash_mx_fmt;
  *                      together read src once.
  *   diag: NULL, or (rows == cols, else DASH_ERR_SHAPE) [N, rows] receives the diagonals in fp32 and
  *         their codes are 0: a root's diagonal, far above the rest of its row, then neither sets its
- *         group's scale nor loses its own precision. */
+ *         group's scale nor loses its own precision.
+ * src and the outputs are different buffers. */
 dash_status dash_mx_quantize(const void* src, dash_prec type, int64_t N, int64_t rows, int64_t cols, int64_t ld,
                              dash_mx_fmt fmt, void* codes, void* scales, void* codes_t, void* scales_t, float* diag,
                              void* stream);

@@ -7,6 +7,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <utility>
 #include <vector>
 
@@ -79,6 +80,13 @@ dash_status stats_args_check(const float* G_stack, int64_t NG, int32_t B, float 
 bool valid_fmt(dash_mx_fmt f) { return f == DASH_MX_E2M1 || f == DASH_MX_E4M3; }
 bool plain_type(dash_prec t) { return t == DASH_FP32 || t == DASH_FP16 || t == DASH_BF16; }
 bool mx_codes_ok(const void* codes, const void* scales) { return codes && scales && aligned(codes, 16); }
+// no two of them equal (NULL apart)
+bool distinct(std::initializer_list<const void*> all) {
+  for (auto p = all.begin(); p != all.end(); ++p)
+    for (auto q = p + 1; q != all.end(); ++q)
+      if (*p && *p == *q) return false;
+  return true;
+}
 // sides of at most 2^31 - 1, and 2^44 elements in all (32 times the memory of one GPU, in bytes): no
 // offset or count overflows 64 bits
 constexpr int64_t MX_MAX_SIDE = 0x7fffffff;
@@ -1730,9 +1738,10 @@ dash_status dash_mx_quantize(const void* src, dash_prec type, int64_t N, int64_t
                              void* stream) {
   const dash_status st = mx_shape_check(type, N, rows, cols, ld, fmt);
   if (st != DASH_OK) return st;
-  if (!src || !aligned(src, type == DASH_FP32 ? 4 : 2) || src == codes || src == codes_t) return DASH_ERR_INVALID_ARG;
+  if (!src || !aligned(src, type == DASH_FP32 ? 4 : 2)) return DASH_ERR_INVALID_ARG;
   if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return DASH_ERR_INVALID_ARG;
-  if (!aligned(codes, 16) || !aligned(codes_t, 16) || (codes && codes == codes_t)) return DASH_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(codes_t, 16)) return DASH_ERR_INVALID_ARG;
+  if (!distinct({src, codes, scales, codes_t, scales_t, diag})) return DASH_ERR_INVALID_ARG;
   if (diag && !aligned(diag, 4)) return DASH_ERR_INVALID_ARG;
   if (diag && rows != cols) return DASH_ERR_SHAPE;
   TRY(launch_mx_quantize(src, type, N, rows, cols, ld, fmt, codes, scales, codes_t, scales_t, diag, as_stream(stream)));
@@ -1768,8 +1777,8 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
   if (!mx_codes_ok(XL, XL_scales) || !mx_codes_ok(XR, XR_scales) || !valid_fmt(fmt)) return DASH_ERR_INVALID_ARG;
   if (!G_stack || !U_stack || !aligned(G_stack, 16) || !aligned(U_stack, 16) || !valid_N(NG))
     return DASH_ERR_INVALID_ARG;
-  if (U_stack == G_stack || U_stack == XL || U_stack == XR || U_stack == XL_diag || U_stack == XR_diag)
-    return DASH_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)G_stack, XL, XL_scales, (const void*)XL_diag, XR, XR_scales, (const void*)XR_diag})
+    if (U_stack == p) return DASH_ERR_INVALID_ARG;
   if ((XL_diag && !aligned(XL_diag, 4)) || (XR_diag && !aligned(XR_diag, 4)))
     return DASH_ERR_INVALID_ARG;
   if (!valid_B(B)) return DASH_ERR_SHAPE;
@@ -1809,7 +1818,8 @@ dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, cons
   if (!valid_fmt(fmt) || accumulate < 0 || accumulate > 1) return DASH_ERR_INVALID_ARG;
   if (T > 0 && (!dY || !aligned(dY, type == DASH_FP32 ? 4 : 2) || !mx_codes_ok(codes, scales)))
     return DASH_ERR_INVALID_ARG;
-  if (!G_stack || !aligned(G_stack, 16) || G_stack == dY || G_stack == codes) return DASH_ERR_INVALID_ARG;
+  if (!G_stack || !aligned(G_stack, 16) || G_stack == dY || G_stack == codes || G_stack == scales)
+    return DASH_ERR_INVALID_ARG;
   if (!valid_B(B)) return DASH_ERR_SHAPE;
   const size_t need = mx_grad_workspace_bytes(T, out, in, type);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return DASH_ERR_WORKSPACE;
