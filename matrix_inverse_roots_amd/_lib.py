@@ -271,9 +271,11 @@ def _nbytes(t):
 
 
 def _prec_of(dtype):
-    """The dash_prec of a torch element type (None for others)."""
+    """The dash_prec of a torch element type."""
     _torch()
-    return _precs.get(dtype)
+    if dtype not in _precs:
+        raise ValueError("dtype must be torch.float32, torch.float16 or torch.bfloat16, got %s" % (dtype,))
+    return _precs[dtype]
 
 
 def _tiles(shapes, B):
@@ -610,6 +612,8 @@ def dash_apply_vec(X, g_pieces, P: int, B: int, u_pieces, stream=None):
 def mx_buffers(N: int, rows: int, cols: int, fmt: int, device="cuda"):
     """(codes, scales): uint8 tensors [N, rows, bytes of a row] and [N, rows, groups] for N microscaled
     matrices of rows x cols."""
+    if fmt not in (DASH_MX_E2M1, DASH_MX_E4M3):
+        raise ValueError("mx_buffers: fmt must be DASH_MX_E2M1 or DASH_MX_E4M3, got %s" % (fmt,))
     torch = _torch()
     g = -(-cols // 32)
     return (torch.empty((N, rows, g * (32 if fmt == DASH_MX_E4M3 else 16)), dtype=torch.uint8, device=device),
