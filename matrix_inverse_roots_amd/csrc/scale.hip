@@ -702,9 +702,14 @@ hipError_t launch_start_pool(uint64_t seed, int64_t n, float* V0, hipStream_t st
 }
 
 hipError_t launch_frobenius(const float* A, int64_t N, int B, float* s, hipStream_t stream) {
-  if (N > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(frobenius_kernel, dim3((unsigned)N), dim3(1024), 0, stream, A, B, s);
-  return hipGetLastError();
+  const int64_t most = most_workgroups(1024);
+  for (int64_t b = 0; b < N; b += most) {
+    const int64_t n = N - b < most ? N - b : most;
+    hipLaunchKernelGGL(frobenius_kernel, dim3((unsigned)n), dim3(1024), 0, stream, A + b * B * B, B, s + b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Ring depth for a k-loop of KT slices: the largest of 4, 2, 1 that divides KT and is <= max_depth.

@@ -79,13 +79,20 @@ __global__ __launch_bounds__(256) void vec_apply_kernel(const float* X, const fl
 hipError_t launch_vec_copy(float* v, int64_t len, float* pieces, int B, bool to_pieces, hipStream_t stream) {
   const int64_t total = (len + B - 1) / B * B;
   const int64_t n = to_pieces ? total : len;
-  const int64_t grid = (n + 255) / 256;
-  if (grid < 1 || grid > 0x7fffffffLL) return hipErrorInvalidValue;
-  if (to_pieces)
-    hipLaunchKernelGGL(vec_copy_kernel<true>, dim3((unsigned)grid), dim3(256), 0, stream, v, len, pieces, total);
-  else
-    hipLaunchKernelGGL(vec_copy_kernel<false>, dim3((unsigned)grid), dim3(256), 0, stream, v, len, pieces, total);
-  return hipGetLastError();
+  if (n < 1) return hipErrorInvalidValue;
+  const int64_t most = most_workgroups(256) * 256;  // elements of a launch
+  for (int64_t e0 = 0; e0 < n; e0 += most) {
+    const int64_t grid = ((n - e0 < most ? n - e0 : most) + 255) / 256;
+    if (to_pieces)
+      hipLaunchKernelGGL(vec_copy_kernel<true>, dim3((unsigned)grid), dim3(256), 0, stream, v + e0, len - e0,
+                         pieces + e0, total - e0);
+    else
+      hipLaunchKernelGGL(vec_copy_kernel<false>, dim3((unsigned)grid), dim3(256), 0, stream, v + e0, len - e0,
+                         pieces + e0, total - e0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_vec_stats(const float* g, int64_t P, int B, float beta, float* L, hipStream_t stream) {
