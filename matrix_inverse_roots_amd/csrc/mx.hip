@@ -341,9 +341,9 @@ template <typename T, int F>
 hipError_t quantize(QuantArgs& a, hipStream_t stream) {
   if (a.codes_t) {
     // 64-wide tiles, but 128-wide ones (whole lines written per column) for large stacks of fp32 that fill
-    // them.  Both measured (us, 64 / 128): 1777 x 1001 fp16 10 / 12, 60 x 320 x 320 8 / 13, 48 x 1024 x 1024
-    // 61 / 70, 96 x 1024 x 1024 128 / 114, 192 x 1024 x 1024 269 / 218, 4000 x 192 x 192 172 / 255, 20000 x 6437
-    // 316 / 283 (fp32 to E4M3); 16384 x 16384 bfloat16 328 / 372.
+    // them.  Both measured, rows and columns to E4M3, calls back to back (us, 64 / 128): 1777 x 1001 fp16 7.3 /
+    // 11.5; fp32 60 x 320 x 320 7.8 / 12.6, 48 x 1024 x 1024 58 / 62, 96 x 1024 x 1024 129 / 114, 192 x 1024 x
+    // 1024 270 / 218, 4000 x 192 x 192 174 / 255, 20000 x 6437 315 / 284; 16384 x 16384 bfloat16 325 / 373.
     if constexpr (sizeof(T) == 4) {
       const int64_t tiles = a.N * ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
       if (tiles >= 4096 && (double)tiles * (128 * 128) <= 1.1 * (double)a.N * (double)a.rows * (double)a.cols)
