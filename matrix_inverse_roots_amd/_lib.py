@@ -7,6 +7,7 @@ torch's current HIP stream on the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import sys
 
@@ -670,11 +671,15 @@ def dash_grad_stack_mx_workspace(T: int, out_features: int, in_features: int, ty
 
 def grad_stack_mx_workspace(T, out_features: int, in_features: int, dtype, device="cuda"):
     """A byte tensor of the size dash_grad_stack_mx_workspace reports for dY of torch type `dtype` (None
-    when no workspace is needed).  T: a token count, or several (a list, tuple or range) whose calls share
-    the workspace: a smaller count can need more than a larger one, so it holds the largest size of all."""
+    when no workspace is needed).  T: a token count, or several (any iterable) whose calls share the
+    workspace: a smaller count can need more than a larger one, so it holds the largest size of all."""
     torch = _torch()
-    n = max(dash_grad_stack_mx_workspace(t, out_features, in_features, _prec_of(dtype))
-            for t in ((T,) if hasattr(T, "__index__") else T))
+    try:
+        counts = [operator.index(T)]
+    except TypeError:
+        counts = [operator.index(t) for t in T]
+    prec = _prec_of(dtype)
+    n = max(dash_grad_stack_mx_workspace(t, out_features, in_features, prec) for t in counts)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 

@@ -1,4 +1,6 @@
 """Host-side tests of the update's and the gradient tiles' workspace sizes (no GPU): nothing is launched."""
+import numpy as np
+import pytest
 import torch
 
 import matrix_inverse_roots_amd as dash
@@ -31,14 +33,20 @@ def test_gradient_workspace_is_for_its_token_count():
     """The size can fall as T grows: a workspace for one T alone is refused by another that needs more, and one
     for several serves each."""
     size = lambda T: dash.dash_grad_stack_mx_workspace(T, 256, 192, dash.DASH_BF16)
-    assert size(2000) == 4032 * 1024 > size(4096) == 3648 * 1024 > size(100) == 0
-    call = lambda T, n: status(dash.dash_grad_stack_mx, P[0], P[1], P[2], E4, T, 256, 192, 64, P[3], type=dash.DASH_BF16,
-                               ws=Ws(P[8], n))
-    assert call(2000, size(4096)) == WS
+    make = lambda T: dash.grad_stack_mx_workspace(T, 256, 192, torch.bfloat16, device="cpu")
+    sizes = {T: size(T) for T in range(1, 4097)}
+    for T in range(1, 4096):
+        if sizes[T] > sizes[4096]:
+            assert status(dash.dash_grad_stack_mx, P[0], P[1], P[2], E4, T, 256, 192, 64, P[3], type=dash.DASH_BF16,
+                          ws=Ws(P[8], sizes[4096])) == WS
+            break
     counts = [100, 1024, 2000, 4096]
-    for T in (counts, tuple(counts), range(1, 4097)):
-        ws = dash.grad_stack_mx_workspace(T, 256, 192, torch.bfloat16, device="cpu")
-        assert ws.numel() >= max(size(t) for t in counts)
-    assert ws.numel() == max(size(t) for t in range(1, 4097))
-    assert dash.grad_stack_mx_workspace(2000, 256, 192, torch.bfloat16, device="cpu").numel() == size(2000)
-    assert dash.grad_stack_mx_workspace([1, 100], 256, 192, torch.bfloat16, device="cpu") is None
+    for T in (counts, tuple(counts), iter(counts), np.array(counts), torch.tensor(counts)):
+        assert make(T).numel() == max(sizes[t] for t in counts) > 0
+    assert make(range(1, 4097)).numel() == max(sizes.values())
+    for T in (4096, np.int64(4096), torch.tensor(4096)):
+        assert make(T).numel() == sizes[4096]
+    assert make([1, 2]) is None and make(1) is None
+    for T in ([], 1.5, [1.5]):
+        with pytest.raises((TypeError, ValueError)):
+            make(T)
