@@ -460,6 +460,9 @@ dash_status dash_apply_vec(const float* X, const float* g_pieces, int64_t P, int
  *               to a byte, the even one in the low half; DASH_MX_E4M3: 8 bits (sign, 4, 3; largest 448).
  * e is the least integer >= -127 with max|x| <= m 2^e, m the format's largest value, so nothing
  * saturates; x 2^-e is rounded to the nearest element value, ties to the even code.
+ * (A magnitude from 3.5 2^126 in E2M1, or 248 2^120 in E4M3, rounds to 2^128, one beyond fp32: its code is
+ * that value's, it reads back as Inf in fp32 and bfloat16, and statistics and gradient tiles that it
+ * enters may be Inf or NaN.)
  * A matrix of `rows` x `cols` is rows * ceil(cols / 32) * 32 (E4M3) or 16 (E2M1) bytes of codes, 16-byte
  * aligned, and rows * ceil(cols / 32) scale bytes, both row-major; a stack of matrices follows one
  * after the other. */

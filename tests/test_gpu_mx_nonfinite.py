@@ -168,3 +168,24 @@ def test_gradient_nan_groups(T, out, inp, B, fmt):
     if fmt == dash.DASH_MX_E4M3:
         bad[:, 70] = 1
     assert np.array_equal(np.isnan(G), ref.tiles(bad, B) != 0)
+
+
+@pytest.mark.parametrize("fmt,step", zip(FMTS, (3.5 * 2.0**126, 248 * 2.0**120)), ids=IDS)
+def test_magnitudes_that_round_beyond_fp32(fmt, step):
+    """From half a step below 2^128 up an element's value is 2^128: the definition's code, and Inf as a value."""
+    big = np.array([step, np.nextafter(np.float32(step), np.float32(0)), torch.finfo(torch.float32).max,
+                    torch.finfo(torch.bfloat16).min, -1.0], np.float32)
+    x = np.zeros((5, 40), np.float32)
+    x[:, 3] = big
+    x[:, 35] = 2.0  # (another group)
+    c, s = dash.mx_buffers(1, 5, 40, fmt, device=DEV)
+    dash.dash_mx_quantize(torch.from_numpy(x).to(DEV), 1, 5, 40, fmt, c, s)
+    code, byte = ref.quantize(x[None], fmt)
+    assert np.array_equal(mx.host(c).numpy(), ref.pack(code, fmt)) and np.array_equal(mx.host(s).numpy(), byte)
+    want = ref.values(ref.pack(code, fmt), byte, 40, fmt)[0]
+    assert want[0, 3] == 2.0**128 and want[1, 3] < 2.0**128
+    for dtype in (torch.float32, torch.bfloat16):
+        v = torch.empty((1, 5, 40), dtype=dtype, device=DEV)
+        dash.dash_mx_dequantize(c, s, 1, 5, 40, fmt, v)
+        with np.errstate(over="ignore"):
+            assert np.array_equal(f64(v)[0], want.astype(np.float32).astype(np.float64))
