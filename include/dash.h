@@ -523,10 +523,10 @@ dash_status dash_apply_mx(const void* XL, const void* XL_scales, const float* XL
  * codes/scales (the input quantised by rows in the forward pass), written as dash_stack would stack an
  * out x in weight: ceil(out/B) x ceil(in/B) tiles, the part of an edge tile outside the weight zero.
  * accumulate = 1 adds to the tiles that G_stack holds (earlier micro-batches; the padding keeps what it
- * holds), 0 overwrites them.  in, ldy at most 2^26.  dY enters exactly (fp32 magnitudes from 2^-100 to
- * 3.38e38; smaller ones lose low bits, those above 3.39e38 count as Inf), sums are fp32, an Inf or a NaN in
- * dY gives its row of W the infinities and NaN of those sums, and equal calls give equal bits.  T = 0 (dY,
- * codes and scales may be NULL): an empty sum.
+ * holds), 0 overwrites them.  in, ldy at most 2^26.  dY enters exactly (fp32 magnitudes below 2^-100 lose low
+ * bits), sums are fp32, an Inf or a NaN in dY gives its row of W the infinities and NaN of those sums
+ * (products beyond fp32 are Inf), and equal calls give equal bits.  T = 0 (dY, codes and scales may be NULL):
+ * an empty sum.
  * ws: dash_grad_stack_mx_workspace bytes (0 where the token axis is not split), 256-byte aligned.  The size
  * is that of one T: the split of the tokens is chosen by a measured cost, and a smaller T can need more
  * (out = 256, in = 192, bfloat16: 4032 KiB at T = 2000, 3648 KiB at 4096).  One workspace for calls of

@@ -103,13 +103,27 @@ struct Elem<DASH_MX_E2M1> {
 };
 
 // x = p[0] + p[1] + ... for the 8 elements lo[0..3], hi[0..3]: each piece the nearest bfloat16 to what is
-// left, every difference exact in fp32.  Three pieces hold fp32's bits (split3), two binary16's 11.
-// INF: an Inf, or a magnitude that rounds to one, is its first piece alone; without it the second is
-// Inf - Inf, NaN.
+// left, every difference exact in fp32.  Three pieces hold fp32's bits (split3), two binary16's 11.  An Inf, or
+// a magnitude that rounds to one, leaves Inf - Inf, NaN, in the second piece; and the products of two pieces
+// that differ in sign may overflow to infinities that do.
+// INF: pieces of one sign, cut off instead of rounded (8 bits each, so they hold x all the same), with an Inf
+// or a NaN in the first alone.  Their products' sum is finite, Inf or NaN where x's product is.
 template <int P, bool INF>
 __device__ __forceinline__ void pieces(const f32x4& lo, const f32x4& hi, bf16x8 (&p)[P]) {
   static_assert(P == 2 || P == 3, "binary16 or fp32");
-  if constexpr (P == 3) {
+  if constexpr (INF) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float left = q < 4 ? lo[q] : hi[q - 4];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const bool finite = fabsf(left) < __builtin_inff();
+        const float a = finite ? __builtin_bit_cast(float, __builtin_bit_cast(unsigned, left) & 0xffff0000u) : left;
+        p[i][q] = (__bf16)a;
+        left = finite ? left - a : 0.f;
+      }
+    }
+  } else if constexpr (P == 3) {
     split3(lo, hi, p[0], p[1], p[2]);
   } else {
 #pragma unroll
@@ -118,13 +132,6 @@ __device__ __forceinline__ void pieces(const f32x4& lo, const f32x4& hi, bf16x8 
       p[0][q] = (__bf16)x;
       p[1][q] = (__bf16)(x - (float)p[0][q]);
     }
-  }
-  if constexpr (INF) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (fabsf((float)p[0][q]) == __builtin_inff())
-#pragma unroll
-        for (int i = 1; i < P; ++i) p[i][q] = (__bf16)0.f;
   }
 }
 
@@ -1292,10 +1299,10 @@ __global__ __launch_bounds__(2 * TILE) void mx_grad_kernel(GradArgs a) {
   const int64_t whole = inside ? (k1 - k0) / BK : 0;
   multiply<TILE>(la, lb, slices, whole, stage0, stage1, wm, wn, lane, acc);
   if constexpr (Pieces<T>::N > 1) {
-    // An infinity in pieces has made its row NaN: a tile with a NaN is formed once more, slice by slice, with
-    // the infinities minded.  (Minded at once, 16384 x 2048 x 8192 took 6 % more in binary16 and 5 % in fp32;
-    // this test takes 2 % of 50000 x 520 x 264 in fp32 and under 1 % elsewhere, a call full of NaN 2.3 times as
-    // long.  The pipelined loop again in its place cost the first loop registers: 3 %.)
+    // Infinities among the pieces' products have left NaN: a tile with a NaN is formed once more, slice by
+    // slice, in pieces that mind them.  (Minded at once, 16384 x 2048 x 8192 took 6 % more in binary16 and 5 %
+    // in fp32; this test takes 2 % of 50000 x 520 x 264 in fp32 and up to 1.4 % elsewhere, a call full of NaN
+    // 2.3 times as long.  The pipelined loop again in its place cost the first loop registers: 3 %.)
     float sum[4] = {0.f, 0.f, 0.f, 0.f};  // NaN if an addend is (or from Inf - Inf)
 #pragma unroll
     for (int mt = 0; mt < MTM; ++mt)

@@ -1,5 +1,5 @@
-"""Infinities in dY, and magnitudes that its bfloat16 pieces cannot hold, give the infinities and NaN of the
-same sum in 64 bits."""
+"""Infinities in dY give the infinities and NaN of their sums, and its largest finite magnitudes their
+products, or Inf where those are beyond fp32."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ import dash_inputs as di
 import matrix_inverse_roots_amd as dash
 import mx_ref as ref
 import test_gpu_mx as mx
-from test_gpu_mx import DEV, FMTS, IDS, TYPES, f64
+from test_gpu_mx import DEV, FMTS, IDS, TYPES, U, f64
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -25,28 +25,34 @@ def test_inf_in_dy(T, out, inp, B, dtype, fmt):
     dY[20, 9] = INF
     dY[T - 1, out - 1] = -INF
     dY[3, 40], dY[4, 40] = INF, INF  # sums of two infinities: NaN where they differ in sign
+    # finite, in rows of their own: their products reach beyond fp32, and the parts of one may differ in sign
+    large = {61: torch.finfo(dtype).max}
     if dtype == torch.float32:
-        dY[5, 60] = 3.4e38  # above every bfloat16: counts as Inf
-    dY[6, 61] = torch.finfo(dtype).max if dtype != torch.float32 else 3.38e38  # the largest that does not
+        large.update({60: 3.4e38, 62: 2.0**126 * (1 + 0.75 * 2.0**-7)})
+    for i, x in large.items():
+        dY[6, i] = x
     G = f64(mx.grad(dY, q, s, fmt, T, out, inp, B)).reshape(-1, B, B)
-    # by rules: terms of the infinite elements alone decide the rows that hold one
+    # the infinite elements' terms alone decide the rows that hold one
     d = f64(dY)
-    d[np.abs(d) > 3.39e38] *= INF
     want = np.zeros((out, inp))
     with np.errstate(invalid="ignore"):
         for t, i in np.argwhere(np.isinf(d)):
             want[i] += d[t, i] * X[0][t]
+    rows = lambda keep: ref.tiles(np.repeat(np.isin(np.arange(out), keep)[:, None], inp, 1).astype(float), B) != 0
+    held, lone = rows(np.flatnonzero(np.isinf(d).any(0))), rows(list(large))
     want = ref.tiles(want, B)
-    row = np.zeros((out, inp))
-    row[np.isinf(d).any(0)] = 1
-    row = ref.tiles(row, B) != 0
-    assert np.array_equal(np.isnan(G[row]), np.isnan(want[row]))
-    inf = row & np.isinf(want)
+    assert np.array_equal(np.isnan(G[held]), np.isnan(want[held]))
+    inf = held & np.isinf(want)
     assert np.array_equal(G[inf], want[inf])
-    one = np.zeros((out, inp))
-    one[61] = 1
-    one = ref.tiles(one, B) != 0
-    big = ref.tiles(np.outer(np.eye(out)[61], d[6, 61] * X[0][6]), B)
-    over = one & (np.abs(big) > 3.5e38)
-    assert np.all(np.isfinite(G[~row & ~one]))
-    assert np.all(np.isfinite(G[one & (np.abs(big) < 3e38)])) and np.all(np.isinf(G[over]))
+    assert np.all(np.isfinite(G[~held & ~lone]))
+    # a large finite element: its product where fp32 holds it, else Inf of its sign
+    big = np.zeros((out, inp))
+    for i in large:
+        big[i] = d[6, i] * X[0][6]
+    big = ref.tiles(big, B)
+    assert np.all(np.isfinite(G[lone & (np.abs(big) < 3.3e38)]))
+    over = lone & (np.abs(big) > 3.5e38)
+    assert np.array_equal(G[over], np.sign(big[over]) * np.inf)
+    # and to fp32's sums of 3 T parts, joined in up to 260 (the row's other terms are below 2^-17 of these)
+    clear = lone & (np.abs(big) < 3.3e38) & (np.abs(big) > 1e6 * T * np.abs(X[0]).max())
+    assert np.all(np.abs(G[clear] - big[clear]) <= ((3 * T + 260) * U + 2.0**-17) * np.abs(big[clear]))
