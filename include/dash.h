@@ -95,6 +95,14 @@ typedef struct {
   int64_t len;
 } dash_vec;
 
+/* A gradient of any parameter (device memory): rows x cols elements of `type` (DASH_FP32, DASH_FP16 or
+ * DASH_BF16), element (r, c) at ptr + r * ld + c; a vector or a contiguous tensor is one row. */
+typedef struct {
+  void* ptr;
+  int64_t rows, cols, ld;
+  dash_prec type;
+} dash_tensor;
+
 /* Blockify: copy the B x B tiles of n weight gradients into G_stack, weight-major, then tile row,
  * then tile column ([PT] Metodologia, item 1: gradient blocks G_ij are stacked into an (N, B, B)
  * tensor so one batched call processes them all).
@@ -535,6 +543,66 @@ dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, cons
                                dash_mx_fmt fmt, int64_t T, int64_t out, int64_t in, int32_t B, int32_t accumulate,
                                float* G_stack, void* ws, size_t ws_bytes, void* stream);
 dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, dash_prec type, size_t* bytes);
+
+/* ---- A layer's norm, written as the microscaled rows that its weights' gradient reads ----
+ *
+ * Root-mean-square norm of T >= 0 rows of n (1 .. 2^26) elements, with the residual's addition:
+ *   h = x + res,   rstd = (sum_j h_j^2 / n + eps)^{-1/2},   y = h rstd gain,
+ * x, res, h and y of `type` (DASH_FP32, DASH_FP16 or DASH_BF16, aligned to their element), each with a row pitch
+ * (ldx, ldr, ldh, ldy) >= n of its own; rows that start on 16 bytes load fastest.
+ *   res:   [T, n] or NULL (h = x).       gain: [n] of gain_type, or NULL (1).
+ *   h:     NULL, or receives h; x or res itself (with its pitch) to replace it: the residual stream.
+ *   y:     NULL, or receives y.
+ *   codes, scales: both NULL, or receive y by rows as dash_mx_quantize would write it in `fmt` (what
+ *          dash_grad_stack_mx takes in the backward pass).
+ *   rstd:  NULL, or [T] in fp32, which dash_rmsnorm_backward takes.
+ * At least one output is given; apart from h they share no memory with the inputs or with each other.
+ * h enters the norm, and y its codes, in fp32 before they are rounded; the sum of squares is kept in 64 bits
+ * (no row of finite elements overflows it).  eps >= 0.  A row of zeros with eps = 0 has rstd = Inf and y = NaN;
+ * a NaN in a row makes its rstd and y NaN, an Inf rstd = 0, its own y NaN and the rest 0. */
+dash_status dash_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, dash_prec type, const void* gain,
+                         dash_prec gain_type, int64_t T, int64_t n, float eps, void* h, int64_t ldh, void* y,
+                         int64_t ldy, dash_mx_fmt fmt, void* codes, void* scales, float* rstd, void* stream);
+
+/* The gradient of dash_rmsnorm.  With xhat = h rstd, m = dy gain and c = sum_j m_j xhat_j / n of each row:
+ *   dx = dh + rstd (m - xhat c),   dgain (+)= sum over rows of dy xhat,
+ * dy the gradient of y, h and rstd as the forward call wrote them, dh (or NULL: 0) the gradient that reaches h
+ * on the residual's way; dx is the gradient of x and of res.  dy, h, dh and dx of `type`, pitches as above;
+ * dx may be dy or dh itself (with its pitch) and shares no memory with the rest.
+ *   dgain: NULL, or [n] in fp32; accumulate = 1 adds to what it holds, 0 overwrites it.  A 1-D gradient
+ *          (dash_stack_vec).  Equal calls give equal bits.
+ * Sums are fp32 (dgain's over the workgroups' shares 64 bits), dx is rounded once; where m is a multiple of
+ * xhat the terms of dx cancel and what is left is their rounding.  T = 0: empty sums (only dgain is used).
+ * ws: dash_rmsnorm_backward_workspace bytes, 256-byte aligned (NULL without dgain); the size for one T serves
+ * any smaller one. */
+dash_status dash_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                  int64_t lddh, dash_prec type, const void* gain, dash_prec gain_type,
+                                  const float* rstd, int64_t T, int64_t n, void* dx, int64_t lddx, float* dgain,
+                                  int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+dash_status dash_rmsnorm_backward_workspace(int64_t T, int64_t n, size_t* bytes);
+
+/* ---- The global gradient norm, and clipping ----
+ *
+ * norm[0] = (sum over the n >= 0 gradients of |g_i|^2)^{1/2} and, when norms is given, norms[i] = |g_i| (Frobenius
+ * norms; fp32, device memory).  grads [host]: descriptors of any types and shapes, each aligned to its element;
+ * ld >= cols; without elements (rows or cols 0) its norm is 0 and ptr may be NULL.  Sums are kept in 64 bits: the
+ * norm of finite elements is right unless it leaves fp32's range itself.  Equal calls give equal bits.  An Inf or
+ * NaN among the elements makes the norm Inf or NaN.  (Over several GPUs: the root of the sum of squared norms.)
+ * ws: dash_grad_norm_workspace bytes for these descriptors' sizes and types, 256-byte aligned. */
+dash_status dash_grad_norm(const dash_tensor* grads, int32_t n, float* norm, float* norms, void* ws, size_t ws_bytes,
+                           void* stream);
+dash_status dash_grad_norm_workspace(const dash_tensor* grads, int32_t n, size_t* bytes);
+
+/* g_i <- g_i min(1, max_norm / norm[0]) in place for the n >= 0 gradients, which share no memory (slices of one
+ * buffer with the same pitch may interleave).  max_norm >= 0.  The product is formed in fp32 and rounded once.
+ * norm[0] <= max_norm leaves the gradients unread; norm[0] = Inf makes finite elements 0 and the others NaN (any
+ * finite max_norm), norm[0] = NaN makes all NaN. */
+dash_status dash_grad_clip(const dash_tensor* grads, int32_t n, const float* norm, float max_norm, void* stream);
+
+/* dash_stack of clipped gradients: the tiles of g_i min(1, max_norm / norm[0]), the gradients left as they are.
+ * Arguments, tiles and errors as dash_stack, norm and max_norm as dash_grad_clip. */
+dash_status dash_stack_clip(const dash_mat* grads, int32_t n, int32_t B, const float* norm, float max_norm,
+                            float* G_stack, void* stream);
 
 /* Workspace bytes for an operation.  k_or_degree: the number of start vectors for
  * DASH_OP_SCALE (power iteration; Frobenius needs 0), ignored otherwise.  DASH_OP_STATS: 0, or

@@ -37,6 +37,11 @@ class DashVec(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("len", ctypes.c_int64)]
 
 
+class DashTensor(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
 _lib = None
 _torch_module = None
 _Tensor = ()  # torch.Tensor
@@ -113,6 +118,14 @@ def library() -> ctypes.CDLL:
             "dash_apply_mx": (st, [vp, vp, vp, vp, vp, vp, vp, i64, i32, st, vp, vp, sz, vp]),
             "dash_grad_stack_mx": (st, [vp, st, i64, vp, vp, st, i64, i64, i64, i32, i32, vp, vp, sz, vp]),
             "dash_grad_stack_mx_workspace": (st, [i64, i64, i64, st, ctypes.POINTER(sz)]),
+            "dash_rmsnorm": (st, [vp, i64, vp, i64, st, vp, st, i64, i64, f32, vp, i64, vp, i64, st, vp, vp, vp, vp]),
+            "dash_rmsnorm_backward": (st, [vp, i64, vp, i64, vp, i64, st, vp, st, vp, i64, i64, vp, i64, vp, i32, vp, sz,
+                                           vp]),
+            "dash_rmsnorm_backward_workspace": (st, [i64, i64, ctypes.POINTER(sz)]),
+            "dash_grad_norm": (st, [ctypes.POINTER(DashTensor), i32, vp, vp, vp, sz, vp]),
+            "dash_grad_norm_workspace": (st, [ctypes.POINTER(DashTensor), i32, ctypes.POINTER(sz)]),
+            "dash_grad_clip": (st, [ctypes.POINTER(DashTensor), i32, vp, f32, vp]),
+            "dash_stack_clip": (st, [ctypes.POINTER(DashMat), i32, i32, vp, f32, vp, vp]),
             "dash_workspace_size": (st, [st, i64, i32, st, i32, ctypes.POINTER(sz)]),
             "dash_solver_products": (i64, [st, i32, i32]),
             "dash_flops": (f64, [st, i64, i32, st, i32, i32]),
@@ -222,6 +235,16 @@ class _Args:
             raise ValueError("%s: %s has a row pitch of %d, not %d" % (self.call, name, pitch, ld))
         return t.data_ptr(), have, pitch
 
+    def vector(self, t, name, n, type):
+        """(pointer, dash_prec type) of a contiguous vector of at least n elements of float32, float16 or
+        bfloat16; a raw pointer takes type."""
+        if t is None or t.__class__ is int or not self._tensor(t, name):
+            return t if t is None or isinstance(t, int) else t.data_ptr(), DASH_FP32 if type is None else type
+        have = _precs.get(t.dtype)
+        if have is None or type not in (None, have):
+            raise ValueError("%s: %s must be float32, float16 or bfloat16, got %s" % (self.call, name, t.dtype))
+        return self.ptr(t, name, None, n), have
+
     def codes(self, codes, scales, name, N, rows, cols, fmt):
         """Pointers of the codes and scale bytes of N microscaled matrices of rows x cols."""
         n = N * rows * -(-cols // 32)
@@ -241,6 +264,36 @@ class _Args:
             arr[i].len = t.shape[0]
         return arr
 
+    def tensors(self, ts, name):
+        """dash_tensor descriptors of GPU gradients: contiguous ones of any shape, or matrices with unit column
+        stride, of float32, float16 or bfloat16; a GradList's own."""
+        if isinstance(ts, GradList):
+            if ts.index is not None:
+                if self.index not in (-1, ts.index):
+                    raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, ts.device,
+                                                                                          self.device))
+                self.device, self.index = ts.device, ts.index
+            return ts.array
+        arr = (DashTensor * len(ts))()
+        for i, t in enumerate(ts):
+            if not self._tensor(t, "%s[%d]" % (name, i)):
+                raise ValueError("%s: %s[%d] must be a tensor" % (self.call, name, i))
+            have = _precs.get(t.dtype)
+            if have is None:
+                raise ValueError("%s: %s[%d] must be float32, float16 or bfloat16, got %s" % (self.call, name, i, t.dtype))
+            if t.is_contiguous():
+                rows, cols = 1, t.numel()
+                ld = cols
+            elif t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and (t.shape[0] == 1 or
+                                                                              t.stride(0) >= t.shape[1]):
+                rows, cols = t.shape
+                ld = t.stride(0) if rows > 1 else cols
+            else:
+                raise ValueError("%s: %s[%d] must be contiguous, or a matrix with unit column stride"
+                                 % (self.call, name, i))
+            arr[i] = (t.data_ptr(), rows, cols, ld, have)
+        return arr
+
     def stream(self, stream):
         if stream is not None:
             return stream if isinstance(stream, int) else stream.cuda_stream
@@ -258,6 +311,29 @@ class _Args:
                 status = fn(*args)
         if status != DASH_OK:
             raise DashError(self.call, status)
+
+
+class GradList:
+    """The gradients of a model, described once for many calls (dash_grad_norm, dash_grad_clip, dash_stack_clip).
+    It holds the tensors themselves, so what it describes stays where it is; a gradient that gets another
+    tensor needs a new list."""
+
+    __slots__ = ("tensors", "array", "device", "index", "_mats")
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        a = _Args("grad_list")
+        self.array = a.tensors(self.tensors, "tensors")
+        self.device, self.index = a.device, a.index if a.device is not None else None
+        self._mats = None
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def mats(self, call):
+        if self._mats is None:
+            self._mats = _Args(call).mats(self.tensors, "grads")
+        return self._mats
 
 
 def _check(name, status):
@@ -693,3 +769,95 @@ def dash_grad_stack_mx(dY, codes, scales, fmt: int, T: int, out_features: int, i
     n = _tiles([(out_features, in_features)], B) * B * B
     a.run(library().dash_grad_stack_mx, p, prec, pitch, *c, fmt, T, out_features, in_features, B, int(bool(accumulate)),
           a.ptr(G_stack, "G_stack", numel=n), a.ws(ws), _nbytes(ws), a.stream(stream))
+
+
+def dash_rmsnorm(x, T: int, n: int, eps: float, res=None, gain=None, h=None, y=None, fmt: int = DASH_MX_E4M3, codes=None,
+                 scales=None, rstd=None, type=None, gain_type=None, ldx=None, ldr=None, ldh=None, ldy=None, stream=None):
+    """x, res, h and y: tensors [T, n]; their element type and row pitches are taken from them (raw pointers
+    take type and the pitches), gain's from it."""
+    a = _Args("dash_rmsnorm")
+    px, prec, pitch = a.rows(x, "x", 1, T, n, type, ldx)
+    pr, _, pitch_r = a.rows(res, "res", 1, T, n, prec, ldr)
+    pg, gprec = a.vector(gain, "gain", n, gain_type)
+    ph, _, pitch_h = a.rows(h, "h", 1, T, n, prec, ldh)
+    py, _, pitch_y = a.rows(y, "y", 1, T, n, prec, ldy)
+    c = a.codes(codes, scales, "", 1, T, n, fmt)
+    a.run(library().dash_rmsnorm, px, pitch, pr, pitch_r, prec, pg, gprec, T, n, eps, ph, pitch_h, py, pitch_y, fmt, *c,
+          a.ptr(rstd, "rstd", numel=T), a.stream(stream))
+
+
+def dash_rmsnorm_backward_workspace(T: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("dash_rmsnorm_backward_workspace", library().dash_rmsnorm_backward_workspace(T, n, ctypes.byref(out)))
+    return out.value
+
+
+def rmsnorm_backward_workspace(T: int, n: int, device="cuda"):
+    """A byte tensor of the size dash_rmsnorm_backward_workspace reports (None when no workspace is needed); it
+    serves calls of fewer rows too."""
+    torch = _torch()
+    size = dash_rmsnorm_backward_workspace(T, n)
+    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+
+def dash_rmsnorm_backward(dy, h, rstd, T: int, n: int, dx, gain=None, dh=None, dgain=None, accumulate: bool = False,
+                          type=None, gain_type=None, lddy=None, ldh=None, lddh=None, lddx=None, ws=None, stream=None):
+    """dy, h, dh and dx: tensors [T, n], as dash_rmsnorm's."""
+    a = _Args("dash_rmsnorm_backward")
+    py, prec, pitch_y = a.rows(dy, "dy", 1, T, n, type, lddy)
+    ph, _, pitch_h = a.rows(h, "h", 1, T, n, prec, ldh)
+    pd, _, pitch_d = a.rows(dh, "dh", 1, T, n, prec, lddh)
+    px, _, pitch_x = a.rows(dx, "dx", 1, T, n, prec, lddx)
+    pg, gprec = a.vector(gain, "gain", n, gain_type)
+    a.run(library().dash_rmsnorm_backward, py, pitch_y, ph, pitch_h, pd, pitch_d, prec, pg, gprec,
+          a.ptr(rstd, "rstd", numel=T), T, n, px, pitch_x, a.ptr(dgain, "dgain", numel=n), int(bool(accumulate)),
+          a.ws(ws), _nbytes(ws), a.stream(stream))
+
+
+def grad_list(tensors) -> GradList:
+    """Describes gradients (contiguous tensors of any shape, or matrices with unit column stride; float32, float16
+    or bfloat16) once, for a program whose gradients keep their buffers from step to step."""
+    return GradList(tensors)
+
+
+def dash_grad_norm_workspace(grads) -> int:
+    out = ctypes.c_size_t(0)
+    _check("dash_grad_norm_workspace",
+           library().dash_grad_norm_workspace(_Args("dash_grad_norm_workspace").tensors(grads, "grads"), len(grads),
+                                              ctypes.byref(out)))
+    return out.value
+
+
+def grad_norm_workspace(grads, device="cuda"):
+    """A byte tensor of the size dash_grad_norm_workspace reports for these gradients (None for none)."""
+    torch = _torch()
+    size = dash_grad_norm_workspace(grads)
+    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+
+def dash_grad_norm(grads, norm, norms=None, ws=None, stream=None):
+    """grads: tensors, or a grad_list of them."""
+    a = _Args("dash_grad_norm")
+    arr = a.tensors(grads, "grads")
+    a.run(library().dash_grad_norm, arr, len(grads), a.ptr(norm, "norm", numel=1), a.ptr(norms, "norms", numel=len(grads)),
+          a.ws(ws), _nbytes(ws), a.stream(stream))
+
+
+def dash_grad_clip(grads, norm, max_norm: float, stream=None):
+    """grads: tensors, or a grad_list of them; norm: what dash_grad_norm wrote."""
+    a = _Args("dash_grad_clip")
+    arr = a.tensors(grads, "grads")
+    a.run(library().dash_grad_clip, arr, len(grads), a.ptr(norm, "norm", numel=1), max_norm, a.stream(stream))
+
+
+def dash_stack_clip(grads, B: int, norm, max_norm: float, G_stack, stream=None):
+    """grads: matrices as dash_stack's, or a grad_list of them."""
+    a = _Args("dash_stack_clip")
+    if isinstance(grads, GradList):
+        a.tensors(grads, "grads")  # (the call's device)
+        arr, shapes = grads.mats(a.call), [t.shape for t in grads.tensors]
+    else:
+        arr, shapes = a.mats(grads, "grads"), [t.shape for t in grads]
+    n = _tiles(shapes, B) * B * B
+    a.run(library().dash_stack_clip, arr, len(grads), B, a.ptr(norm, "norm", numel=1), max_norm,
+          a.ptr(G_stack, "G_stack", numel=n), a.stream(stream))

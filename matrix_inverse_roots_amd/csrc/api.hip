@@ -5,9 +5,12 @@
 // workspace, and per-block scalars derived from s stay on the device (coefficient table).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <memory>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -105,6 +108,91 @@ dash_status grad_shape_check(int64_t T, int64_t out, int64_t in, int64_t ldy, da
     return DASH_ERR_SHAPE;
   const double most = (double)(T > out ? T : out) * (double)(ldy > in ? ldy : in);
   return most > MX_MAX_ELEMENTS ? DASH_ERR_SHAPE : DASH_OK;
+}
+// A matrix in memory: rows of `width` bytes, `pitch` bytes apart
+struct Region {
+  const void* p;
+  int64_t rows, width, pitch;
+};
+Region region(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t size) {
+  return {p, rows, cols * (int64_t)size, ld * (int64_t)size};
+}
+Region region(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// Whether two matrices have a byte in common: exact where their pitches are the same (columns of one buffer) or
+// one of them is a single row of bytes, else by their ends.
+bool overlap(const Region& a, const Region& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  if ((uintptr_t)a.p > (uintptr_t)b.p) return overlap(b, a);
+  const uint64_t gap = (uintptr_t)b.p - (uintptr_t)a.p;
+  if (gap >= (uint64_t)((a.rows - 1) * a.pitch + a.width)) return false;
+  if (a.rows > 1 && (b.rows == 1 || a.pitch == b.pitch)) {
+    const uint64_t at = gap % (uint64_t)a.pitch;  // b's first byte after the start of a row of a
+    const uint64_t row = gap / (uint64_t)a.pitch;
+    if (at < (uint64_t)a.width) return true;
+    return at + (uint64_t)b.width > (uint64_t)a.pitch && row + 1 < (uint64_t)a.rows;
+  }
+  return true;
+}
+bool apart(const Region& out, std::initializer_list<Region> others) {
+  for (const Region& r : others)
+    if (overlap(out, r)) return false;
+  return true;
+}
+// the same matrix: an output that takes an input's place
+bool in_place(const Region& a, const Region& b) {
+  return a.p == b.p && (a.pitch == b.pitch || a.rows <= 1) && a.p;
+}
+// rows of at most 2^26 elements
+constexpr int64_t NORM_MAX_ROW = (int64_t)1 << 26;
+dash_status norm_shape_check(dash_prec type, const void* gain, dash_prec gain_type, int64_t T, int64_t n,
+                             std::initializer_list<int64_t> pitches) {
+  if (!plain_type(type) || (gain && (!plain_type(gain_type) || !aligned(gain, elem_size(gain_type)))))
+    return DASH_ERR_INVALID_ARG;
+  if (T < 0 || T > MX_MAX_SIDE || n < 1 || n > NORM_MAX_ROW) return DASH_ERR_SHAPE;
+  for (int64_t ld : pitches)
+    if (ld < n || ld > MX_MAX_SIDE || (double)T * (double)ld > MX_MAX_ELEMENTS) return DASH_ERR_SHAPE;
+  return DASH_OK;
+}
+// gradients of any type: those without elements may have no address
+dash_status grads_check(const dash_tensor* g, int32_t n) {
+  if (n < 0 || (n > 0 && !g)) return DASH_ERR_INVALID_ARG;
+  double all = 0.;
+  for (int32_t i = 0; i < n; ++i) {
+    const dash_tensor& t = g[i];
+    if (!plain_type(t.type)) return DASH_ERR_INVALID_ARG;
+    if (t.rows < 0 || t.cols < 0 || t.ld < t.cols) return DASH_ERR_SHAPE;
+    if (t.rows == 0 || t.cols == 0) continue;
+    if (!t.ptr || !aligned(t.ptr, elem_size(t.type))) return DASH_ERR_INVALID_ARG;
+    const bool flat = t.rows == 1 || t.ld == t.cols;
+    if (!flat && (t.rows > MX_MAX_SIDE || t.ld > MX_MAX_SIDE)) return DASH_ERR_SHAPE;
+    all += (double)t.rows * (double)(t.rows == 1 ? t.cols : t.ld);
+    if (all > MX_MAX_ELEMENTS) return DASH_ERR_SHAPE;
+  }
+  return DASH_OK;
+}
+Region region(const dash_tensor& t) {
+  const size_t size = elem_size(t.type);
+  if (t.rows == 1 || t.ld == t.cols) return region(t.ptr, t.rows * t.cols * (int64_t)size);
+  return region(t.ptr, t.rows, t.cols, t.ld, size);
+}
+// No two tensors of a list share memory.  In order of their addresses, each against those that begin before it ends.
+dash_status grads_apart(const dash_tensor* g, int32_t n) {
+  std::unique_ptr<int32_t[]> at(new (std::nothrow) int32_t[n > 0 ? n : 1]);
+  if (!at) return DASH_ERR_DEVICE;
+  int32_t m = 0;
+  for (int32_t i = 0; i < n; ++i)
+    if (g[i].rows > 0 && g[i].cols > 0) at[m++] = i;
+  std::sort(at.get(), at.get() + m, [g](int32_t a, int32_t b) { return (uintptr_t)g[a].ptr < (uintptr_t)g[b].ptr; });
+  for (int32_t i = 0; i < m; ++i) {
+    const Region r = region(g[at[i]]);
+    const uintptr_t end = (uintptr_t)r.p + (uintptr_t)((r.rows - 1) * r.pitch + r.width);
+    for (int32_t j = i + 1; j < m && (uintptr_t)g[at[j]].ptr < end; ++j)
+      if (overlap(r, region(g[at[j]]))) return DASH_ERR_INVALID_ARG;
+  }
+  return DASH_OK;
+}
+dash_status clip_args_check(const float* norm, float max_norm) {
+  return !norm || !aligned(norm, 4) || !(max_norm >= 0.f) ? DASH_ERR_INVALID_ARG : DASH_OK;
 }
 // apply: the intermediate stack T = XL G, and for two-piece binary16 products the bounds of XL, G
 // and XR per block and T's per-wave maxima
@@ -1825,6 +1913,144 @@ dash_status dash_grad_stack_mx(const void* dY, dash_prec type, int64_t ldy, cons
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return DASH_ERR_WORKSPACE;
   TRY(launch_mx_grad(dY, type, ldy, mx_codes(codes, scales, T, in, fmt), fmt, T, out, in, B, accumulate != 0, G_stack, ws,
                      as_stream(stream)));
+  return DASH_OK;
+}
+
+// ------------------------------------------------------------------------------------------------
+// The norm with a microscaled output, its gradient, and clipping
+// ------------------------------------------------------------------------------------------------
+
+dash_status dash_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, dash_prec type, const void* gain,
+                         dash_prec gain_type, int64_t T, int64_t n, float eps, void* h, int64_t ldh, void* y,
+                         int64_t ldy, dash_mx_fmt fmt, void* codes, void* scales, float* rstd, void* stream) {
+  const dash_status st = norm_shape_check(type, gain, gain_type, T, n,
+                                          {ldx, res ? ldr : n, h ? ldh : n, y ? ldy : n});
+  if (st != DASH_OK) return st;
+  if (!(eps >= 0.f) || std::isinf(eps) || !valid_fmt(fmt)) return DASH_ERR_INVALID_ARG;
+  if (T == 0) return DASH_OK;  // (buffers without elements may have no address)
+  if (!codes != !scales || (!h && !y && !codes && !rstd)) return DASH_ERR_INVALID_ARG;
+  const size_t size = elem_size(type);
+  if (!x || !aligned(codes, 16) || !aligned(rstd, 4)) return DASH_ERR_INVALID_ARG;
+  for (const void* p : {x, res, (const void*)h, (const void*)y})
+    if (!aligned(p, size)) return DASH_ERR_INVALID_ARG;
+  const Region rx = region(x, T, n, ldx, size), rr = region(res, T, n, ldr, size), rh = region(h, T, n, ldh, size),
+               ry = region(y, T, n, ldy, size), rg = region(gain, n * (int64_t)elem_size(gain_type)),
+               rc = region(codes, T * mx_row_bytes(n, fmt)), rs = region(scales, T * mx_row_groups(n)),
+               rt = region(rstd, T * 4);
+  if (!(in_place(rh, rx) || apart(rh, {rx})) || !(in_place(rh, rr) || apart(rh, {rr})) ||
+      !apart(rh, {rg, ry, rc, rs, rt}) || !apart(ry, {rx, rr, rg, rc, rs, rt}) ||
+      !apart(rc, {rx, rr, rg, rs, rt}) || !apart(rs, {rx, rr, rg, rt}) || !apart(rt, {rx, rr, rg}))
+    return DASH_ERR_INVALID_ARG;
+  RmsNorm p;
+  p.T = T;
+  p.n = n;
+  p.eps = eps;
+  p.x = {const_cast<void*>(x), ldx};
+  p.res = {const_cast<void*>(res), ldr};
+  p.h = {h, ldh};
+  p.y = {y, ldy};
+  p.gain = gain;
+  p.gain_type = gain_type;
+  p.codes = (uint8_t*)codes;
+  p.scales = (uint8_t*)scales;
+  p.rstd = rstd;
+  TRY(launch_rmsnorm(p, type, fmt, as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_rmsnorm_backward_workspace(int64_t T, int64_t n, size_t* bytes) {
+  if (!bytes) return DASH_ERR_INVALID_ARG;
+  const dash_status st = norm_shape_check(DASH_FP32, nullptr, DASH_FP32, T, n, {n});
+  if (st != DASH_OK) return st;
+  *bytes = rmsnorm_back_workspace_bytes(T, n);
+  return DASH_OK;
+}
+
+dash_status dash_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                  int64_t lddh, dash_prec type, const void* gain, dash_prec gain_type,
+                                  const float* rstd, int64_t T, int64_t n, void* dx, int64_t lddx, float* dgain,
+                                  int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  const dash_status st = norm_shape_check(type, gain, gain_type, T, n, {lddy, ldh, dh ? lddh : n, lddx});
+  if (st != DASH_OK) return st;
+  if (accumulate < 0 || accumulate > 1 || !aligned(dgain, 4)) return DASH_ERR_INVALID_ARG;
+  if (T == 0) {  // an empty sum
+    if (dgain && !accumulate) TRY(launch_fill_f32(dgain, n, 0.f, as_stream(stream)));
+    return DASH_OK;
+  }
+  const size_t size = elem_size(type);
+  if (!dy || !h || !rstd || !dx || !aligned(rstd, 4)) return DASH_ERR_INVALID_ARG;
+  for (const void* p : {dy, h, dh, (const void*)dx})
+    if (!aligned(p, size)) return DASH_ERR_INVALID_ARG;
+  const size_t need = dgain ? rmsnorm_back_workspace_bytes(T, n) : 0;
+  const Region ry = region(dy, T, n, lddy, size), rh = region(h, T, n, ldh, size), rd = region(dh, T, n, lddh, size),
+               rx = region(dx, T, n, lddx, size), rg = region(gain, n * (int64_t)elem_size(gain_type)),
+               rt = region(rstd, T * 4), rs = region(dgain, n * 4);
+  if (!(in_place(rx, ry) || apart(rx, {ry})) || !(in_place(rx, rd) || apart(rx, {rd})) || !apart(rx, {rh, rg, rt, rs}) ||
+      !apart(rs, {ry, rh, rd, rg, rt}))
+    return DASH_ERR_INVALID_ARG;
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return DASH_ERR_WORKSPACE;
+  if (need && !apart(region(ws, (int64_t)need), {ry, rh, rd, rx, rg, rt, rs})) return DASH_ERR_WORKSPACE;
+  RmsNormBack p;
+  p.T = T;
+  p.n = n;
+  p.dy = {const_cast<void*>(dy), lddy};
+  p.h = {const_cast<void*>(h), ldh};
+  p.dh = {const_cast<void*>(dh), lddh};
+  p.dx = {dx, lddx};
+  p.gain = gain;
+  p.gain_type = gain_type;
+  p.rstd = rstd;
+  p.dgain = dgain;
+  p.accumulate = accumulate != 0;
+  TRY(launch_rmsnorm_back(p, type, ws, as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_grad_norm_workspace(const dash_tensor* grads, int32_t n, size_t* bytes) {
+  if (!bytes) return DASH_ERR_INVALID_ARG;
+  const dash_status st = grads_check(grads, n);
+  if (st != DASH_OK) return st;
+  *bytes = grad_norm_workspace_bytes(grads, n);
+  return DASH_OK;
+}
+
+dash_status dash_grad_norm(const dash_tensor* grads, int32_t n, float* norm, float* norms, void* ws, size_t ws_bytes,
+                           void* stream) {
+  const dash_status st = grads_check(grads, n);
+  if (st != DASH_OK) return st;
+  if (!norm || !aligned(norm, 4) || !aligned(norms, 4)) return DASH_ERR_INVALID_ARG;
+  const size_t need = grad_norm_workspace_bytes(grads, n);
+  const Region rn = region(norm, 4), rs = region(norms, (int64_t)n * 4), rw = region(ws, (int64_t)need);
+  if (overlap(rn, rs)) return DASH_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (!apart(region(grads[i]), {rn, rs})) return DASH_ERR_INVALID_ARG;
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need || !apart(rw, {rn, rs}))) return DASH_ERR_WORKSPACE;
+  for (int32_t i = 0; i < n; ++i)
+    if (overlap(rw, region(grads[i]))) return DASH_ERR_WORKSPACE;
+  TRY(launch_grad_norm(grads, n, norm, norms, ws, as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_grad_clip(const dash_tensor* grads, int32_t n, const float* norm, float max_norm, void* stream) {
+  dash_status st = grads_check(grads, n);
+  if (st == DASH_OK) st = clip_args_check(norm, max_norm);
+  if (st == DASH_OK) st = grads_apart(grads, n);
+  if (st != DASH_OK) return st;
+  for (int32_t i = 0; i < n; ++i)
+    if (overlap(region(grads[i]), region(norm, 4))) return DASH_ERR_INVALID_ARG;
+  TRY(launch_grad_clip(grads, n, norm, max_norm, as_stream(stream)));
+  return DASH_OK;
+}
+
+dash_status dash_stack_clip(const dash_mat* grads, int32_t n, int32_t B, const float* norm, float max_norm,
+                            float* G_stack, void* stream) {
+  int64_t tiles = 0;
+  dash_status st = check_mats(grads, n, B, &tiles);
+  if (st == DASH_OK) st = clip_args_check(norm, max_norm);
+  if (st != DASH_OK) return st;
+  if (!G_stack || !aligned(G_stack, 16)) return DASH_ERR_INVALID_ARG;
+  if (overlap(region(G_stack, tiles * B * B * 4), region(norm, 4))) return DASH_ERR_INVALID_ARG;
+  TRY(launch_tile_copy(grads, n, B, G_stack, true, as_stream(stream), norm, max_norm));
   return DASH_OK;
 }
 

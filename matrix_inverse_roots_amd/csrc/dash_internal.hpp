@@ -275,7 +275,9 @@ struct CopyGroup {
   int32_t tiles_c[COPY_GROUP];       // tile columns of weight i
   int32_t n;
 };
-hipError_t launch_tile_copy(const dash_mat* w, int n, int B, float* stack, bool to_stack, hipStream_t stream);
+// With a norm (to_stack): times min(1, most / norm), as launch_grad_clip.
+hipError_t launch_tile_copy(const dash_mat* w, int n, int B, float* stack, bool to_stack, hipStream_t stream,
+                            const float* norm = nullptr, float most = 0.f);
 
 // 1-D parameters (vec.hip): a vector's pieces of B (the last zero-padded) copied to or from a
 // contiguous run of pieces; the rank-one statistic update L_p <- beta L_p + (1 - beta) g_p g_p^T;
@@ -349,6 +351,39 @@ hipError_t launch_mx_apply(const MxApply& p, dash_mx_fmt fmt, hipStream_t stream
 size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in, dash_prec type);
 hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
                           int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream);
+
+// The norm with a microscaled output, and its gradient (norm.hip): T rows of n, every matrix with its own pitch.
+// gain: NULL, or [n] of gain_type.  h, y, codes and scales, rstd (outputs): NULL where not wanted.
+struct RowsOf {
+  void* p = nullptr;
+  int64_t ld = 0;
+};
+struct RmsNorm {
+  int64_t T, n;
+  float eps;
+  RowsOf x, res, h, y;
+  const void* gain;
+  dash_prec gain_type;
+  uint8_t *codes, *scales;
+  float* rstd;
+};
+hipError_t launch_rmsnorm(const RmsNorm& p, dash_prec type, dash_mx_fmt fmt, hipStream_t stream);
+struct RmsNormBack {
+  int64_t T, n;
+  RowsOf dy, h, dh, dx;
+  const void* gain;
+  dash_prec gain_type;
+  const float* rstd;
+  float* dgain;
+  bool accumulate;
+};
+size_t rmsnorm_back_workspace_bytes(int64_t T, int64_t n);
+hipError_t launch_rmsnorm_back(const RmsNormBack& p, dash_prec type, void* ws, hipStream_t stream);
+
+// Gradients of any type and pitch (grads.hip): norm (and norms[n]) from ws, and in-place clipping by it.
+size_t grad_norm_workspace_bytes(const dash_tensor* t, int n);
+hipError_t launch_grad_norm(const dash_tensor* t, int n, float* norm, float* norms, void* ws, hipStream_t stream);
+hipError_t launch_grad_clip(const dash_tensor* t, int n, const float* norm, float most, hipStream_t stream);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

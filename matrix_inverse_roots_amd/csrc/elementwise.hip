@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "dash_internal.hpp"
+#include "vectors.hpp"
 
 namespace dash {
 namespace {
@@ -259,8 +260,10 @@ __global__ void freeze_update_kernel(const float* monitor, int mon_stride, int c
 // element).
 constexpr int COPY_VEC = 4;
 
-template <bool TO_STACK>
-__global__ __launch_bounds__(256) void tile_copy_kernel(CopyGroup g, int B, float* stack) {
+// CLIP (to the stack): times min(1, most / norm), which the copy hides.
+template <bool TO_STACK, bool CLIP>
+__global__ __launch_bounds__(256) void tile_copy_kernel(CopyGroup g, int B, float* stack, const float* norm, float most) {
+  const float factor = CLIP ? clip_factor(norm, most) : 1.f;
   const int wg = blockIdx.x;
   int wi = 0;
   while (wi + 1 < g.n && wg >= g.wg_base[wi + 1]) ++wi;
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(256) void tile_copy_kernel(CopyGroup g, int B, floa
 #pragma unroll
     for (int i = 0; i < COPY_VEC; ++i) {
       const unsigned d = i * 256 + threadIdx.x;
-      if (q0 + d < total) __builtin_nontemporal_store(v[i], TO_STACK ? lin + d : (f32x4*)wp[i]);
+      if (q0 + d < total) __builtin_nontemporal_store(CLIP ? v[i] * factor : v[i], TO_STACK ? lin + d : (f32x4*)wp[i]);
     }
     return;
   }
@@ -322,7 +325,7 @@ __global__ __launch_bounds__(256) void tile_copy_kernel(CopyGroup g, int B, floa
     const unsigned d = i * 256 + threadIdx.x;
     if (q0 + d >= total) continue;
     if (TO_STACK) {
-      __builtin_nontemporal_store(v[i], lin + d);
+      __builtin_nontemporal_store(CLIP ? v[i] * factor : v[i], lin + d);
     } else if (in_rows[i] && col[i] + 3 < cols) {
       __builtin_nontemporal_store(v[i], (f32x4*)wp[i]);
     } else if (in_rows[i]) {
@@ -431,7 +434,8 @@ hipError_t launch_freeze_update(const float* monitor, int mon_stride, int col, i
   return hipGetLastError();
 }
 
-hipError_t launch_tile_copy(const dash_mat* w, int n, int B, float* stack, bool to_stack, hipStream_t stream) {
+hipError_t launch_tile_copy(const dash_mat* w, int n, int B, float* stack, bool to_stack, hipStream_t stream,
+                            const float* norm, float most) {
   const int64_t f4_per_wg = 256 * COPY_VEC;
   for (int i0 = 0; i0 < n; i0 += COPY_GROUP) {
     CopyGroup g{};
@@ -455,10 +459,15 @@ hipError_t launch_tile_copy(const dash_mat* w, int n, int B, float* stack, bool 
       g.wg_base[j + 1] = (int32_t)wgs;
     }
     if (wgs > 0) {
-      if (to_stack)
-        hipLaunchKernelGGL(tile_copy_kernel<true>, dim3((unsigned)wgs), dim3(256), 0, stream, g, B, stack);
+      if (to_stack && norm)
+        hipLaunchKernelGGL((tile_copy_kernel<true, true>), dim3((unsigned)wgs), dim3(256), 0, stream, g, B, stack, norm,
+                           most);
+      else if (to_stack)
+        hipLaunchKernelGGL((tile_copy_kernel<true, false>), dim3((unsigned)wgs), dim3(256), 0, stream, g, B, stack, norm,
+                           most);
       else
-        hipLaunchKernelGGL(tile_copy_kernel<false>, dim3((unsigned)wgs), dim3(256), 0, stream, g, B, stack);
+        hipLaunchKernelGGL((tile_copy_kernel<false, false>), dim3((unsigned)wgs), dim3(256), 0, stream, g, B, stack, norm,
+                           most);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;
     }

@@ -1,0 +1,580 @@
+// norm.hip -- the root-mean-square norm of a layer's input, written as the microscaled rows that
+// dash_grad_stack_mx reads, and its gradient.
+//
+//   h = x + res,  rstd = (sum h^2 / n + eps)^{-1/2},  y = h rstd gain          (a row of n elements)
+//   m = dy gain,  xhat = h rstd,  c = sum m xhat / n:
+//   dx = dh + rstd (m - xhat c),  dgain = sum over rows of dy xhat
+//
+// Both are a few operations per element: the bytes in and out over the memory bandwidth is their time.  A row
+// is read once and stays in the registers of the `lanes` threads that share it (K pieces of 16 bytes each)
+// until its sum is known; longer rows are read twice.  Neighbouring threads take neighbouring pieces, so that a
+// wave's access is one run and a group of 32 lies in neighbouring lanes.
+#include <hip/hip_runtime.h>
+
+#include "dash_internal.hpp"
+#include "mx_format.hpp"
+#include "vectors.hpp"
+
+namespace dash {
+namespace {
+
+struct NormArgs {
+  const void *x, *res, *gain;
+  void *h, *y;
+  uint8_t *codes, *scales;
+  float* rstd;
+  int64_t ldx, ldr, ldh, ldy;
+  int64_t T, n, first_wg;
+  double over_n, eps;
+  dash_prec gain_type;
+  int lanes;  // threads of a row (a power of two)
+};
+
+// Elements c .. c + E - 1 of the gain (1 where there is none), zero beyond n; n >= E
+template <int E>
+__device__ __forceinline__ void load_gain(const void* gain, dash_prec type, int64_t c, int64_t n, float* g) {
+  if (!gain) {
+#pragma unroll
+    for (int q = 0; q < E; ++q) g[q] = 1.f;
+  } else if (type == DASH_FP32) {
+#pragma unroll
+    for (int p = 0; p < E / 4; ++p) {
+      const vec_of<float> v = load_piece((const float*)gain, c + 4 * p, n);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) g[4 * p + q] = v[q];
+    }
+  } else {
+    const auto v = load_elements<E>((const uint16_t*)gain, c, n);
+#pragma unroll
+    for (int q = 0; q < E; ++q)
+      g[q] = type == DASH_BF16 ? (float)__builtin_bit_cast(__bf16, (uint16_t)v[q])
+                               : (float)__builtin_bit_cast(_Float16, (uint16_t)v[q]);
+  }
+}
+__device__ __forceinline__ float gain_at(const void* gain, dash_prec type, int64_t c) {
+  if (!gain) return 1.f;
+  if (type == DASH_FP32) return ((const float*)gain)[c];
+  return type == DASH_BF16 ? (float)((const __bf16*)gain)[c] : (float)((const _Float16*)gain)[c];
+}
+
+// The sum over the `lanes` threads of a row, the same bits in each.  Every thread of the workgroup calls it;
+// `shared` holds a value per wave.
+template <typename S>
+__device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
+  for (int o = 1; o < 64 && o < lanes; o *= 2) v += __shfl_xor(v, o, 64);
+  if (lanes > 64) {
+    const int wave = threadIdx.x >> 6, waves = lanes >> 6, first = wave & ~(waves - 1);
+    __syncthreads();  // (the last row's values have been read)
+    if ((threadIdx.x & 63) == 0) shared[wave] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < waves; ++i) v += shared[first + i];
+  }
+  return v;
+}
+
+// One piece of y as codes; the scale byte from the first lane of its group
+template <int F, int E>
+__device__ __forceinline__ void store_codes(const float* y, int64_t group0, int64_t c, uint8_t* codes, uint8_t* scales) {
+  unsigned top = 0;
+#pragma unroll
+  for (int q = 0; q < E; ++q) top = umax(top, mag_bits(y[q]));
+#pragma unroll
+  for (int o = 1; o < GROUP / E; o *= 2) top = umax(top, __shfl_xor(top, o, 64));
+  const unsigned byte = scale_byte<F>(top);
+  typedef typename Codes<F>::raw4 raw4;
+  struct alignas(sizeof(raw4) * (E / 4)) Raw {
+    raw4 q[E / 4];
+  } raw;
+#pragma unroll
+  for (int p = 0; p < E / 4; ++p) raw.q[p] = Codes<F>::encode4(y + 4 * p, byte);
+  *(Raw*)(codes + (group0 * GROUP + c) * Codes<F>::BITS / 8) = raw;
+  if (c % GROUP == 0) scales[group0 + c / GROUP] = (uint8_t)byte;
+}
+
+template <typename T, int F, int K, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void rmsnorm_kernel(NormArgs a) {
+  constexpr int E = EACH<T>;
+  __shared__ double shared[BLOCK / 64];
+  const int lane = threadIdx.x & (a.lanes - 1), per = BLOCK / a.lanes;
+  const int64_t row = (a.first_wg + blockIdx.x) * per + threadIdx.x / a.lanes;
+  const bool live = row < a.T;  // (the others go along to the barriers)
+  const int64_t groups = (a.n + GROUP - 1) / GROUP;
+  const T* x = (const T*)a.x + row * a.ldx;
+  const T* res = (const T*)a.res + row * a.ldr;
+  float h[K][E];
+  {
+    vec_of<T> vx[K], vr[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t c = (int64_t)E * (lane + k * a.lanes);
+      vx[k] = load_piece(x, c, live ? a.n : 0);
+      if (a.res) vr[k] = load_piece(res, c, live ? a.n : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int q = 0; q < E; ++q) h[k][q] = a.res ? (float)vx[k][q] + (float)vr[k][q] : (float)vx[k][q];
+  }
+  float g[K][E];
+  double s = 0.;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
+    s += sum_squares<E>(h[k]);
+  }
+  s = row_sum(s, a.lanes, shared);
+  if (!live) return;
+  const float rstd = (float)rsqrt(fma(s, a.over_n, a.eps));
+  if (a.rstd && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t c = (int64_t)E * (lane + k * a.lanes);
+    if (c >= groups * GROUP) break;  // (the lanes of a group together)
+    if (a.h) store_piece((T*)a.h + row * a.ldh, c, a.n, h[k]);
+    float y[E];
+#pragma unroll
+    for (int q = 0; q < E; ++q) y[q] = h[k][q] * rstd * g[k][q];
+    if (a.y) store_piece((T*)a.y + row * a.ldy, c, a.n, y);
+    if (a.codes) store_codes<F, E>(y, row * groups, c, a.codes, a.scales);
+  }
+}
+
+// Rows that the registers of a workgroup do not hold: x and res are read twice
+template <typename T, int F>
+__global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
+  constexpr int E = EACH<T>;
+  __shared__ double shared[16];
+  const int64_t row = a.first_wg + blockIdx.x;
+  const int64_t groups = (a.n + GROUP - 1) / GROUP;
+  const T* x = (const T*)a.x + row * a.ldx;
+  const T* res = (const T*)a.res + row * a.ldr;
+  double s = 0.;
+  for (int64_t c = (int64_t)E * threadIdx.x; c < a.n; c += E * 1024) {
+    const vec_of<T> vx = load_piece(x, c, a.n);
+    float h[E];
+#pragma unroll
+    for (int q = 0; q < E; ++q) h[q] = (float)vx[q];
+    if (a.res) {
+      const vec_of<T> vr = load_piece(res, c, a.n);
+#pragma unroll
+      for (int q = 0; q < E; ++q) h[q] += (float)vr[q];
+    }
+    s += sum_squares<E>(h);
+  }
+  s = row_sum(s, 1024, shared);
+  const float rstd = (float)rsqrt(fma(s, a.over_n, a.eps));
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  for (int64_t c = (int64_t)E * threadIdx.x; c < groups * GROUP; c += E * 1024) {
+    const vec_of<T> vx = load_piece(x, c, a.n);
+    float h[E], g[E], y[E];
+    load_gain<E>(a.gain, a.gain_type, c, a.n, g);
+#pragma unroll
+    for (int q = 0; q < E; ++q) h[q] = (float)vx[q];
+    if (a.res) {
+      const vec_of<T> vr = load_piece(res, c, a.n);
+#pragma unroll
+      for (int q = 0; q < E; ++q) h[q] += (float)vr[q];
+    }
+    if (a.h) store_piece((T*)a.h + row * a.ldh, c, a.n, h);
+#pragma unroll
+    for (int q = 0; q < E; ++q) y[q] = h[q] * rstd * g[q];
+    if (a.y) store_piece((T*)a.y + row * a.ldy, c, a.n, y);
+    if (a.codes) store_codes<F, E>(y, row * groups, c, a.codes, a.scales);
+  }
+}
+
+// Rows of fewer than 8 elements, which no 16-byte piece fits: a thread each
+constexpr int TINY = 8;
+template <typename T, int F>
+__global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
+  const int64_t row = (a.first_wg + blockIdx.x) * 256 + threadIdx.x;
+  if (row >= a.T) return;
+  const int n = (int)a.n;
+  float h[TINY], y[GROUP];
+  double s = 0.;
+#pragma unroll
+  for (int q = 0; q < TINY; ++q) {
+    h[q] = q < n ? (float)((const T*)a.x)[row * a.ldx + q] : 0.f;
+    if (a.res && q < n) h[q] += (float)((const T*)a.res)[row * a.ldr + q];
+    s = fma((double)h[q], (double)h[q], s);
+  }
+  const float rstd = (float)rsqrt(fma(s, a.over_n, a.eps));
+  if (a.rstd) a.rstd[row] = rstd;
+  unsigned top = 0;
+#pragma unroll
+  for (int q = 0; q < GROUP; ++q) {
+    y[q] = 0.f;
+    if (q < TINY && q < n) {
+      y[q] = h[q] * rstd * gain_at(a.gain, a.gain_type, q);
+      if (a.h) ((T*)a.h)[row * a.ldh + q] = (T)h[q];
+      if (a.y) ((T*)a.y)[row * a.ldy + q] = (T)y[q];
+    }
+    top = umax(top, mag_bits(y[q]));
+  }
+  if (!a.codes) return;
+  const unsigned byte = scale_byte<F>(top);
+  typedef typename Codes<F>::raw4 raw4;
+#pragma unroll
+  for (int p = 0; p < GROUP / 4; ++p) ((raw4*)a.codes)[row * (GROUP / 4) + p] = Codes<F>::encode4(y + 4 * p, byte);
+  a.scales[row] = (uint8_t)byte;
+}
+
+// `grid` workgroups, in as many launches as they take
+template <typename K, typename A>
+hipError_t launch_rows(K kernel, int64_t grid, int block, A& a, hipStream_t stream) {
+  const int64_t most = most_workgroups(block);
+  for (a.first_wg = 0; a.first_wg < grid; a.first_wg += most) {
+    const int64_t n = grid - a.first_wg < most ? grid - a.first_wg : most;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(block), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T, int F, int K>
+hipError_t rmsnorm_rows(NormArgs& a, hipStream_t stream) {
+  if (a.lanes > 256) {
+    const int per = 1024 / a.lanes;
+    return launch_rows(rmsnorm_kernel<T, F, K, 1024>, (a.T + per - 1) / per, 1024, a, stream);
+  }
+  const int per = 256 / a.lanes;
+  return launch_rows(rmsnorm_kernel<T, F, K, 256>, (a.T + per - 1) / per, 256, a, stream);
+}
+
+int64_t up_to_power_of_two(int64_t x) {
+  int64_t p = 1;
+  while (p < x) p *= 2;
+  return p;
+}
+
+template <typename T, int F>
+hipError_t rmsnorm(NormArgs& a, hipStream_t stream) {
+  constexpr int E = EACH<T>;
+  const int64_t pieces = (a.n + GROUP - 1) / GROUP * (GROUP / E);
+  if (a.n < TINY) return launch_rows(rmsnorm_tiny_kernel<T, F>, (a.T + 255) / 256, 256, a, stream);
+  if (pieces > 1024 * (32 / E)) return launch_rows(rmsnorm_long_kernel<T, F>, a.T, 1024, a, stream);
+  int k = a.T >= 512 ? 32 / E : 1;
+  while (k > 1 && pieces < 64 * k) k /= 2;
+  while (pieces > 1024 * k) k *= 2;
+  int64_t lanes = up_to_power_of_two((pieces + k - 1) / k);
+  a.lanes = (int)(lanes < GROUP / E ? GROUP / E : lanes);
+  switch (k) {
+    case 1: return rmsnorm_rows<T, F, 1>(a, stream);
+    case 2: return rmsnorm_rows<T, F, 2>(a, stream);
+    case 4: return rmsnorm_rows<T, F, 4>(a, stream);
+  }
+  if constexpr (E == 4) return rmsnorm_rows<T, F, 8>(a, stream);
+  return hipErrorInvalidValue;
+}
+
+// ------------------------------------------------------------------------------------------------
+// The gradient
+// ------------------------------------------------------------------------------------------------
+
+struct BackArgs {
+  const void *dy, *h, *dh, *gain;
+  const float* rstd;
+  void* dx;
+  float* dgain;  // a single workgroup's
+  float* part;   // or [workgroups, n]
+  int64_t lddy, ldh, lddh, lddx;
+  int64_t T, n, rows_wg;  // rows of a workgroup
+  float over_n;
+  dash_prec gain_type;
+  int lanes;
+  bool accumulate, sums;  // sums: dgain is wanted
+};
+
+constexpr int BACK_BLOCK = 512;
+
+// A workgroup's rows one after the other (several side by side where they are short); every thread keeps the
+// sums dy xhat of its columns in registers, and the workgroup stores one row of them at the end: equal calls
+// add in the same order.
+template <typename T, int K>
+__global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
+  constexpr int E = EACH<T>;
+  extern __shared__ __attribute__((aligned(16))) float columns[];
+  __shared__ float shared[BACK_BLOCK / 64];
+  const int lane = threadIdx.x & (a.lanes - 1), per = BACK_BLOCK / a.lanes, slot = threadIdx.x / a.lanes;
+  const int64_t begin = blockIdx.x * a.rows_wg, end = begin + a.rows_wg < a.T ? begin + a.rows_wg : a.T;
+  float g[K][E], dg[K][E];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
+#pragma unroll
+    for (int q = 0; q < E; ++q) dg[k][q] = 0.f;
+  }
+  for (int64_t r0 = begin; r0 < end; r0 += per) {
+    const int64_t row = r0 + slot;
+    const bool live = row < end;
+    const int64_t n = live ? a.n : 0;
+    vec_of<T> dy[K], h[K], dh[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t c = (int64_t)E * (lane + k * a.lanes);
+      dy[k] = load_piece((const T*)a.dy + row * a.lddy, c, n);
+      h[k] = load_piece((const T*)a.h + row * a.ldh, c, n);
+      if (a.dh) dh[k] = load_piece((const T*)a.dh + row * a.lddh, c, n);
+    }
+    const float rstd = live ? a.rstd[row] : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int q = 0; q < E; ++q) {
+        const float d = (float)dy[k][q], xhat = (float)h[k][q] * rstd;
+        dg[k][q] = fmaf(d, xhat, dg[k][q]);
+        dot = fmaf(d * g[k][q], xhat, dot);
+      }
+    const float mean = row_sum(dot, a.lanes, shared) * a.over_n;
+    if (!live) continue;  // (the workgroup's last rows: no barrier follows in the loop)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t c = (int64_t)E * (lane + k * a.lanes);
+      if (c >= a.n) break;
+      float dx[E];
+#pragma unroll
+      for (int q = 0; q < E; ++q) {
+        const float xhat = (float)h[k][q] * rstd;
+        dx[q] = rstd * fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]);
+        if (a.dh) dx[q] += (float)dh[k][q];
+      }
+      store_piece((T*)a.dx + row * a.lddx, c, a.n, dx);
+    }
+  }
+  if (!a.sums) return;
+  // the rows side by side, in order
+  for (int i = per - 1; i > 0; --i) {
+    __syncthreads();
+    if (slot == i)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int q = 0; q < E; ++q) columns[(k * E + q) * a.lanes + lane] = dg[k][q];
+    __syncthreads();
+    if (slot == i - 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int q = 0; q < E; ++q) dg[k][q] += columns[(k * E + q) * a.lanes + lane];
+  }
+  if (slot) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t c = (int64_t)E * (lane + k * a.lanes);
+#pragma unroll
+    for (int p = 0; p < E / 4; ++p) {
+      float* out = a.dgain ? a.dgain : a.part + blockIdx.x * a.n;
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = dg[k][4 * p + q];
+      if (a.dgain && a.accumulate) {
+        const vec_of<float> old = load_piece(out, c + 4 * p, a.n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += old[q];
+      }
+      store_piece(out, c + 4 * p, a.n, v);
+    }
+  }
+}
+
+// Rows that the registers of a workgroup do not hold: each is read twice, and the sums stay in the workgroup's
+// row of `part`
+template <typename T>
+__global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
+  constexpr int E = EACH<T>;
+  __shared__ float shared[16];
+  const int64_t begin = blockIdx.x * a.rows_wg, end = begin + a.rows_wg < a.T ? begin + a.rows_wg : a.T;
+  float* part = a.part + blockIdx.x * a.n;
+  for (int64_t row = begin; row < end; ++row) {
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const T* h = (const T*)a.h + row * a.ldh;
+    const float rstd = a.rstd[row];
+    float dot = 0.f;
+    for (int64_t c = (int64_t)E * threadIdx.x; c < a.n; c += E * 1024) {
+      const vec_of<T> vd = load_piece(dy, c, a.n), vh = load_piece(h, c, a.n);
+      float g[E];
+      load_gain<E>(a.gain, a.gain_type, c, a.n, g);
+#pragma unroll
+      for (int q = 0; q < E; ++q) dot = fmaf((float)vd[q] * g[q], (float)vh[q] * rstd, dot);
+    }
+    const float mean = row_sum(dot, 1024, shared) * a.over_n;
+    for (int64_t c = (int64_t)E * threadIdx.x; c < a.n; c += E * 1024) {
+      const vec_of<T> vd = load_piece(dy, c, a.n), vh = load_piece(h, c, a.n);
+      float g[E], dx[E];
+      load_gain<E>(a.gain, a.gain_type, c, a.n, g);
+#pragma unroll
+      for (int q = 0; q < E; ++q) dx[q] = rstd * fmaf(-((float)vh[q] * rstd), mean, (float)vd[q] * g[q]);
+      if (a.dh) {
+        const vec_of<T> vr = load_piece((const T*)a.dh + row * a.lddh, c, a.n);
+#pragma unroll
+        for (int q = 0; q < E; ++q) dx[q] += (float)vr[q];
+      }
+      store_piece((T*)a.dx + row * a.lddx, c, a.n, dx);
+      if (a.sums) {
+#pragma unroll
+        for (int p = 0; p < E / 4; ++p) {
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = (float)vd[4 * p + q] * ((float)vh[4 * p + q] * rstd);
+          if (row > begin) {
+            const vec_of<float> old = load_piece(part, c + 4 * p, a.n);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += old[q];
+          }
+          store_piece(part, c + 4 * p, a.n, v);
+        }
+      }
+    }
+  }
+}
+
+// Rows of fewer than 8 elements: a thread each, whose sums a workgroup joins in order
+template <typename T>
+__global__ __launch_bounds__(256) void rmsnorm_back_tiny_kernel(BackArgs a) {
+  __shared__ float sums[TINY][256];
+  const int n = (int)a.n;
+  const int64_t begin = blockIdx.x * a.rows_wg, end = begin + a.rows_wg < a.T ? begin + a.rows_wg : a.T;
+  float dg[TINY];
+#pragma unroll
+  for (int q = 0; q < TINY; ++q) dg[q] = 0.f;
+  for (int64_t row = begin + threadIdx.x; row < end; row += 256) {
+    const float rstd = a.rstd[row];
+    float m[TINY], xhat[TINY], dot = 0.f;
+#pragma unroll
+    for (int q = 0; q < TINY; ++q) {
+      const float d = q < n ? (float)((const T*)a.dy)[row * a.lddy + q] : 0.f;
+      xhat[q] = q < n ? (float)((const T*)a.h)[row * a.ldh + q] * rstd : 0.f;
+      m[q] = q < n ? d * gain_at(a.gain, a.gain_type, q) : 0.f;
+      dg[q] = fmaf(d, xhat[q], dg[q]);
+      dot = fmaf(m[q], xhat[q], dot);
+    }
+    const float mean = dot * a.over_n;
+#pragma unroll
+    for (int q = 0; q < TINY; ++q) {
+      if (q >= n) break;
+      float dx = rstd * fmaf(-xhat[q], mean, m[q]);
+      if (a.dh) dx += (float)((const T*)a.dh)[row * a.lddh + q];
+      ((T*)a.dx)[row * a.lddx + q] = (T)dx;
+    }
+  }
+  if (!a.sums) return;
+#pragma unroll
+  for (int q = 0; q < TINY; ++q) sums[q][threadIdx.x] = dg[q];
+  __syncthreads();
+  if ((int)threadIdx.x >= n) return;
+  double s = 0.;
+  for (int i = 0; i < 256; ++i) s += (double)sums[threadIdx.x][i];
+  a.part[blockIdx.x * a.n + threadIdx.x] = (float)s;
+}
+
+// dgain (+)= the sum of the workgroups' rows, in order.  32 columns x 32 threads, each a share of the rows.
+__global__ __launch_bounds__(1024) void rmsnorm_join_kernel(const float* part, int parts, int64_t n, float* dgain,
+                                                            bool accumulate) {
+  __shared__ double sums[32][33];
+  const int col = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  double s = 0.;
+  if (c < n)
+#pragma unroll 8
+    for (int p = share; p < parts; p += 32) s += (double)part[p * n + c];
+  sums[share][col] = s;
+  __syncthreads();
+  if (share || c >= n) return;
+#pragma unroll 8
+  for (int i = 1; i < 32; ++i) s += sums[i][col];
+  dgain[c] = (float)(accumulate ? s + (double)dgain[c] : s);
+}
+
+// How the rows are shared out, over at most MOST_PARTS workgroups
+constexpr int64_t MOST_PARTS = 512;
+struct BackPlan {
+  int k, lanes;  // 0: the kernels of long and of tiny rows
+  int64_t wgs, rows_wg;
+};
+BackPlan back_plan(int64_t T, int64_t n, int E) {
+  BackPlan p;
+  const int64_t pieces = (n + E - 1) / E;
+  const int most_k = 32 / E;
+  int64_t per = 1;
+  if (n < TINY || pieces > (int64_t)BACK_BLOCK * most_k) {
+    p.k = p.lanes = 0;
+    if (n < TINY) per = 256;
+  } else {
+    p.k = T >= 512 ? most_k : 1;
+    while (p.k > 1 && pieces < 64 * p.k) p.k /= 2;
+    while (pieces > (int64_t)BACK_BLOCK * p.k) p.k *= 2;
+    p.lanes = (int)up_to_power_of_two((pieces + p.k - 1) / p.k);
+    per = BACK_BLOCK / p.lanes;
+  }
+  p.rows_wg = (T + MOST_PARTS - 1) / MOST_PARTS;
+  p.rows_wg = (p.rows_wg + per - 1) / per * per;
+  p.wgs = (T + p.rows_wg - 1) / p.rows_wg;
+  return p;
+}
+
+template <typename T, int K>
+hipError_t back_rows(const BackArgs& a, const BackPlan& p, hipStream_t stream) {
+  const size_t lds = a.sums && p.lanes < BACK_BLOCK ? (size_t)p.lanes * K * EACH<T> * sizeof(float) : 0;
+  hipLaunchKernelGGL((rmsnorm_back_kernel<T, K>), dim3((unsigned)p.wgs), dim3(BACK_BLOCK), lds, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
+  const BackPlan p = back_plan(a.T, a.n, EACH<T>);
+  float* dgain = a.dgain;
+  a.lanes = p.lanes;
+  a.rows_wg = p.rows_wg;
+  a.part = (float*)ws;
+  const bool join = a.sums && (p.wgs > 1 || p.k == 0);
+  if (join) a.dgain = nullptr;
+  hipError_t e = hipErrorInvalidValue;
+  if (p.k == 0) {
+    if (a.n < TINY)
+      hipLaunchKernelGGL(rmsnorm_back_tiny_kernel<T>, dim3((unsigned)p.wgs), dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL(rmsnorm_back_long_kernel<T>, dim3((unsigned)p.wgs), dim3(1024), 0, stream, a);
+    e = hipGetLastError();
+  } else if (p.k == 1) {
+    e = back_rows<T, 1>(a, p, stream);
+  } else if (p.k == 2) {
+    e = back_rows<T, 2>(a, p, stream);
+  } else if (p.k == 4) {
+    e = back_rows<T, 4>(a, p, stream);
+  } else {
+    if constexpr (EACH<T> == 4) e = back_rows<T, 8>(a, p, stream);
+  }
+  if (e != hipSuccess || !join) return e;
+  hipLaunchKernelGGL(rmsnorm_join_kernel, dim3((unsigned)((a.n + 31) / 32)), dim3(1024), 0, stream, a.part, (int)p.wgs,
+                     a.n, dgain, a.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const RmsNorm& p, dash_prec type, dash_mx_fmt fmt, hipStream_t stream) {
+  NormArgs a{p.x.p, p.res.p, p.gain, p.h.p, p.y.p, p.codes, p.scales, p.rstd, p.x.ld, p.res.ld, p.h.ld, p.y.ld,
+             p.T, p.n, 0, 1.0 / (double)p.n, (double)p.eps, p.gain_type, 0};
+  const bool e4 = fmt == DASH_MX_E4M3;
+  if (type == DASH_FP32) return e4 ? rmsnorm<float, DASH_MX_E4M3>(a, stream) : rmsnorm<float, DASH_MX_E2M1>(a, stream);
+  if (type == DASH_BF16) return e4 ? rmsnorm<__bf16, DASH_MX_E4M3>(a, stream) : rmsnorm<__bf16, DASH_MX_E2M1>(a, stream);
+  return e4 ? rmsnorm<_Float16, DASH_MX_E4M3>(a, stream) : rmsnorm<_Float16, DASH_MX_E2M1>(a, stream);
+}
+
+// a row of partial sums for every workgroup that any smaller T may have
+size_t rmsnorm_back_workspace_bytes(int64_t T, int64_t n) {
+  return (size_t)(T < MOST_PARTS ? T : MOST_PARTS) * (size_t)n * sizeof(float);
+}
+
+hipError_t launch_rmsnorm_back(const RmsNormBack& p, dash_prec type, void* ws, hipStream_t stream) {
+  BackArgs a{p.dy.p, p.h.p, p.dh.p, p.gain, p.rstd, p.dx.p, p.dgain, nullptr, p.dy.ld, p.h.ld, p.dh.ld, p.dx.ld,
+             p.T, p.n, 0, 1.f / (float)p.n, p.gain_type, 0, p.accumulate, p.dgain != nullptr};
+  if (type == DASH_FP32) return back<float>(a, ws, stream);
+  if (type == DASH_BF16) return back<__bf16>(a, ws, stream);
+  return back<_Float16>(a, ws, stream);
+}
+
+}  // namespace dash

@@ -1,0 +1,109 @@
+// vectors.hpp -- 16-byte pieces of rows of fp32, binary16 or bfloat16 on the device.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+namespace dash {
+namespace {
+
+// 16 bytes of elements that start on any element: the hardware takes such loads and stores whole
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  typedef float type __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <>
+struct Vec<__bf16> {
+  typedef __bf16 type __attribute__((ext_vector_type(8), aligned(2)));
+};
+template <>
+struct Vec<_Float16> {
+  typedef _Float16 type __attribute__((ext_vector_type(8), aligned(2)));
+};
+template <typename T>
+using vec_of = typename Vec<T>::type;
+template <typename T>
+constexpr int EACH = 16 / (int)sizeof(T);
+
+// w >> (8 BYTES - bits): the last elements of w come first, zeros follow.  0 < bits < 8 BYTES.
+__device__ __forceinline__ uint64_t last_first(uint64_t w, int bits) { return w >> (64 - bits); }
+struct Bytes16 {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ Bytes16 last_first(Bytes16 w, int bits) {
+  const int by = 128 - bits;
+  if (by >= 64) return {w.hi >> (by - 64), 0};
+  return {(w.lo >> by) | (w.hi << (64 - by)), w.hi >> by};
+}
+
+// The N elements from c on of a row of n, zero beyond it: one load, where the row ends inside the piece of the
+// row's last N elements.  n >= N, or 0 (nothing is loaded).
+template <int N, typename T>
+__device__ __forceinline__ auto load_elements(const T* row, int64_t c, int64_t n) {
+  typedef T piece_t __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+  typedef std::conditional_t<N * sizeof(T) == 16, Bytes16, uint64_t> bytes_t;
+  piece_t v = {};
+  if (c < n) {
+    const int64_t at = c + N <= n ? c : n - N;
+    v = *(const piece_t*)(row + at);
+    if (at != c)
+      v = __builtin_bit_cast(piece_t, last_first(__builtin_bit_cast(bytes_t, v), (int)(n - c) * 8 * (int)sizeof(T)));
+  }
+  return v;
+}
+// Elements c .. c + EACH - 1 of a row of n, zero beyond it; n >= EACH, or 0
+template <typename T>
+__device__ __forceinline__ vec_of<T> load_piece(const T* row, int64_t c, int64_t n) {
+  return __builtin_bit_cast(vec_of<T>, load_elements<EACH<T>>(row, c, n));
+}
+// The same for a row of any length
+template <typename T>
+__device__ __forceinline__ vec_of<T> load_short(const T* row, int64_t c, int64_t n) {
+  if (n >= EACH<T>) return load_piece(row, c, n);
+  vec_of<T> v;
+#pragma unroll
+  for (int q = 0; q < EACH<T>; ++q) v[q] = c + q < n ? row[c + q] : (T)0.f;
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_piece(T* row, int64_t c, int64_t n, const float* x) {
+  if (c + EACH<T> <= n) {
+    vec_of<T> v;
+#pragma unroll
+    for (int q = 0; q < EACH<T>; ++q) v[q] = (T)x[q];
+    *(vec_of<T>*)(row + c) = v;
+  } else {
+#pragma unroll
+    for (int q = 0; q < EACH<T>; ++q)
+      if (c + q < n) row[c + q] = (T)x[q];
+  }
+}
+
+// x_0^2 + ... + x_{E-1}^2 in 64 bits.  Formed in 32 bits where neither the sum leaves their range nor a term
+// that matters falls below it (the sum is then off by at most E roundings of 2^-24 of it); else, a sum of
+// zeros too, term by term in 64.
+template <int E>
+__device__ __forceinline__ double sum_squares(const float* x) {
+  float s = x[0] * x[0];
+#pragma unroll
+  for (int q = 1; q < E; ++q) s = fmaf(x[q], x[q], s);
+  if (s >= 0x1p-96f && s <= 0x1p126f) return (double)s;
+  double d = 0.;
+#pragma unroll
+  for (int q = 0; q < E; ++q) d = fma((double)x[q], (double)x[q], d);
+  return d;
+}
+
+// The factor of a norm: 1 up to `most`, most / norm beyond it, NaN for a NaN
+__device__ __forceinline__ float clip_factor(const float* norm, float most) {
+  const float v = *norm;
+  return v <= most ? 1.f : most / v;
+}
+
+}  // namespace
+}  // namespace dash
