@@ -223,7 +223,12 @@ class _Args:
         have = _precs.get(t.dtype)
         if have is None or type not in (None, have):
             raise ValueError("%s: %s must be float32, float16 or bfloat16, got %s" % (self.call, name, t.dtype))
-        shape = tuple(t.shape)
+        shape = t.shape
+        if N == 1 and ld is None and shape == (rows, cols):  # (the usual matrix, by the shortest way)
+            pitch, step = t.stride()
+            if step == 1 and (pitch >= cols or rows == 1):
+                return t.data_ptr(), have, pitch if pitch >= cols else cols
+        shape = tuple(shape)
         if shape != (N, rows, cols) and (N != 1 or shape != (rows, cols)):
             raise ValueError("%s: %s must be [%d, %d, %d], got %s" % (self.call, name, N, rows, cols, shape))
         if t.numel() == 0:

@@ -15,72 +15,95 @@
 namespace dash {
 namespace {
 
-constexpr int GROUP_TENSORS = 80;
+constexpr int GROUP_TENSORS = 160;
 struct Tensors {
-  void* ptr[GROUP_TENSORS];
-  int64_t pieces[GROUP_TENSORS];  // of all rows
-  int64_t row_pieces[GROUP_TENSORS];
-  int64_t len[GROUP_TENSORS], ld[GROUP_TENSORS];  // elements of a row, and its pitch
-  int32_t wg_base[GROUP_TENSORS + 1];             // first workgroup
-  uint8_t type[GROUP_TENSORS];
-  int32_t n, first;  // `first`: number of the launch's first tensor
-  int64_t wg_first;  // and workgroup
+  uint64_t where[GROUP_TENSORS];     // address, and the type in the highest byte
+  uint64_t size[GROUP_TENSORS];      // elements; or those of a row, and its pitch in the high half
+  uint32_t rows[GROUP_TENSORS];      // 0: one run of elements
+  int32_t wg_base[GROUP_TENSORS];    // first workgroup
+  int32_t n, first;                  // `first`: number of the launch's first tensor
+  int64_t wg_first;                  // and workgroup
   int64_t per_wg;
 };
 static_assert(sizeof(Tensors) <= 4000, "kernel arguments hold 4 KiB");
 
-// The tensor of this workgroup
+// The tensor of this workgroup, the last whose first workgroup is not behind it: every lane looks at some
 __device__ __forceinline__ int find_tensor(const Tensors& g) {
-  int lo = 0, hi = g.n;  // wg_base[lo] <= workgroup < wg_base[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int)blockIdx.x >= g.wg_base[mid])
-      lo = mid;
-    else
-      hi = mid;
+  int below = 0;
+#pragma unroll
+  for (int i = 0; i < (GROUP_TENSORS + 63) / 64; ++i) {
+    const int t = i * 64 + (threadIdx.x & 63);
+    below += __popcll(__ballot(t < g.n && g.wg_base[t < GROUP_TENSORS ? t : 0] <= (int)blockIdx.x));
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(below - 1);
 }
 
-// Calls f(row pointer, column, row length) for every piece of this workgroup, DEPTH of them together
-template <typename T, int DEPTH, typename F>
-__device__ __forceinline__ void each_piece(const Tensors& g, int t, F f) {
+// One tensor in pieces of 16 bytes
+template <typename T>
+struct Pieces {
+  T* p;
+  int64_t len, pieces;  // elements of a row (or of all), pieces of all
+  uint32_t row_pieces, ld;
+  bool flat;
+  __device__ __forceinline__ Pieces(const Tensors& g, int t) {
+    constexpr int E = EACH<T>;
+    p = (T*)(g.where[t] & 0x00ffffffffffffffull);
+    const uint64_t size = g.size[t];
+    const uint32_t rows = g.rows[t];
+    flat = rows == 0;
+    len = flat ? (int64_t)size : (int64_t)(uint32_t)size;
+    ld = (uint32_t)(size >> 32);
+    row_pieces = (uint32_t)((len + E - 1) / E);
+    pieces = flat ? (len + E - 1) / E : (int64_t)rows * row_pieces;
+  }
+};
+
+// Calls f(row pointers, columns, row lengths) for DEPTH pieces at a time out of [first, first + most), every
+// `threads`-th from `thread` on; pieces that there are not have length 0
+template <int DEPTH, typename T, typename F>
+__device__ __forceinline__ void each_piece(const Pieces<T>& v, int64_t first, int64_t most, int thread, int threads,
+                                           F f) {
   constexpr int E = EACH<T>;
-  const int64_t first = (int64_t)((int)blockIdx.x - g.wg_base[t]) * g.per_wg;
-  const int64_t left = g.pieces[t] - first, mine = left < g.per_wg ? left : g.per_wg;
-  const int64_t row0 = first / g.row_pieces[t], at0 = first - row0 * g.row_pieces[t];
-  T* const p = (T*)g.ptr[t] + row0 * g.ld[t];
-  const bool flat = g.row_pieces[t] == g.pieces[t];  // (one row)
-  for (int64_t i = threadIdx.x; i < mine; i += 256 * DEPTH) {
+  const int64_t left = v.pieces - first, mine = left < most ? left : most;
+  T* p = v.p;
+  uint32_t at0 = 0;
+  if (v.flat) {
+    p += first * E;
+  } else {  // (a row has fewer than 2^31 pieces, a workgroup fewer than 2^30)
+    const int64_t row0 = first / v.row_pieces;
+    at0 = (uint32_t)(first - row0 * v.row_pieces);
+    p += row0 * (int64_t)v.ld;
+  }
+  for (int64_t i = thread; i < mine; i += (int64_t)threads * DEPTH) {
     T* row[DEPTH];
-    int64_t c[DEPTH];
-    bool in[DEPTH];
+    int64_t c[DEPTH], len[DEPTH];
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) {
-      const int64_t at = at0 + i + 256 * k;
-      in[k] = i + 256 * k < mine;
-      if (flat) {
-        row[k] = p;
-        c[k] = at * E;
-      } else {  // (at < 2^32: a row has fewer than 2^31 pieces, and so has a workgroup)
-        const unsigned r = (unsigned)at / (unsigned)g.row_pieces[t];
-        row[k] = p + r * g.ld[t];
-        c[k] = (int64_t)((unsigned)at - r * (unsigned)g.row_pieces[t]) * E;
+      const int64_t at = i + (int64_t)threads * k;
+      row[k] = p;
+      c[k] = at * E;
+      len[k] = v.flat ? v.len - first * E : v.len;
+      if (!v.flat) {
+        const uint32_t a = at0 + (uint32_t)at, r = a / v.row_pieces;
+        row[k] = p + (int64_t)r * v.ld;
+        c[k] = (int64_t)(a - r * v.row_pieces) * E;
       }
+      if (at >= mine) len[k] = 0;
     }
-    f(row, c, in, g.len[t]);
+    f(row, c, len);
   }
 }
 
 constexpr int DEPTH = 4;
 
 template <typename T>
-__device__ __forceinline__ double tensor_squares(const Tensors& g, int t) {
+__device__ __forceinline__ double squares(const Tensors& g, int t, int64_t first, int64_t most, int thread, int threads) {
   double s = 0.;
-  each_piece<T, DEPTH>(g, t, [&](T* const* row, const int64_t* c, const bool* in, int64_t len) {
+  each_piece<DEPTH>(Pieces<T>(g, t), first, most, thread, threads, [&](T* const* row, const int64_t* c,
+                                                                       const int64_t* len) {
     vec_of<T> v[DEPTH];
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) v[k] = load_short(row[k], c[k], in[k] ? len : 0);
+    for (int k = 0; k < DEPTH; ++k) v[k] = load_short(row[k], c[k], len[k]);
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) {
       float x[EACH<T>];
@@ -91,25 +114,45 @@ __device__ __forceinline__ double tensor_squares(const Tensors& g, int t) {
   });
   return s;
 }
+__device__ __forceinline__ double squares_of(const Tensors& g, int t, int64_t first, int64_t most, int thread, int threads) {
+  const int type = (int)(g.where[t] >> 56);
+  if (type == DASH_FP32) return squares<float>(g, t, first, most, thread, threads);
+  if (type == DASH_BF16) return squares<__bf16>(g, t, first, most, thread, threads);
+  return squares<_Float16>(g, t, first, most, thread, threads);
+}
+__device__ __forceinline__ double wave_sum(double s) {
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o, 64);
+  return s;
+}
 
 // part[w] = the sum of squares of workgroup w's pieces; base[t] = tensor t's first workgroup
 __global__ __launch_bounds__(256) void grad_squares_kernel(Tensors g, double* part, int64_t* base) {
-  const int t = find_tensor(g);
-  double s;
-  if (g.type[t] == DASH_FP32)
-    s = tensor_squares<float>(g, t);
-  else if (g.type[t] == DASH_BF16)
-    s = tensor_squares<__bf16>(g, t);
-  else
-    s = tensor_squares<_Float16>(g, t);
+  const int t = find_tensor(g), w = (int)blockIdx.x - g.wg_base[t];
+  const double s = wave_sum(squares_of(g, t, w * g.per_wg, g.per_wg, threadIdx.x, 256));
   __shared__ double waves[4];
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o, 64);
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x) return;
   part[g.wg_first + blockIdx.x] = (waves[0] + waves[1]) + (waves[2] + waves[3]);
-  if ((int)blockIdx.x == g.wg_base[t]) base[g.first + t] = g.wg_first + blockIdx.x;
+  if (w == 0) base[g.first + t] = g.wg_first + blockIdx.x;
+}
+
+// A few small tensors: a wave takes one after the other, and their norm is ready with this launch
+__global__ __launch_bounds__(1024) void grad_norm_small_kernel(Tensors g, float* norm, float* norms) {
+  __shared__ double waves[16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double all = 0.;
+  for (int t = wave; t < g.n; t += 16) {
+    const double s = wave_sum(squares_of(g, t, 0, INT64_MAX, lane, 64));
+    if (norms && lane == 0) norms[t] = (float)sqrt(s);
+    all += s;
+  }
+  if (lane == 0) waves[wave] = all;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 16; ++i) all += waves[i];
+  *norm = (float)sqrt(all);
 }
 
 // Workgroup 0: the norm of all; the others: each wave one tensor's
@@ -127,8 +170,7 @@ __global__ __launch_bounds__(1024) void grad_norm_kernel(const double* part, con
     const int64_t end = t + 1 < n ? base[t + 1] : parts;
     for (int64_t i = base[t] + lane; i < end; i += 64) s += part[i];
   }
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o, 64);
+  s = wave_sum(s);
   if (blockIdx.x) {
     if (lane == 0) norms[(int64_t)(blockIdx.x - 1) * 16 + wave] = (float)sqrt(s);
     return;
@@ -142,16 +184,18 @@ __global__ __launch_bounds__(1024) void grad_norm_kernel(const double* part, con
 
 template <typename T>
 __device__ __forceinline__ void clip_tensor(const Tensors& g, int t, float factor) {
-  each_piece<T, DEPTH>(g, t, [&](T* const* row, const int64_t* c, const bool* in, int64_t len) {
+  const int64_t first = (int64_t)((int)blockIdx.x - g.wg_base[t]) * g.per_wg;
+  each_piece<DEPTH>(Pieces<T>(g, t), first, g.per_wg, threadIdx.x, 256, [&](T* const* row, const int64_t* c,
+                                                                            const int64_t* len) {
     vec_of<T> v[DEPTH];
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) v[k] = load_short(row[k], c[k], in[k] ? len : 0);
+    for (int k = 0; k < DEPTH; ++k) v[k] = load_short(row[k], c[k], len[k]);
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) {
       float x[EACH<T>];
 #pragma unroll
       for (int q = 0; q < EACH<T>; ++q) x[q] = (float)v[k][q] * factor;
-      store_piece(row[k], c[k], in[k] ? len : 0, x);
+      store_piece(row[k], c[k], len[k], x);
     }
   });
 }
@@ -159,70 +203,75 @@ __device__ __forceinline__ void clip_tensor(const Tensors& g, int t, float facto
 __global__ __launch_bounds__(256) void grad_clip_kernel(Tensors g, const float* norm, float most) {
   const float factor = clip_factor(norm, most);
   if (factor == 1.f) return;  // (the gradients stay as they are)
-  const int t = find_tensor(g);
-  if (g.type[t] == DASH_FP32)
+  const int t = find_tensor(g), type = (int)(g.where[t] >> 56);
+  if (type == DASH_FP32)
     clip_tensor<float>(g, t, factor);
-  else if (g.type[t] == DASH_BF16)
+  else if (type == DASH_BF16)
     clip_tensor<__bf16>(g, t, factor);
   else
     clip_tensor<_Float16>(g, t, factor);
 }
 
-// A tensor as rows: one where nothing lies between them
-struct Rows {
-  int64_t rows, len, ld, row_pieces;
-  Rows(const dash_tensor& g) {
+// A tensor as the kernels take it: one run where nothing lies between its rows
+struct Shape {
+  int64_t rows, len;  // rows 0: one run
+  int64_t pieces;
+  Shape(const dash_tensor& g) {
     const int each = g.type == DASH_FP32 ? 4 : 8;
-    rows = g.rows;
-    len = g.cols;
-    ld = g.ld;
-    if (rows == 0 || len == 0) {
-      rows = 1;
-      len = 0;
-    } else if (ld == len || rows == 1) {
-      len *= rows;
-      rows = 1;
+    rows = 0;
+    len = g.rows * g.cols;
+    if (len && g.rows > 1 && g.ld != g.cols) {
+      rows = g.rows;
+      len = g.cols;
     }
-    row_pieces = (len + each - 1) / each;
-    if (row_pieces == 0) row_pieces = 1;  // (an empty tensor has a piece of no elements)
+    pieces = (len + each - 1) / each * (rows ? rows : 1);
   }
-  int64_t pieces() const { return rows * row_pieces; }
+  int64_t workgroups(int64_t per_wg) const { return pieces ? (pieces + per_wg - 1) / per_wg : 1; }
 };
 
-// Pieces of a workgroup: enough to hide the latency of its start (16 for each thread, 64 KiB a workgroup), more
-// where that would make over 16384 workgroups
-int64_t pieces_per_wg(const dash_tensor* g, int n) {
-  int64_t all = 0;
-  for (int i = 0; i < n; ++i) all += Rows(g[i]).pieces();
-  const int64_t least = 256 * 16;
-  const int64_t even = (all / 16384 + 256 * DEPTH - 1) / (256 * DEPTH) * (256 * DEPTH);
-  return even > least ? even : least;
+// How a list is shared out: pieces of a workgroup, and workgroups in all
+struct Share {
+  int64_t per_wg, wgs;
+  bool small;  // for grad_norm_small_kernel
+};
+constexpr int64_t SMALL_PIECES = 512;
+Share share_out(const dash_tensor* g, int n) {
+  int64_t all = 0, most = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t p = Shape(g[i]).pieces;
+    all += p;
+    if (p > most) most = p;
+  }
+  Share s;
+  const int64_t least = 256 * DEPTH, even = (all / 16384 + least - 1) / least * least;
+  s.per_wg = even > least ? even : least;
+  s.small = n <= 64 && most <= SMALL_PIECES;
+  s.wgs = 0;
+  for (int i = 0; i < n; ++i) s.wgs += Shape(g[i]).workgroups(s.per_wg);
+  return s;
 }
 
 // f(group, its workgroups) for every launch
 template <typename F>
-hipError_t each_group(const dash_tensor* t, int n, F f) {
-  const int64_t per_wg = pieces_per_wg(t, n);
+hipError_t each_group(const dash_tensor* t, int n, const Share& s, F f) {
   int64_t wgs = 0;
   for (int i0 = 0; i0 < n;) {
-    Tensors g{};
+    Tensors g;
+    g.n = 0;
     g.first = i0;
     g.wg_first = wgs;
-    g.per_wg = per_wg;
+    g.per_wg = s.per_wg;
     int64_t here = 0;
     for (; i0 + g.n < n && g.n < GROUP_TENSORS; ++g.n) {
       const dash_tensor& m = t[i0 + g.n];
-      const Rows r(m);
-      const int64_t more = (r.pieces() + per_wg - 1) / per_wg;
+      const Shape r(m);
+      const int64_t more = r.workgroups(s.per_wg);
       if (here + more > most_workgroups(256)) break;
-      g.ptr[g.n] = m.ptr;
-      g.pieces[g.n] = r.pieces();
-      g.row_pieces[g.n] = r.row_pieces;
-      g.len[g.n] = r.len;
-      g.ld[g.n] = r.ld;
-      g.type[g.n] = (uint8_t)m.type;
+      g.where[g.n] = (uint64_t)(uintptr_t)m.ptr | (uint64_t)m.type << 56;
+      g.size[g.n] = r.rows ? (uint64_t)r.len | (uint64_t)m.ld << 32 : (uint64_t)r.len;
+      g.rows[g.n] = (uint32_t)r.rows;
+      g.wg_base[g.n] = (int32_t)here;
       here += more;
-      g.wg_base[g.n + 1] = (int32_t)here;
     }
     if (g.n == 0) return hipErrorInvalidValue;
     f(g, here);
@@ -234,34 +283,32 @@ hipError_t each_group(const dash_tensor* t, int n, F f) {
   return hipSuccess;
 }
 
-int64_t all_workgroups(const dash_tensor* t, int n) {
-  const int64_t per_wg = pieces_per_wg(t, n);
-  int64_t wgs = 0;
-  for (int i = 0; i < n; ++i) wgs += (Rows(t[i]).pieces() + per_wg - 1) / per_wg;
-  return wgs;
-}
-
 }  // namespace
 
 size_t grad_norm_workspace_bytes(const dash_tensor* t, int n) {
-  return align_up((size_t)all_workgroups(t, n) * sizeof(double), 256) + (size_t)n * sizeof(int64_t);
+  return align_up((size_t)share_out(t, n).wgs * sizeof(double), 256) + (size_t)n * sizeof(int64_t);
 }
 
 hipError_t launch_grad_norm(const dash_tensor* t, int n, float* norm, float* norms, void* ws, hipStream_t stream) {
-  const int64_t parts = all_workgroups(t, n);
+  const Share s = share_out(t, n);
+  if (s.small && n) {
+    return each_group(t, n, s, [&](const Tensors& g, int64_t) {
+      hipLaunchKernelGGL(grad_norm_small_kernel, dim3(1), dim3(1024), 0, stream, g, norm, norms);
+    });
+  }
   double* part = (double*)ws;
-  int64_t* base = (int64_t*)((char*)ws + align_up((size_t)parts * sizeof(double), 256));
-  const hipError_t e = each_group(t, n, [&](const Tensors& g, int64_t wgs) {
+  int64_t* base = (int64_t*)((char*)ws + align_up((size_t)s.wgs * sizeof(double), 256));
+  const hipError_t e = each_group(t, n, s, [&](const Tensors& g, int64_t wgs) {
     hipLaunchKernelGGL(grad_squares_kernel, dim3((unsigned)wgs), dim3(256), 0, stream, g, part, base);
   });
   if (e != hipSuccess) return e;
   const int64_t grid = 1 + (norms ? ((int64_t)n + 15) / 16 : 0);
-  hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)grid), dim3(1024), 0, stream, part, base, parts, n, norm, norms);
+  hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)grid), dim3(1024), 0, stream, part, base, s.wgs, n, norm, norms);
   return hipGetLastError();
 }
 
 hipError_t launch_grad_clip(const dash_tensor* t, int n, const float* norm, float most, hipStream_t stream) {
-  return each_group(t, n, [&](const Tensors& g, int64_t wgs) {
+  return each_group(t, n, share_out(t, n), [&](const Tensors& g, int64_t wgs) {
     hipLaunchKernelGGL(grad_clip_kernel, dim3((unsigned)wgs), dim3(256), 0, stream, g, norm, most);
   });
 }

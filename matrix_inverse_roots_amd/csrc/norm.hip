@@ -27,7 +27,7 @@ struct NormArgs {
   int64_t T, n, first_wg;
   double over_n, eps;
   dash_prec gain_type;
-  int lanes;  // threads of a row (a power of two)
+  int lanes, per;  // threads of a row (a power of two up to 64, or whole waves), and rows of a workgroup
 };
 
 // Elements c .. c + E - 1 of the gain (1 where there is none), zero beyond n; n >= E
@@ -63,7 +63,7 @@ template <typename S>
 __device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
   for (int o = 1; o < 64 && o < lanes; o *= 2) v += __shfl_xor(v, o, 64);
   if (lanes > 64) {
-    const int wave = threadIdx.x >> 6, waves = lanes >> 6, first = wave & ~(waves - 1);
+    const int wave = threadIdx.x >> 6, waves = lanes >> 6, first = wave / waves * waves;
     __syncthreads();  // (the last row's values have been read)
     if ((threadIdx.x & 63) == 0) shared[wave] = v;
     __syncthreads();
@@ -92,12 +92,12 @@ __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int6
   if (c % GROUP == 0) scales[group0 + c / GROUP] = (uint8_t)byte;
 }
 
-template <typename T, int F, int K, int BLOCK>
-__global__ __launch_bounds__(BLOCK) void rmsnorm_kernel(NormArgs a) {
+template <typename T, int F, int K>
+__global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   constexpr int E = EACH<T>;
-  __shared__ double shared[BLOCK / 64];
-  const int lane = threadIdx.x & (a.lanes - 1), per = BLOCK / a.lanes;
-  const int64_t row = (a.first_wg + blockIdx.x) * per + threadIdx.x / a.lanes;
+  __shared__ double shared[16];
+  const int slot = (int)(threadIdx.x / (unsigned)a.lanes), lane = (int)threadIdx.x - slot * a.lanes;
+  const int64_t row = (a.first_wg + blockIdx.x) * a.per + slot;
   const bool live = row < a.T;  // (the others go along to the barriers)
   const int64_t groups = (a.n + GROUP - 1) / GROUP;
   const T* x = (const T*)a.x + row * a.ldx;
@@ -235,18 +235,25 @@ hipError_t launch_rows(K kernel, int64_t grid, int block, A& a, hipStream_t stre
 
 template <typename T, int F, int K>
 hipError_t rmsnorm_rows(NormArgs& a, hipStream_t stream) {
-  if (a.lanes > 256) {
-    const int per = 1024 / a.lanes;
-    return launch_rows(rmsnorm_kernel<T, F, K, 1024>, (a.T + per - 1) / per, 1024, a, stream);
-  }
-  const int per = 256 / a.lanes;
-  return launch_rows(rmsnorm_kernel<T, F, K, 256>, (a.T + per - 1) / per, 256, a, stream);
+  return launch_rows(rmsnorm_kernel<T, F, K>, (a.T + a.per - 1) / a.per, a.per * a.lanes, a, stream);
 }
 
-int64_t up_to_power_of_two(int64_t x) {
-  int64_t p = 1;
-  while (p < x) p *= 2;
-  return p;
+// Threads for a row of `pieces`, k each: whole waves, or within one a power of two
+int row_lanes(int64_t pieces, int k) {
+  const int64_t need = (pieces + k - 1) / k;
+  if (need > 64) return (int)((need + 63) / 64 * 64);
+  int lanes = 1;
+  while (lanes < need) lanes *= 2;
+  return lanes;
+}
+
+// Pieces of a thread, where at most `threads` share a row.  One, so that many waves have loads under way (8192 x
+// 2048 bfloat16 with 1 / 2 / 4: 30.7 / 36.0 / 37.3 us; its gradient 31.1 / 33.4); but two where the last
+// one of a row is cut, which the wave that holds it pays for (50001 x 263: 39.6 / 35.4, gradient 50 / 42).
+int row_pieces(int64_t pieces, bool whole, int threads) {
+  int k = whole ? 1 : 2;
+  while (pieces > (int64_t)threads * k) k *= 2;
+  return k;
 }
 
 template <typename T, int F>
@@ -255,11 +262,12 @@ hipError_t rmsnorm(NormArgs& a, hipStream_t stream) {
   const int64_t pieces = (a.n + GROUP - 1) / GROUP * (GROUP / E);
   if (a.n < TINY) return launch_rows(rmsnorm_tiny_kernel<T, F>, (a.T + 255) / 256, 256, a, stream);
   if (pieces > 1024 * (32 / E)) return launch_rows(rmsnorm_long_kernel<T, F>, a.T, 1024, a, stream);
-  int k = a.T >= 512 ? 32 / E : 1;
-  while (k > 1 && pieces < 64 * k) k /= 2;
-  while (pieces > 1024 * k) k *= 2;
-  int64_t lanes = up_to_power_of_two((pieces + k - 1) / k);
-  a.lanes = (int)(lanes < GROUP / E ? GROUP / E : lanes);
+  // (fp32, with half as many elements a thread, from 512 threads on: 16384 x 4096 with 512 / 1024 198 / 206 us,
+  // 32768 x 8192 without y 604 / 619)
+  const int k = row_pieces(pieces, a.n % E == 0, E == 4 && pieces <= 2048 ? 512 : 1024);
+  a.lanes = row_lanes(pieces, k);
+  if (a.lanes < GROUP / E) a.lanes = GROUP / E;
+  a.per = a.lanes < 256 ? 256 / a.lanes : 1;
   switch (k) {
     case 1: return rmsnorm_rows<T, F, 1>(a, stream);
     case 2: return rmsnorm_rows<T, F, 2>(a, stream);
@@ -280,25 +288,34 @@ struct BackArgs {
   float* dgain;  // a single workgroup's
   float* part;   // or [workgroups, n]
   int64_t lddy, ldh, lddh, lddx;
-  int64_t T, n, rows_wg;  // rows of a workgroup
+  int64_t T, n;
   float over_n;
   dash_prec gain_type;
-  int lanes;
+  int lanes, per;  // threads of a row, and rows side by side
   bool accumulate, sums;  // sums: dgain is wanted
 };
 
 constexpr int BACK_BLOCK = 512;
 
-// A workgroup's rows one after the other (several side by side where they are short); every thread keeps the
-// sums dy xhat of its columns in registers, and the workgroup stores one row of them at the end: equal calls
-// add in the same order.
+// The compiler takes v for a new value here, so that it keeps the 16 bytes and not what it widened them to
+template <typename V>
+__device__ __forceinline__ V keep_packed(V v) {
+  typedef unsigned words_t __attribute__((ext_vector_type(4)));
+  words_t w = __builtin_bit_cast(words_t, v);
+  asm volatile("" : "+v"(w));
+  return __builtin_bit_cast(V, w);
+}
+
+// `per` rows side by side, then the next ones a grid further (the workgroups together read one run of rows:
+// 32768 x 8192 bfloat16 417 -> 395 us over a run of rows for each).  Every thread keeps the sums dy xhat of
+// its columns in registers, and the workgroup stores one row of them at the end: equal calls add in the same
+// order.
 template <typename T, int K>
 __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
   extern __shared__ __attribute__((aligned(16))) float columns[];
   __shared__ float shared[BACK_BLOCK / 64];
-  const int lane = threadIdx.x & (a.lanes - 1), per = BACK_BLOCK / a.lanes, slot = threadIdx.x / a.lanes;
-  const int64_t begin = blockIdx.x * a.rows_wg, end = begin + a.rows_wg < a.T ? begin + a.rows_wg : a.T;
+  const int per = a.per, slot = (int)(threadIdx.x / (unsigned)a.lanes), lane = (int)threadIdx.x - slot * a.lanes;
   float g[K][E], dg[K][E];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -306,10 +323,8 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
 #pragma unroll
     for (int q = 0; q < E; ++q) dg[k][q] = 0.f;
   }
-  for (int64_t r0 = begin; r0 < end; r0 += per) {
-    const int64_t row = r0 + slot;
-    const bool live = row < end;
-    const int64_t n = live ? a.n : 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.T; r0 += (int64_t)gridDim.x * per) {
+    const int64_t row = r0 + slot, n = row < a.T ? a.n : 0;  // (rows behind the last are zeros)
     vec_of<T> dy[K], h[K], dh[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -318,7 +333,7 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
       h[k] = load_piece((const T*)a.h + row * a.ldh, c, n);
       if (a.dh) dh[k] = load_piece((const T*)a.dh + row * a.lddh, c, n);
     }
-    const float rstd = live ? a.rstd[row] : 0.f;
+    const float rstd = row < a.T ? a.rstd[row] : 0.f;
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -329,19 +344,19 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
         dot = fmaf(d * g[k][q], xhat, dot);
       }
     const float mean = row_sum(dot, a.lanes, shared) * a.over_n;
-    if (!live) continue;  // (the workgroup's last rows: no barrier follows in the loop)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int64_t c = (int64_t)E * (lane + k * a.lanes);
-      if (c >= a.n) break;
+      if (c >= n) break;
+      dy[k] = keep_packed(dy[k]);  // (kept as they were loaded until here, and widened again)
+      h[k] = keep_packed(h[k]);
       float dx[E];
 #pragma unroll
       for (int q = 0; q < E; ++q) {
         const float xhat = (float)h[k][q] * rstd;
-        dx[q] = rstd * fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]);
-        if (a.dh) dx[q] += (float)dh[k][q];
+        dx[q] = fmaf(rstd, fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]), a.dh ? (float)dh[k][q] : 0.f);
       }
-      store_piece((T*)a.dx + row * a.lddx, c, a.n, dx);
+      store_piece((T*)a.dx + row * a.lddx, c, n, dx);
     }
   }
   if (!a.sums) return;
@@ -386,9 +401,8 @@ template <typename T>
 __global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
   __shared__ float shared[16];
-  const int64_t begin = blockIdx.x * a.rows_wg, end = begin + a.rows_wg < a.T ? begin + a.rows_wg : a.T;
   float* part = a.part + blockIdx.x * a.n;
-  for (int64_t row = begin; row < end; ++row) {
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const T* dy = (const T*)a.dy + row * a.lddy;
     const T* h = (const T*)a.h + row * a.ldh;
     const float rstd = a.rstd[row];
@@ -419,7 +433,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
           float v[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = (float)vd[4 * p + q] * ((float)vh[4 * p + q] * rstd);
-          if (row > begin) {
+          if (row > blockIdx.x) {
             const vec_of<float> old = load_piece(part, c + 4 * p, a.n);
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] += old[q];
@@ -436,11 +450,10 @@ template <typename T>
 __global__ __launch_bounds__(256) void rmsnorm_back_tiny_kernel(BackArgs a) {
   __shared__ float sums[TINY][256];
   const int n = (int)a.n;
-  const int64_t begin = blockIdx.x * a.rows_wg, end = begin + a.rows_wg < a.T ? begin + a.rows_wg : a.T;
   float dg[TINY];
 #pragma unroll
   for (int q = 0; q < TINY; ++q) dg[q] = 0.f;
-  for (int64_t row = begin + threadIdx.x; row < end; row += 256) {
+  for (int64_t row = blockIdx.x * 256 + threadIdx.x; row < a.T; row += gridDim.x * 256) {
     const float rstd = a.rstd[row];
     float m[TINY], xhat[TINY], dot = 0.f;
 #pragma unroll
@@ -470,7 +483,8 @@ __global__ __launch_bounds__(256) void rmsnorm_back_tiny_kernel(BackArgs a) {
   a.part[blockIdx.x * a.n + threadIdx.x] = (float)s;
 }
 
-// dgain (+)= the sum of the workgroups' rows, in order.  32 columns x 32 threads, each a share of the rows.
+// dgain (+)= the sum of the workgroups' rows: 32 columns x 32 threads with a share of the rows each, which are
+// joined across a wave.
 __global__ __launch_bounds__(1024) void rmsnorm_join_kernel(const float* part, int parts, int64_t n, float* dgain,
                                                             bool accumulate) {
   __shared__ double sums[32][33];
@@ -478,47 +492,43 @@ __global__ __launch_bounds__(1024) void rmsnorm_join_kernel(const float* part, i
   const int64_t c = (int64_t)blockIdx.x * 32 + col;
   double s = 0.;
   if (c < n)
-#pragma unroll 8
+#pragma unroll 16
     for (int p = share; p < parts; p += 32) s += (double)part[p * n + c];
   sums[share][col] = s;
   __syncthreads();
-  if (share || c >= n) return;
-#pragma unroll 8
-  for (int i = 1; i < 32; ++i) s += sums[i][col];
-  dgain[c] = (float)(accumulate ? s + (double)dgain[c] : s);
+  s = sums[col][share];
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) s += __shfl_xor(s, o, 64);
+  const int64_t out = (int64_t)blockIdx.x * 32 + share;
+  if (col == 0 && out < n) dgain[out] = (float)(accumulate ? s + (double)dgain[out] : s);
 }
 
 // How the rows are shared out, over at most MOST_PARTS workgroups
 constexpr int64_t MOST_PARTS = 512;
 struct BackPlan {
-  int k, lanes;  // 0: the kernels of long and of tiny rows
-  int64_t wgs, rows_wg;
+  int k, lanes, per;  // pieces of a thread (0: the kernels of long and of tiny rows), threads of a row, rows abreast
+  int64_t wgs;
 };
 BackPlan back_plan(int64_t T, int64_t n, int E) {
   BackPlan p;
   const int64_t pieces = (n + E - 1) / E;
-  const int most_k = 32 / E;
-  int64_t per = 1;
-  if (n < TINY || pieces > (int64_t)BACK_BLOCK * most_k) {
+  if (n < TINY || pieces > (int64_t)BACK_BLOCK * (32 / E)) {
     p.k = p.lanes = 0;
-    if (n < TINY) per = 256;
+    p.per = n < TINY ? 256 : 1;
   } else {
-    p.k = T >= 512 ? most_k : 1;
-    while (p.k > 1 && pieces < 64 * p.k) p.k /= 2;
-    while (pieces > (int64_t)BACK_BLOCK * p.k) p.k *= 2;
-    p.lanes = (int)up_to_power_of_two((pieces + p.k - 1) / p.k);
-    per = BACK_BLOCK / p.lanes;
+    p.k = row_pieces(pieces, n % E == 0, BACK_BLOCK);
+    p.lanes = row_lanes(pieces, p.k);
+    p.per = BACK_BLOCK / p.lanes;
   }
-  p.rows_wg = (T + MOST_PARTS - 1) / MOST_PARTS;
-  p.rows_wg = (p.rows_wg + per - 1) / per * per;
-  p.wgs = (T + p.rows_wg - 1) / p.rows_wg;
+  p.wgs = (T + p.per - 1) / p.per;
+  if (p.wgs > MOST_PARTS) p.wgs = MOST_PARTS;
   return p;
 }
 
 template <typename T, int K>
 hipError_t back_rows(const BackArgs& a, const BackPlan& p, hipStream_t stream) {
-  const size_t lds = a.sums && p.lanes < BACK_BLOCK ? (size_t)p.lanes * K * EACH<T> * sizeof(float) : 0;
-  hipLaunchKernelGGL((rmsnorm_back_kernel<T, K>), dim3((unsigned)p.wgs), dim3(BACK_BLOCK), lds, stream, a);
+  const size_t lds = a.sums && p.per > 1 ? (size_t)p.lanes * K * EACH<T> * sizeof(float) : 0;
+  hipLaunchKernelGGL((rmsnorm_back_kernel<T, K>), dim3((unsigned)p.wgs), dim3(p.per * p.lanes), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -527,7 +537,7 @@ hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
   const BackPlan p = back_plan(a.T, a.n, EACH<T>);
   float* dgain = a.dgain;
   a.lanes = p.lanes;
-  a.rows_wg = p.rows_wg;
+  a.per = p.per;
   a.part = (float*)ws;
   const bool join = a.sums && (p.wgs > 1 || p.k == 0);
   if (join) a.dgain = nullptr;
@@ -557,7 +567,7 @@ hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
 
 hipError_t launch_rmsnorm(const RmsNorm& p, dash_prec type, dash_mx_fmt fmt, hipStream_t stream) {
   NormArgs a{p.x.p, p.res.p, p.gain, p.h.p, p.y.p, p.codes, p.scales, p.rstd, p.x.ld, p.res.ld, p.h.ld, p.y.ld,
-             p.T, p.n, 0, 1.0 / (double)p.n, (double)p.eps, p.gain_type, 0};
+             p.T, p.n, 0, 1.0 / (double)p.n, (double)p.eps, p.gain_type, 0, 0};
   const bool e4 = fmt == DASH_MX_E4M3;
   if (type == DASH_FP32) return e4 ? rmsnorm<float, DASH_MX_E4M3>(a, stream) : rmsnorm<float, DASH_MX_E2M1>(a, stream);
   if (type == DASH_BF16) return e4 ? rmsnorm<__bf16, DASH_MX_E4M3>(a, stream) : rmsnorm<__bf16, DASH_MX_E2M1>(a, stream);
@@ -571,7 +581,7 @@ size_t rmsnorm_back_workspace_bytes(int64_t T, int64_t n) {
 
 hipError_t launch_rmsnorm_back(const RmsNormBack& p, dash_prec type, void* ws, hipStream_t stream) {
   BackArgs a{p.dy.p, p.h.p, p.dh.p, p.gain, p.rstd, p.dx.p, p.dgain, nullptr, p.dy.ld, p.h.ld, p.dh.ld, p.dx.ld,
-             p.T, p.n, 0, 1.f / (float)p.n, p.gain_type, 0, p.accumulate, p.dgain != nullptr};
+             p.T, p.n, 1.f / (float)p.n, p.gain_type, 0, 0, p.accumulate, p.dgain != nullptr};
   if (type == DASH_FP32) return back<float>(a, ws, stream);
   if (type == DASH_BF16) return back<__bf16>(a, ws, stream);
   return back<_Float16>(a, ws, stream);

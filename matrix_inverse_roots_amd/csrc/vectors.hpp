@@ -70,17 +70,33 @@ __device__ __forceinline__ vec_of<T> load_short(const T* row, int64_t c, int64_t
   return v;
 }
 
+// The EACH values at x, each rounded once, to c .. of a row of n; what lies beyond it is not written.  The row's
+// last piece goes out in halves: at most three stores for eight elements where one for each would be seven.
 template <typename T>
 __device__ __forceinline__ void store_piece(T* row, int64_t c, int64_t n, const float* x) {
+  vec_of<T> v;
+#pragma unroll
+  for (int q = 0; q < EACH<T>; ++q) v[q] = (T)x[q];
   if (c + EACH<T> <= n) {
-    vec_of<T> v;
-#pragma unroll
-    for (int q = 0; q < EACH<T>; ++q) v[q] = (T)x[q];
     *(vec_of<T>*)(row + c) = v;
-  } else {
-#pragma unroll
-    for (int q = 0; q < EACH<T>; ++q)
-      if (c + q < n) row[c + q] = (T)x[q];
+  } else if (c < n) {
+    typedef uint64_t __attribute__((aligned(2), may_alias)) u64;
+    typedef uint32_t __attribute__((aligned(2), may_alias)) u32;
+    typedef uint16_t __attribute__((may_alias)) u16;
+    Bytes16 w = __builtin_bit_cast(Bytes16, v);
+    char* p = (char*)(row + c);
+    const int left = (int)(n - c) * (int)sizeof(T);  // bytes
+    if (left & 8) {
+      *(u64*)p = w.lo;
+      w.lo = w.hi;
+      p += 8;
+    }
+    if (left & 4) {
+      *(u32*)p = (uint32_t)w.lo;
+      w.lo >>= 32;
+      p += 4;
+    }
+    if (sizeof(T) == 2 && (left & 2)) *(u16*)p = (uint16_t)w.lo;
   }
 }
 
