@@ -285,8 +285,8 @@ struct BackArgs {
   const void *dy, *h, *dh, *gain;
   const float* rstd;
   void* dx;
-  float* dgain;  // a single workgroup's
-  float* part;   // or [workgroups, n]
+  float* dgain;
+  float* part;  // [workgroups, n]: the sums that are joined into it
   int64_t lddy, ldh, lddh, lddx;
   int64_t T, n;
   float over_n;
@@ -306,6 +306,55 @@ __device__ __forceinline__ V keep_packed(V v) {
   return __builtin_bit_cast(V, w);
 }
 
+// The largest power of two below x (0 for 1)
+__host__ __device__ inline int half_of(int x) {
+  int h = 1;
+  while (2 * h < x) h *= 2;
+  return x > 1 ? h : 0;
+}
+
+// One row of dx, and (SUMS) its part of the thread's column sums.  Every thread of the workgroup calls it; rows
+// behind the last are zeros.
+template <typename T, int K, bool SUMS>
+__device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lane, const float (&g)[K][EACH<T>],
+                                         float (&dg)[K][EACH<T>], float* shared) {
+  constexpr int E = EACH<T>;
+  const int64_t n = row < a.T ? a.n : 0;
+  vec_of<T> dy[K], h[K], dh[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t c = (int64_t)E * (lane + k * a.lanes);
+    dy[k] = load_piece((const T*)a.dy + row * a.lddy, c, n);
+    h[k] = load_piece((const T*)a.h + row * a.ldh, c, n);
+    if (a.dh) dh[k] = load_piece((const T*)a.dh + row * a.lddh, c, n);
+  }
+  const float rstd = row < a.T ? a.rstd[row] : 0.f;
+  float dot = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int q = 0; q < E; ++q) {
+      const float d = (float)dy[k][q], xhat = (float)h[k][q] * rstd;
+      if (SUMS) dg[k][q] = fmaf(d, xhat, dg[k][q]);
+      dot = fmaf(d * g[k][q], xhat, dot);
+    }
+  const float mean = row_sum(dot, a.lanes, shared) * a.over_n;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t c = (int64_t)E * (lane + k * a.lanes);
+    if (c >= n) break;
+    dy[k] = keep_packed(dy[k]);  // (kept as they were loaded until here, and widened again)
+    h[k] = keep_packed(h[k]);
+    float dx[E];
+#pragma unroll
+    for (int q = 0; q < E; ++q) {
+      const float xhat = (float)h[k][q] * rstd;
+      dx[q] = fmaf(rstd, fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]), a.dh ? (float)dh[k][q] : 0.f);
+    }
+    store_piece((T*)a.dx + row * a.lddx, c, n, dx);
+  }
+}
+
 // `per` rows side by side, then the next ones a grid further (the workgroups together read one run of rows:
 // 32768 x 8192 bfloat16 417 -> 395 us over a run of rows for each).  Every thread keeps the sums dy xhat of
 // its columns in registers, and the workgroup stores one row of them at the end: equal calls add in the same
@@ -323,76 +372,73 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
 #pragma unroll
     for (int q = 0; q < E; ++q) dg[k][q] = 0.f;
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.T; r0 += (int64_t)gridDim.x * per) {
-    const int64_t row = r0 + slot, n = row < a.T ? a.n : 0;  // (rows behind the last are zeros)
-    vec_of<T> dy[K], h[K], dh[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int64_t c = (int64_t)E * (lane + k * a.lanes);
-      dy[k] = load_piece((const T*)a.dy + row * a.lddy, c, n);
-      h[k] = load_piece((const T*)a.h + row * a.ldh, c, n);
-      if (a.dh) dh[k] = load_piece((const T*)a.dh + row * a.lddh, c, n);
-    }
-    const float rstd = row < a.T ? a.rstd[row] : 0.f;
-    float dot = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int q = 0; q < E; ++q) {
-        const float d = (float)dy[k][q], xhat = (float)h[k][q] * rstd;
-        dg[k][q] = fmaf(d, xhat, dg[k][q]);
-        dot = fmaf(d * g[k][q], xhat, dot);
-      }
-    const float mean = row_sum(dot, a.lanes, shared) * a.over_n;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int64_t c = (int64_t)E * (lane + k * a.lanes);
-      if (c >= n) break;
-      dy[k] = keep_packed(dy[k]);  // (kept as they were loaded until here, and widened again)
-      h[k] = keep_packed(h[k]);
-      float dx[E];
-#pragma unroll
-      for (int q = 0; q < E; ++q) {
-        const float xhat = (float)h[k][q] * rstd;
-        dx[q] = fmaf(rstd, fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]), a.dh ? (float)dh[k][q] : 0.f);
-      }
-      store_piece((T*)a.dx + row * a.lddx, c, n, dx);
-    }
-  }
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.T; r0 += (int64_t)gridDim.x * per)
+    back_row<T, K, true>(a, r0 + slot, lane, g, dg, shared);
   if (!a.sums) return;
-  // the rows side by side, in order
-  for (int i = per - 1; i > 0; --i) {
+  // the rows side by side, halving (slot by slot 64 of them took 10 us)
+  for (int half = half_of(per); half; half /= 2) {
     __syncthreads();
-    if (slot == i)
+    float* with = columns + (slot & (half - 1)) * (K * E) * a.lanes + lane;
+    if (slot >= half && slot < 2 * half)
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int q = 0; q < E; ++q) columns[(k * E + q) * a.lanes + lane] = dg[k][q];
+        for (int q = 0; q < E; ++q) with[(k * E + q) * a.lanes] = dg[k][q];
     __syncthreads();
-    if (slot == i - 1)
+    if (slot < half && slot + half < per)
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int q = 0; q < E; ++q) dg[k][q] += columns[(k * E + q) * a.lanes + lane];
+        for (int q = 0; q < E; ++q) dg[k][q] += with[(k * E + q) * a.lanes];
   }
   if (slot) return;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int64_t c = (int64_t)E * (lane + k * a.lanes);
 #pragma unroll
-    for (int p = 0; p < E / 4; ++p) {
-      float* out = a.dgain ? a.dgain : a.part + blockIdx.x * a.n;
-      float v[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = dg[k][4 * p + q];
-      if (a.dgain && a.accumulate) {
-        const vec_of<float> old = load_piece(out, c + 4 * p, a.n);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] += old[q];
-      }
-      store_piece(out, c + 4 * p, a.n, v);
-    }
+    for (int p = 0; p < E / 4; ++p) store_piece(a.part + blockIdx.x * a.n, c + 4 * p, a.n, dg[k] + 4 * p);
   }
+}
+
+// Few rows, dy not replaced: the first row_wgs workgroups take `per` rows each, and the others 16 pieces of columns
+// each, whose sums they form from dy and h themselves (the caches hold them): no second launch.
+template <typename T, int K>
+__global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_few_kernel(BackArgs a, int row_wgs) {
+  constexpr int E = EACH<T>, WIDE = 16, SHARES = BACK_BLOCK / WIDE;
+  __shared__ float shared[2 * (BACK_BLOCK / 64)];  // (of a row that the workgroup's last waves would begin, too)
+  __shared__ float sums[SHARES][WIDE * E + 1];
+  if ((int)blockIdx.x < row_wgs) {
+    const int slot = (int)(threadIdx.x / (unsigned)a.lanes), lane = (int)threadIdx.x - slot * a.lanes;
+    float g[K][E];
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
+    // (threads behind the workgroup's last row go along to the barriers with a row of zeros)
+    const int64_t row = slot < a.per ? (int64_t)blockIdx.x * a.per + slot : a.T;
+    back_row<T, K, false>(a, row, lane, g, g, shared);
+    return;
+  }
+  const int piece = threadIdx.x % WIDE, share = threadIdx.x / WIDE;
+  const int64_t c0 = (int64_t)((int)blockIdx.x - row_wgs) * (WIDE * E), c = c0 + piece * E;
+  float s[E];
+#pragma unroll
+  for (int q = 0; q < E; ++q) s[q] = 0.f;
+#pragma unroll 4
+  for (int64_t row = share; row < a.T; row += SHARES) {
+    const vec_of<T> dy = load_piece((const T*)a.dy + row * a.lddy, c, a.n);
+    const vec_of<T> h = load_piece((const T*)a.h + row * a.ldh, c, a.n);
+    const float rstd = a.rstd[row];
+#pragma unroll
+    for (int q = 0; q < E; ++q) s[q] = fmaf((float)dy[q], (float)h[q] * rstd, s[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < E; ++q) sums[share][piece * E + q] = s[q];
+  __syncthreads();
+  const int64_t out = c0 + threadIdx.x;
+  if (threadIdx.x >= WIDE * E || out >= a.n) return;
+  double all = a.accumulate ? (double)a.dgain[out] : 0.;
+#pragma unroll
+  for (int i = 0; i < SHARES; ++i) all += (double)sums[i][threadIdx.x];
+  a.dgain[out] = (float)all;
 }
 
 // Rows that the registers of a workgroup do not hold: each is read twice, and the sums stay in the workgroup's
@@ -508,7 +554,9 @@ constexpr int64_t MOST_PARTS = 512;
 struct BackPlan {
   int k, lanes, per;  // pieces of a thread (0: the kernels of long and of tiny rows), threads of a row, rows abreast
   int64_t wgs;
+  bool few = false;  // rmsnorm_back_few_kernel
 };
+constexpr int64_t FEW_ROWS = 512;
 BackPlan back_plan(int64_t T, int64_t n, int E) {
   BackPlan p;
   const int64_t pieces = (n + E - 1) / E;
@@ -527,20 +575,24 @@ BackPlan back_plan(int64_t T, int64_t n, int E) {
 
 template <typename T, int K>
 hipError_t back_rows(const BackArgs& a, const BackPlan& p, hipStream_t stream) {
-  const size_t lds = a.sums && p.per > 1 ? (size_t)p.lanes * K * EACH<T> * sizeof(float) : 0;
-  hipLaunchKernelGGL((rmsnorm_back_kernel<T, K>), dim3((unsigned)p.wgs), dim3(p.per * p.lanes), lds, stream, a);
+  if (p.few) {
+    const int64_t wide = 16 * EACH<T>;
+    hipLaunchKernelGGL((rmsnorm_back_few_kernel<T, K>), dim3((unsigned)(p.wgs + (a.n + wide - 1) / wide)),
+                       dim3(BACK_BLOCK), 0, stream, a, (int)p.wgs);
+  } else {
+    const size_t lds = a.sums ? (size_t)half_of(p.per) * p.lanes * K * EACH<T> * sizeof(float) : 0;
+    hipLaunchKernelGGL((rmsnorm_back_kernel<T, K>), dim3((unsigned)p.wgs), dim3(p.per * p.lanes), lds, stream, a);
+  }
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
-  const BackPlan p = back_plan(a.T, a.n, EACH<T>);
-  float* dgain = a.dgain;
+  BackPlan p = back_plan(a.T, a.n, EACH<T>);
+  p.few = p.k && a.sums && a.T <= FEW_ROWS && a.dx != a.dy;
   a.lanes = p.lanes;
   a.per = p.per;
   a.part = (float*)ws;
-  const bool join = a.sums && (p.wgs > 1 || p.k == 0);
-  if (join) a.dgain = nullptr;
   hipError_t e = hipErrorInvalidValue;
   if (p.k == 0) {
     if (a.n < TINY)
@@ -557,9 +609,9 @@ hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
   } else {
     if constexpr (EACH<T> == 4) e = back_rows<T, 8>(a, p, stream);
   }
-  if (e != hipSuccess || !join) return e;
+  if (e != hipSuccess || !a.sums || p.few) return e;
   hipLaunchKernelGGL(rmsnorm_join_kernel, dim3((unsigned)((a.n + 31) / 32)), dim3(1024), 0, stream, a.part, (int)p.wgs,
-                     a.n, dgain, a.accumulate);
+                     a.n, a.dgain, a.accumulate);
   return hipGetLastError();
 }
 
