@@ -352,6 +352,9 @@ size_t mx_grad_workspace_bytes(int64_t T, int64_t out, int64_t in, dash_prec typ
 hipError_t launch_mx_grad(const void* dY, dash_prec type, int64_t ldy, const MxCodes& q, dash_mx_fmt fmt, int64_t T,
                           int64_t out, int64_t in, int B, bool accumulate, float* G, void* ws, hipStream_t stream);
 
+// Calls that move more than this (the memory-side cache's size) load and store past the caches.
+constexpr int64_t LARGE_BYTES = (int64_t)256 << 20;
+
 // The norm with a microscaled output, and its gradient (norm.hip): T rows of n, every matrix with its own pitch.
 // gain: NULL, or [n] of gain_type.  h, y, codes and scales, rstd (outputs): NULL where not wanted.
 struct RowsOf {

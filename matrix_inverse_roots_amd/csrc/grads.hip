@@ -96,14 +96,14 @@ __device__ __forceinline__ void each_piece(const Pieces<T>& v, int64_t first, in
 
 constexpr int DEPTH = 4;
 
-template <typename T>
+template <bool PAST, typename T>
 __device__ __forceinline__ double squares(const Tensors& g, int t, int64_t first, int64_t most, int thread, int threads) {
   double s = 0.;
   each_piece<DEPTH>(Pieces<T>(g, t), first, most, thread, threads, [&](T* const* row, const int64_t* c,
                                                                        const int64_t* len) {
     vec_of<T> v[DEPTH];
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) v[k] = load_short(row[k], c[k], len[k]);
+    for (int k = 0; k < DEPTH; ++k) v[k] = load_short<PAST>(row[k], c[k], len[k]);
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) {
       float x[EACH<T>];
@@ -114,11 +114,12 @@ __device__ __forceinline__ double squares(const Tensors& g, int t, int64_t first
   });
   return s;
 }
+template <bool PAST>
 __device__ __forceinline__ double squares_of(const Tensors& g, int t, int64_t first, int64_t most, int thread, int threads) {
   const int type = (int)(g.where[t] >> 56);
-  if (type == DASH_FP32) return squares<float>(g, t, first, most, thread, threads);
-  if (type == DASH_BF16) return squares<__bf16>(g, t, first, most, thread, threads);
-  return squares<_Float16>(g, t, first, most, thread, threads);
+  if (type == DASH_FP32) return squares<PAST, float>(g, t, first, most, thread, threads);
+  if (type == DASH_BF16) return squares<PAST, __bf16>(g, t, first, most, thread, threads);
+  return squares<PAST, _Float16>(g, t, first, most, thread, threads);
 }
 __device__ __forceinline__ double wave_sum(double s) {
 #pragma unroll
@@ -127,9 +128,10 @@ __device__ __forceinline__ double wave_sum(double s) {
 }
 
 // part[w] = the sum of squares of workgroup w's pieces; base[t] = tensor t's first workgroup
+template <bool PAST>
 __global__ __launch_bounds__(256) void grad_squares_kernel(Tensors g, double* part, int64_t* base) {
   const int t = find_tensor(g), w = (int)blockIdx.x - g.wg_base[t];
-  const double s = wave_sum(squares_of(g, t, w * g.per_wg, g.per_wg, threadIdx.x, 256));
+  const double s = wave_sum(squares_of<PAST>(g, t, w * g.per_wg, g.per_wg, threadIdx.x, 256));
   __shared__ double waves[4];
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -144,7 +146,7 @@ __global__ __launch_bounds__(1024) void grad_norm_small_kernel(Tensors g, float*
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double all = 0.;
   for (int t = wave; t < g.n; t += 16) {
-    const double s = wave_sum(squares_of(g, t, 0, INT64_MAX, lane, 64));
+    const double s = wave_sum(squares_of<false>(g, t, 0, INT64_MAX, lane, 64));
     if (norms && lane == 0) norms[t] = (float)sqrt(s);
     all += s;
   }
@@ -182,34 +184,35 @@ __global__ __launch_bounds__(1024) void grad_norm_kernel(const double* part, con
   *norm = (float)sqrt(s);
 }
 
-template <typename T>
+template <bool PAST, typename T>
 __device__ __forceinline__ void clip_tensor(const Tensors& g, int t, float factor) {
   const int64_t first = (int64_t)((int)blockIdx.x - g.wg_base[t]) * g.per_wg;
   each_piece<DEPTH>(Pieces<T>(g, t), first, g.per_wg, threadIdx.x, 256, [&](T* const* row, const int64_t* c,
                                                                             const int64_t* len) {
     vec_of<T> v[DEPTH];
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) v[k] = load_short(row[k], c[k], len[k]);
+    for (int k = 0; k < DEPTH; ++k) v[k] = load_short<PAST>(row[k], c[k], len[k]);
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) {
       float x[EACH<T>];
 #pragma unroll
       for (int q = 0; q < EACH<T>; ++q) x[q] = (float)v[k][q] * factor;
-      store_piece(row[k], c[k], len[k], x);
+      store_piece<PAST>(row[k], c[k], len[k], x);
     }
   });
 }
 
+template <bool PAST>
 __global__ __launch_bounds__(256) void grad_clip_kernel(Tensors g, const float* norm, float most) {
   const float factor = clip_factor(norm, most);
   if (factor == 1.f) return;  // (the gradients stay as they are)
   const int t = find_tensor(g), type = (int)(g.where[t] >> 56);
   if (type == DASH_FP32)
-    clip_tensor<float>(g, t, factor);
+    clip_tensor<PAST, float>(g, t, factor);
   else if (type == DASH_BF16)
-    clip_tensor<__bf16>(g, t, factor);
+    clip_tensor<PAST, __bf16>(g, t, factor);
   else
-    clip_tensor<_Float16>(g, t, factor);
+    clip_tensor<PAST, _Float16>(g, t, factor);
 }
 
 // A tensor as the kernels take it: one run where nothing lies between its rows
@@ -233,6 +236,7 @@ struct Shape {
 struct Share {
   int64_t per_wg, wgs;
   bool small;  // for grad_norm_small_kernel
+  bool past;   // the caches: they hold no part of it until the next pass
 };
 constexpr int64_t SMALL_PIECES = 512;
 Share share_out(const dash_tensor* g, int n) {
@@ -245,6 +249,7 @@ Share share_out(const dash_tensor* g, int n) {
   Share s;
   const int64_t least = 256 * DEPTH, even = (all / 16384 + least - 1) / least * least;
   s.per_wg = even > least ? even : least;
+  s.past = all > LARGE_BYTES / 16;
   s.small = n <= 64 && most <= SMALL_PIECES;
   s.wgs = 0;
   for (int i = 0; i < n; ++i) s.wgs += Shape(g[i]).workgroups(s.per_wg);
@@ -299,7 +304,8 @@ hipError_t launch_grad_norm(const dash_tensor* t, int n, float* norm, float* nor
   double* part = (double*)ws;
   int64_t* base = (int64_t*)((char*)ws + align_up((size_t)s.wgs * sizeof(double), 256));
   const hipError_t e = each_group(t, n, s, [&](const Tensors& g, int64_t wgs) {
-    hipLaunchKernelGGL(grad_squares_kernel, dim3((unsigned)wgs), dim3(256), 0, stream, g, part, base);
+    hipLaunchKernelGGL(s.past ? grad_squares_kernel<true> : grad_squares_kernel<false>, dim3((unsigned)wgs), dim3(256),
+                       0, stream, g, part, base);
   });
   if (e != hipSuccess) return e;
   const int64_t grid = 1 + (norms ? ((int64_t)n + 15) / 16 : 0);
@@ -308,8 +314,10 @@ hipError_t launch_grad_norm(const dash_tensor* t, int n, float* norm, float* nor
 }
 
 hipError_t launch_grad_clip(const dash_tensor* t, int n, const float* norm, float most, hipStream_t stream) {
-  return each_group(t, n, share_out(t, n), [&](const Tensors& g, int64_t wgs) {
-    hipLaunchKernelGGL(grad_clip_kernel, dim3((unsigned)wgs), dim3(256), 0, stream, g, norm, most);
+  const Share s = share_out(t, n);
+  return each_group(t, n, s, [&](const Tensors& g, int64_t wgs) {
+    hipLaunchKernelGGL(s.past ? grad_clip_kernel<true> : grad_clip_kernel<false>, dim3((unsigned)wgs), dim3(256), 0,
+                       stream, g, norm, most);
   });
 }
 

@@ -28,6 +28,7 @@ struct NormArgs {
   double over_n, eps;
   dash_prec gain_type;
   int lanes, per;  // threads of a row (a power of two up to 64, or whole waves), and rows of a workgroup
+  bool past;       // outputs past the caches (which hold no part of them until they are read)
 };
 
 // Elements c .. c + E - 1 of the gain (1 where there is none), zero beyond n; n >= E
@@ -74,7 +75,7 @@ __device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
 }
 
 // One piece of y as codes; the scale byte from the first lane of its group
-template <int F, int E>
+template <int F, int E, bool PAST>
 __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int64_t c, uint8_t* codes, uint8_t* scales) {
   unsigned top = 0;
 #pragma unroll
@@ -83,16 +84,19 @@ __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int6
   for (int o = 1; o < GROUP / E; o *= 2) top = umax(top, __shfl_xor(top, o, 64));
   const unsigned byte = scale_byte<F>(top);
   typedef typename Codes<F>::raw4 raw4;
-  struct alignas(sizeof(raw4) * (E / 4)) Raw {
-    raw4 q[E / 4];
-  } raw;
+  typedef raw4 raw_t __attribute__((ext_vector_type(E / 4)));
+  raw_t raw;
 #pragma unroll
-  for (int p = 0; p < E / 4; ++p) raw.q[p] = Codes<F>::encode4(y + 4 * p, byte);
-  *(Raw*)(codes + (group0 * GROUP + c) * Codes<F>::BITS / 8) = raw;
+  for (int p = 0; p < E / 4; ++p) raw[p] = Codes<F>::encode4(y + 4 * p, byte);
+  raw_t* out = (raw_t*)(codes + (group0 * GROUP + c) * Codes<F>::BITS / 8);
+  if (PAST)
+    __builtin_nontemporal_store(raw, out);
+  else
+    *out = raw;
   if (c % GROUP == 0) scales[group0 + c / GROUP] = (uint8_t)byte;
 }
 
-template <typename T, int F, int K>
+template <typename T, int F, int K, bool PAST>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   constexpr int E = EACH<T>;
   __shared__ double shared[16];
@@ -131,12 +135,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   for (int k = 0; k < K; ++k) {
     const int64_t c = (int64_t)E * (lane + k * a.lanes);
     if (c >= groups * GROUP) break;  // (the lanes of a group together)
-    if (a.h) store_piece((T*)a.h + row * a.ldh, c, a.n, h[k]);
+    if (a.h) store_piece<PAST>((T*)a.h + row * a.ldh, c, a.n, h[k]);
     float y[E];
 #pragma unroll
     for (int q = 0; q < E; ++q) y[q] = h[k][q] * rstd * g[k][q];
-    if (a.y) store_piece((T*)a.y + row * a.ldy, c, a.n, y);
-    if (a.codes) store_codes<F, E>(y, row * groups, c, a.codes, a.scales);
+    if (a.y) store_piece<PAST>((T*)a.y + row * a.ldy, c, a.n, y);
+    if (a.codes) store_codes<F, E, PAST>(y, row * groups, c, a.codes, a.scales);
   }
 }
 
@@ -180,7 +184,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
 #pragma unroll
     for (int q = 0; q < E; ++q) y[q] = h[q] * rstd * g[q];
     if (a.y) store_piece((T*)a.y + row * a.ldy, c, a.n, y);
-    if (a.codes) store_codes<F, E>(y, row * groups, c, a.codes, a.scales);
+    if (a.codes) store_codes<F, E, false>(y, row * groups, c, a.codes, a.scales);
   }
 }
 
@@ -235,7 +239,7 @@ hipError_t launch_rows(K kernel, int64_t grid, int block, A& a, hipStream_t stre
 
 template <typename T, int F, int K>
 hipError_t rmsnorm_rows(NormArgs& a, hipStream_t stream) {
-  return launch_rows(rmsnorm_kernel<T, F, K>, (a.T + a.per - 1) / a.per, a.per * a.lanes, a, stream);
+  return launch_rows(a.past ? rmsnorm_kernel<T, F, K, true> : rmsnorm_kernel<T, F, K, false>, (a.T + a.per - 1) / a.per, a.per * a.lanes, a, stream);
 }
 
 // Threads for a row of `pieces`, k each: whole waves, or within one a power of two
@@ -268,6 +272,8 @@ hipError_t rmsnorm(NormArgs& a, hipStream_t stream) {
   a.lanes = row_lanes(pieces, k);
   if (a.lanes < GROUP / E) a.lanes = GROUP / E;
   a.per = a.lanes < 256 ? 256 / a.lanes : 1;
+  const int streams = 1 + (a.res != nullptr) + (a.h != nullptr) + (a.y != nullptr);
+  a.past = a.T * a.n * (int64_t)sizeof(T) * streams > LARGE_BYTES;
   switch (k) {
     case 1: return rmsnorm_rows<T, F, 1>(a, stream);
     case 2: return rmsnorm_rows<T, F, 2>(a, stream);
@@ -315,7 +321,7 @@ __host__ __device__ inline int half_of(int x) {
 
 // One row of dx, and (SUMS) its part of the thread's column sums.  Every thread of the workgroup calls it; rows
 // behind the last are zeros.
-template <typename T, int K, bool SUMS>
+template <typename T, int K, bool SUMS, bool PAST>
 __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lane, const float (&g)[K][EACH<T>],
                                          float (&dg)[K][EACH<T>], float* shared) {
   constexpr int E = EACH<T>;
@@ -324,9 +330,9 @@ __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lan
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int64_t c = (int64_t)E * (lane + k * a.lanes);
-    dy[k] = load_piece((const T*)a.dy + row * a.lddy, c, n);
-    h[k] = load_piece((const T*)a.h + row * a.ldh, c, n);
-    if (a.dh) dh[k] = load_piece((const T*)a.dh + row * a.lddh, c, n);
+    dy[k] = load_piece<PAST>((const T*)a.dy + row * a.lddy, c, n);
+    h[k] = load_piece<PAST>((const T*)a.h + row * a.ldh, c, n);
+    if (a.dh) dh[k] = load_piece<PAST>((const T*)a.dh + row * a.lddh, c, n);
   }
   const float rstd = row < a.T ? a.rstd[row] : 0.f;
   float dot = 0.f;
@@ -351,7 +357,7 @@ __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lan
       const float xhat = (float)h[k][q] * rstd;
       dx[q] = fmaf(rstd, fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]), a.dh ? (float)dh[k][q] : 0.f);
     }
-    store_piece((T*)a.dx + row * a.lddx, c, n, dx);
+    store_piece<PAST>((T*)a.dx + row * a.lddx, c, n, dx);
   }
 }
 
@@ -359,7 +365,7 @@ __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lan
 // 32768 x 8192 bfloat16 417 -> 395 us over a run of rows for each).  Every thread keeps the sums dy xhat of
 // its columns in registers, and the workgroup stores one row of them at the end: equal calls add in the same
 // order.
-template <typename T, int K>
+template <typename T, int K, bool PAST>
 __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
   extern __shared__ __attribute__((aligned(16))) float columns[];
@@ -373,7 +379,7 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
     for (int q = 0; q < E; ++q) dg[k][q] = 0.f;
   }
   for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.T; r0 += (int64_t)gridDim.x * per)
-    back_row<T, K, true>(a, r0 + slot, lane, g, dg, shared);
+    back_row<T, K, true, PAST>(a, r0 + slot, lane, g, dg, shared);
   if (!a.sums) return;
   // the rows side by side, halving (slot by slot 64 of them took 10 us)
   for (int half = half_of(per); half; half /= 2) {
@@ -414,7 +420,7 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_few_kernel(BackArgs a
     for (int k = 0; k < K; ++k) load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
     // (threads behind the workgroup's last row go along to the barriers with a row of zeros)
     const int64_t row = slot < a.per ? (int64_t)blockIdx.x * a.per + slot : a.T;
-    back_row<T, K, false>(a, row, lane, g, g, shared);
+    back_row<T, K, false, false>(a, row, lane, g, g, shared);
     return;
   }
   const int piece = threadIdx.x % WIDE, share = threadIdx.x / WIDE;
@@ -564,12 +570,19 @@ BackPlan back_plan(int64_t T, int64_t n, int E) {
     p.k = p.lanes = 0;
     p.per = n < TINY ? 256 : 1;
   } else {
-    p.k = row_pieces(pieces, n % E == 0, BACK_BLOCK);
+    // (16-bit rows that end inside a piece: up to four pieces a thread, 12001 x 8001 198 -> 188 us, whole ones of
+    // 8192 are 2 % the other way)
+    const bool whole = n % E == 0;
+    p.k = row_pieces(pieces, whole, E == 8 && !whole ? 256 : BACK_BLOCK);
+    if (p.k > 32 / E) p.k = 32 / E;
     p.lanes = row_lanes(pieces, p.k);
     p.per = BACK_BLOCK / p.lanes;
   }
+  // With four pieces a thread one workgroup fills a compute unit's registers (fp32 16384 x 6144 with 256 / 512 of
+  // them 288 / 299 us, 12001 x 8001 289 / 297); with fewer, two (50001 x 263 bfloat16 with 256 / 512 49 / 38).
+  const int64_t most = p.k >= 4 ? MOST_PARTS / 2 : MOST_PARTS;
   p.wgs = (T + p.per - 1) / p.per;
-  if (p.wgs > MOST_PARTS) p.wgs = MOST_PARTS;
+  if (p.wgs > most) p.wgs = most;
   return p;
 }
 
@@ -581,7 +594,9 @@ hipError_t back_rows(const BackArgs& a, const BackPlan& p, hipStream_t stream) {
                        dim3(BACK_BLOCK), 0, stream, a, (int)p.wgs);
   } else {
     const size_t lds = a.sums ? (size_t)half_of(p.per) * p.lanes * K * EACH<T> * sizeof(float) : 0;
-    hipLaunchKernelGGL((rmsnorm_back_kernel<T, K>), dim3((unsigned)p.wgs), dim3(p.per * p.lanes), lds, stream, a);
+    const bool past = a.T * a.n * (int64_t)sizeof(T) * (a.dh ? 4 : 3) > LARGE_BYTES;
+    hipLaunchKernelGGL((past ? rmsnorm_back_kernel<T, K, true> : rmsnorm_back_kernel<T, K, false>),
+                       dim3((unsigned)p.wgs), dim3(p.per * p.lanes), lds, stream, a);
   }
   return hipGetLastError();
 }
@@ -590,6 +605,7 @@ template <typename T>
 hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
   BackPlan p = back_plan(a.T, a.n, EACH<T>);
   p.few = p.k && a.sums && a.T <= FEW_ROWS && a.dx != a.dy;
+  if (p.few) p.wgs = (a.T + p.per - 1) / p.per;
   a.lanes = p.lanes;
   a.per = p.per;
   a.part = (float*)ws;
@@ -619,7 +635,7 @@ hipError_t back(BackArgs& a, void* ws, hipStream_t stream) {
 
 hipError_t launch_rmsnorm(const RmsNorm& p, dash_prec type, dash_mx_fmt fmt, hipStream_t stream) {
   NormArgs a{p.x.p, p.res.p, p.gain, p.h.p, p.y.p, p.codes, p.scales, p.rstd, p.x.ld, p.res.ld, p.h.ld, p.y.ld,
-             p.T, p.n, 0, 1.0 / (double)p.n, (double)p.eps, p.gain_type, 0, 0};
+             p.T, p.n, 0, 1.0 / (double)p.n, (double)p.eps, p.gain_type, 0, 0, false};
   const bool e4 = fmt == DASH_MX_E4M3;
   if (type == DASH_FP32) return e4 ? rmsnorm<float, DASH_MX_E4M3>(a, stream) : rmsnorm<float, DASH_MX_E2M1>(a, stream);
   if (type == DASH_BF16) return e4 ? rmsnorm<__bf16, DASH_MX_E4M3>(a, stream) : rmsnorm<__bf16, DASH_MX_E2M1>(a, stream);

@@ -41,29 +41,31 @@ __device__ __forceinline__ Bytes16 last_first(Bytes16 w, int bits) {
 }
 
 // The N elements from c on of a row of n, zero beyond it: one load, where the row ends inside the piece of the
-// row's last N elements.  n >= N, or 0 (nothing is loaded).
-template <int N, typename T>
+// row's last N elements.  n >= N, or 0 (nothing is loaded).  PAST, here and below: past the caches, for what is far
+// larger than they are and used once.
+template <int N, bool PAST = false, typename T>
 __device__ __forceinline__ auto load_elements(const T* row, int64_t c, int64_t n) {
   typedef T piece_t __attribute__((ext_vector_type(N), aligned(sizeof(T))));
   typedef std::conditional_t<N * sizeof(T) == 16, Bytes16, uint64_t> bytes_t;
   piece_t v = {};
   if (c < n) {
     const int64_t at = c + N <= n ? c : n - N;
-    v = *(const piece_t*)(row + at);
+    const piece_t* p = (const piece_t*)(row + at);
+    v = PAST ? __builtin_nontemporal_load(p) : *p;
     if (at != c)
       v = __builtin_bit_cast(piece_t, last_first(__builtin_bit_cast(bytes_t, v), (int)(n - c) * 8 * (int)sizeof(T)));
   }
   return v;
 }
 // Elements c .. c + EACH - 1 of a row of n, zero beyond it; n >= EACH, or 0
-template <typename T>
+template <bool PAST = false, typename T>
 __device__ __forceinline__ vec_of<T> load_piece(const T* row, int64_t c, int64_t n) {
-  return __builtin_bit_cast(vec_of<T>, load_elements<EACH<T>>(row, c, n));
+  return __builtin_bit_cast(vec_of<T>, load_elements<EACH<T>, PAST>(row, c, n));
 }
 // The same for a row of any length
-template <typename T>
+template <bool PAST = false, typename T>
 __device__ __forceinline__ vec_of<T> load_short(const T* row, int64_t c, int64_t n) {
-  if (n >= EACH<T>) return load_piece(row, c, n);
+  if (n >= EACH<T>) return load_piece<PAST>(row, c, n);
   vec_of<T> v;
 #pragma unroll
   for (int q = 0; q < EACH<T>; ++q) v[q] = c + q < n ? row[c + q] : (T)0.f;
@@ -72,13 +74,17 @@ __device__ __forceinline__ vec_of<T> load_short(const T* row, int64_t c, int64_t
 
 // The EACH values at x, each rounded once, to c .. of a row of n; what lies beyond it is not written.  The row's
 // last piece goes out in halves: at most three stores for eight elements where one for each would be seven.
-template <typename T>
+template <bool PAST = false, typename T>
 __device__ __forceinline__ void store_piece(T* row, int64_t c, int64_t n, const float* x) {
   vec_of<T> v;
 #pragma unroll
   for (int q = 0; q < EACH<T>; ++q) v[q] = (T)x[q];
   if (c + EACH<T> <= n) {
-    *(vec_of<T>*)(row + c) = v;
+    vec_of<T>* p = (vec_of<T>*)(row + c);
+    if (PAST)
+      __builtin_nontemporal_store(v, p);
+    else
+      *p = v;
   } else if (c < n) {
     typedef uint64_t __attribute__((aligned(2), may_alias)) u64;
     typedef uint32_t __attribute__((aligned(2), may_alias)) u32;

@@ -156,6 +156,26 @@ def test_clip(name, pad):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+def test_large_lists(dtype):
+    """Lists beyond the caches' size, which are read and written past them, with odd pieces among them."""
+    n = 3 * 2**26 if dtype != torch.float32 else 3 * 2**25
+    flat = randn(11, n, scale=1e-3, dtype=dtype)
+    old = flat.clone()
+    grads = [flat[:5], flat[5:n // 2 - 3], flat[n // 2:n // 2 + 4097 * 1000].view(1000, 4097)[:, 1:4090],
+             flat[n // 2 + 4097 * 1000:n - 1]]
+    total, norms = norm(grads)
+    want = [math.sqrt(sum(float(p.double().square().sum()) for p in g.split(1 << 24 if g.dim() == 1 else 1000)))
+            for g in grads]
+    assert close(total, math.sqrt(sum(w * w for w in want)), 6 * U)
+    assert all(close(g, w, 6 * U) for g, w in zip(norms.tolist(), want))
+    dash.dash_grad_clip(grads, total, 0.5 * float(total))  # (the factor is exact)
+    inside = torch.zeros(n, dtype=torch.bool, device=DEV)
+    for g in grads:
+        inside.as_strided(g.shape, g.stride(), g.storage_offset()).fill_(True)
+    assert torch.equal(flat, torch.where(inside, old * 0.5, old))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
 def test_clip_by_any_norm(dtype):
     inf, nan = float("inf"), float("nan")
     for value, most, factor in ((0.0, 0.0, 1), (5.0, 0.0, 0), (1.0, inf, 1), (inf, inf, 1), (inf, 1.0, 0), (nan, 1.0, nan),

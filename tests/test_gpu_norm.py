@@ -10,9 +10,10 @@ least magnitude.
 The gradient.  xhat and m carry u each.  The mean c adds n products in chains of at most 32 in a thread (n / 1024
 + 8 for rows longer than 16384), 6 steps in a wave and up to 16 waves: L = chain + 24 roundings of the sum of
 magnitudes.  dx = dh + rstd (m - xhat c): 4u (|m| + |xhat c|) rstd + rstd |xhat| (L u mean |m xhat|) + u |dx|,
-then its own rounding.  dgain adds rows in at most 512 shares, in each a chain of T / 512 + 1 rows (rows side by
-side: up to 256 of them are added after that), the shares in 64 bits: (T / 512 + 260) u of the sum of
-magnitudes."""
+then its own rounding.  dgain adds rows in at least min(T, 256) and at most 512 shares, in each rows side by side
+(the wider the rows the fewer) whose chains take every `side by side`-th row: at most T / 256 + 1 of them, which the
+joins of those (9 halvings) and of the shares (64 bits) follow; few rows in chains of T / 32: (T / 256 + 260) u of
+the sum of magnitudes covers all."""
 import numpy as np
 import pytest
 import torch
@@ -218,6 +219,25 @@ def test_norm_past_32_bit_offsets():
     assert torch.equal(x_out, dx) and not bool(wide[:, 100 + n:].any()) and not bool(wide[:, n:100].any())
 
 
+LARGE = [(30001, 2047, torch.bfloat16), (9000, 8192, torch.bfloat16), (2300, 32000, torch.float16),
+         (30000, 2048, torch.float32), (15001, 4095, torch.float32), (7000, 8192, torch.float32),
+         (4000, 16384, torch.float32)]
+LARGE_IDS = ["%dx%d-%s" % (T, n, NAMES[t]) for T, n, t in LARGE]
+
+
+@pytest.mark.parametrize("T,n,dtype", LARGE, ids=LARGE_IDS)
+def test_large_calls_equal_their_parts(T, n, dtype):
+    """A row's results do not depend on how many others there are (calls beyond the caches' size store past them)."""
+    x, r = randn(130, T, n, dtype=dtype), randn(131, T, n, dtype=dtype)
+    gain = 1 + randn(132, n, scale=0.3)
+    whole = norm(x, r, gain)
+    for a, b in ((0, 700), (T // 2, T // 2 + 601), (T - 650, T)):
+        part = norm(x[a:b], r[a:b], gain)
+        for w, p in zip(whole, part):
+            w = w[0] if w.dim() == 3 else w
+            assert torch.equal(w[a:b], p[0] if p.dim() == 3 else p)
+
+
 # ------------------------------------------------------------------------------------------------
 # The gradient
 # ------------------------------------------------------------------------------------------------
@@ -236,7 +256,7 @@ def check_back(dy, h, rstd, gain, dh, dx, dgain, old=None):
     assert bool(((dx.double() - want).abs() <= tol).all())
     if dgain is not None:
         want = (d * xhat).sum(0) + (0 if old is None else old.double())
-        tol = (T / 512 + 260) * U * (d * xhat).abs().sum(0) + U * want.abs() + 2.0**-149
+        tol = (T / 256 + 260) * U * (d * xhat).abs().sum(0) + U * want.abs() + 2.0**-149
         assert bool(((dgain.double() - want).abs() <= tol).all())
 
 
@@ -271,6 +291,39 @@ def test_gradient(T, n, dtype):
         if not accumulate:
             assert torch.equal(again, dgain)  # equal calls, equal bits
         assert torch.equal(back(dy, h, rstd, gain, dh), dx)  # without dgain
+
+
+@pytest.mark.parametrize("T,n,dtype", LARGE, ids=LARGE_IDS)
+def test_large_gradients(T, n, dtype):
+    h, dy, dh = (randn(140 + i, T, n, dtype=dtype) for i in range(3))
+    rstd = torch.cat([((h[i:i + 1000].double() ** 2).mean(1) + EPS).rsqrt().float() for i in range(0, T, 1000)])
+    gain, dgain = 1 + randn(143, n, scale=0.3), torch.empty(n, device=DEV)
+    dx = back(dy, h, rstd, gain, dh, dgain=dgain)
+    want, mag = (torch.zeros(n, dtype=torch.float64, device=DEV) for _ in range(2))
+    for i in range(0, T, 1000):
+        rows = slice(i, i + 1000)
+        check_back(dy[rows], h[rows], rstd[rows], gain, dh[rows], dx[rows], None)
+        terms = dy[rows].double() * h[rows].double() * rstd[rows].double()[:, None]
+        want += terms.sum(0)
+        mag += terms.abs().sum(0)
+    assert bool(((dgain.double() - want).abs() <= (T / 256 + 260) * U * mag).all())
+    part = back(dy[:600], h[:600], rstd[:600], gain, dh[:600])
+    assert torch.equal(part, dx[:600])
+
+
+@pytest.mark.parametrize("T,n", [(1, 8), (100, 1001), (512, 2048), (512, 5001), (300, 16000), (513, 2048)])
+def test_gradient_of_few_rows(T, n):
+    """dgain of few rows by one launch, or (dx in dy's place) by two: near each other and the definition."""
+    for dtype in TYPES:
+        h, dy = randn(150, T, n, dtype=dtype), randn(151, T, n, dtype=dtype)
+        rstd = ((h.double() ** 2).mean(1) + EPS).rsqrt().float()
+        old = randn(152, n)
+        for accumulate in (False, True):
+            one, two, over = old.clone(), old.clone(), dy.clone()
+            dx = back(dy, h, rstd, dgain=one, accumulate=accumulate)
+            assert torch.equal(back(over, h, rstd, dx=over, dgain=two, accumulate=accumulate), dx)
+            for dgain in (one, two):
+                check_back(dy, h, rstd, None, None, dx, dgain, old if accumulate else None)
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
