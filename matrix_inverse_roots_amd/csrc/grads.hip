@@ -4,7 +4,7 @@
 //
 // One read for the norm, one read and one write for the clipping: the bytes over the memory bandwidth is
 // their time.  The tensors' descriptors travel as kernel arguments, GROUP_TENSORS to a launch; every tensor is cut into
-// pieces of 16 bytes along its rows and shared out evenly over workgroups, `per_wg` pieces each.  Sums are kept
+// pieces of 16 bytes along its rows, and `per_wg` of them go to a workgroup.  Sums are kept
 // in 64 bits, so that neither large nor small elements leave their range, and joined in a fixed order: equal
 // calls give equal bits.
 #include <hip/hip_runtime.h>
@@ -94,18 +94,19 @@ __device__ __forceinline__ void each_piece(const Pieces<T>& v, int64_t first, in
   }
 }
 
-constexpr int DEPTH = 4;
+// Pieces that a thread has under way together (the norm of 6.4 GB with 2 / 4: 935 / 961 us)
+constexpr int READ_DEPTH = 2, WRITE_DEPTH = 2;
 
 template <bool PAST, typename T>
 __device__ __forceinline__ double squares(const Tensors& g, int t, int64_t first, int64_t most, int thread, int threads) {
   double s = 0.;
-  each_piece<DEPTH>(Pieces<T>(g, t), first, most, thread, threads, [&](T* const* row, const int64_t* c,
+  each_piece<READ_DEPTH>(Pieces<T>(g, t), first, most, thread, threads, [&](T* const* row, const int64_t* c,
                                                                        const int64_t* len) {
-    vec_of<T> v[DEPTH];
+    vec_of<T> v[READ_DEPTH];
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) v[k] = load_short<PAST>(row[k], c[k], len[k]);
+    for (int k = 0; k < READ_DEPTH; ++k) v[k] = load_short<PAST>(row[k], c[k], len[k]);
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) {
+    for (int k = 0; k < READ_DEPTH; ++k) {
       float x[EACH<T>];
 #pragma unroll
       for (int q = 0; q < EACH<T>; ++q) x[q] = (float)v[k][q];
@@ -187,13 +188,13 @@ __global__ __launch_bounds__(1024) void grad_norm_kernel(const double* part, con
 template <bool PAST, typename T>
 __device__ __forceinline__ void clip_tensor(const Tensors& g, int t, float factor) {
   const int64_t first = (int64_t)((int)blockIdx.x - g.wg_base[t]) * g.per_wg;
-  each_piece<DEPTH>(Pieces<T>(g, t), first, g.per_wg, threadIdx.x, 256, [&](T* const* row, const int64_t* c,
+  each_piece<WRITE_DEPTH>(Pieces<T>(g, t), first, g.per_wg, threadIdx.x, 256, [&](T* const* row, const int64_t* c,
                                                                             const int64_t* len) {
-    vec_of<T> v[DEPTH];
+    vec_of<T> v[WRITE_DEPTH];
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) v[k] = load_short<PAST>(row[k], c[k], len[k]);
+    for (int k = 0; k < WRITE_DEPTH; ++k) v[k] = load_short<PAST>(row[k], c[k], len[k]);
 #pragma unroll
-    for (int k = 0; k < DEPTH; ++k) {
+    for (int k = 0; k < WRITE_DEPTH; ++k) {
       float x[EACH<T>];
 #pragma unroll
       for (int q = 0; q < EACH<T>; ++q) x[q] = (float)v[k][q] * factor;
@@ -232,14 +233,16 @@ struct Shape {
   int64_t workgroups(int64_t per_wg) const { return pieces ? (pieces + per_wg - 1) / per_wg : 1; }
 };
 
-// How a list is shared out: pieces of a workgroup, and workgroups in all
+// How a list is shared out: pieces of a workgroup, and workgroups in all.  Clipping takes one pass of every thread (0.8
+// GB of bfloat16 257 us; 16384 workgroups that loop 300), up to 2^22 workgroups.  The norm takes two passes, up to
+// 65536 workgroups, whose sums one more launch adds (6.4 GB: 923 us, with 16384 of them 935, with 393216 1159).
 struct Share {
   int64_t per_wg, wgs;
   bool small;  // for grad_norm_small_kernel
   bool past;   // the caches: they hold no part of it until the next pass
 };
 constexpr int64_t SMALL_PIECES = 512;
-Share share_out(const dash_tensor* g, int n) {
+Share share_out(const dash_tensor* g, int n, bool write) {
   int64_t all = 0, most = 0;
   for (int i = 0; i < n; ++i) {
     const int64_t p = Shape(g[i]).pieces;
@@ -247,7 +250,8 @@ Share share_out(const dash_tensor* g, int n) {
     if (p > most) most = p;
   }
   Share s;
-  const int64_t least = 256 * DEPTH, even = (all / 16384 + least - 1) / least * least;
+  const int64_t step = 256 * (write ? WRITE_DEPTH : READ_DEPTH), least = write ? step : 2 * step;
+  const int64_t even = (all / (write ? 1 << 22 : 1 << 16) + step - 1) / step * step;
   s.per_wg = even > least ? even : least;
   s.past = all > LARGE_BYTES / 16;
   s.small = n <= 64 && most <= SMALL_PIECES;
@@ -291,11 +295,11 @@ hipError_t each_group(const dash_tensor* t, int n, const Share& s, F f) {
 }  // namespace
 
 size_t grad_norm_workspace_bytes(const dash_tensor* t, int n) {
-  return align_up((size_t)share_out(t, n).wgs * sizeof(double), 256) + (size_t)n * sizeof(int64_t);
+  return align_up((size_t)share_out(t, n, false).wgs * sizeof(double), 256) + (size_t)n * sizeof(int64_t);
 }
 
 hipError_t launch_grad_norm(const dash_tensor* t, int n, float* norm, float* norms, void* ws, hipStream_t stream) {
-  const Share s = share_out(t, n);
+  const Share s = share_out(t, n, false);
   if (s.small && n) {
     return each_group(t, n, s, [&](const Tensors& g, int64_t) {
       hipLaunchKernelGGL(grad_norm_small_kernel, dim3(1), dim3(1024), 0, stream, g, norm, norms);
@@ -314,7 +318,7 @@ hipError_t launch_grad_norm(const dash_tensor* t, int n, float* norm, float* nor
 }
 
 hipError_t launch_grad_clip(const dash_tensor* t, int n, const float* norm, float most, hipStream_t stream) {
-  const Share s = share_out(t, n);
+  const Share s = share_out(t, n, true);
   return each_group(t, n, s, [&](const Tensors& g, int64_t wgs) {
     hipLaunchKernelGGL(s.past ? grad_clip_kernel<true> : grad_clip_kernel<false>, dim3((unsigned)wgs), dim3(256), 0,
                        stream, g, norm, most);
