@@ -588,7 +588,7 @@ dash_status dash_rmsnorm_backward_workspace(int64_t T, int64_t n, size_t* bytes)
  * ld >= cols; without elements (rows or cols 0) its norm is 0 and ptr may be NULL.  Sums are kept in 64 bits: the
  * norm of finite elements is right unless it leaves fp32's range itself.  Equal calls give equal bits.  An Inf or
  * NaN among the elements makes the norm Inf or NaN.  (Over several GPUs: the root of the sum of squared norms.)
- * ws: dash_grad_norm_workspace bytes for these descriptors' sizes and types, 256-byte aligned. */
+ * ws: dash_grad_norm_workspace bytes for descriptors of these sizes, pitches and types, 256-byte aligned. */
 dash_status dash_grad_norm(const dash_tensor* grads, int32_t n, float* norm, float* norms, void* ws, size_t ws_bytes,
                            void* stream);
 dash_status dash_grad_norm_workspace(const dash_tensor* grads, int32_t n, size_t* bytes);

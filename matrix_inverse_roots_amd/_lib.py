@@ -154,7 +154,7 @@ class _Args:
     def __init__(self, call: str):
         self.call = call
         self.device = None
-        self.index = -1  # of that device
+        self.index = None  # of that device
 
     def _tensor(self, t, name):
         if _torch_module is None and not _torch_loaded():  # (raw addresses need no torch)
@@ -176,7 +176,7 @@ class _Args:
         at least `numel` elements."""
         if t is None or t.__class__ is int:
             return t
-        if self._tensor(t, name):
+        if (t.__class__ is _Tensor and t.get_device() == self.index) or self._tensor(t, name):
             want = _dtypes.get(dtype)
             if want is not None and t.dtype != want:
                 raise ValueError("%s: %s must be %s, got %s" % (self.call, name, dtype, t.dtype))
@@ -217,7 +217,8 @@ class _Args:
         """(pointer, dash_prec type, row pitch) of N row-major matrices of rows x cols, one after the
         other: a tensor [rows, cols] (N = 1) or [N, rows, cols] of float32, float16 or bfloat16 with unit
         column stride and matrices rows * pitch apart, or a raw pointer with type and ld given."""
-        if t is None or t.__class__ is int or not self._tensor(t, name):
+        if t is None or t.__class__ is int or not ((t.__class__ is _Tensor and t.get_device() == self.index) or
+                                                   self._tensor(t, name)):
             p = t if t is None or isinstance(t, int) else t.data_ptr()
             return p, DASH_FP32 if type is None else type, cols if ld is None else ld
         have = _precs.get(t.dtype)
@@ -274,7 +275,7 @@ class _Args:
         stride, of float32, float16 or bfloat16; a GradList's own."""
         if isinstance(ts, GradList):
             if ts.index is not None:
-                if self.index not in (-1, ts.index):
+                if self.index not in (None, ts.index):
                     raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, ts.device,
                                                                                           self.device))
                 self.device, self.index = ts.device, ts.index
@@ -329,7 +330,7 @@ class GradList:
         self.tensors = tuple(tensors)
         a = _Args("grad_list")
         self.array = a.tensors(self.tensors, "tensors")
-        self.device, self.index = a.device, a.index if a.device is not None else None
+        self.device, self.index = a.device, a.index
         self._mats = None
 
     def __len__(self):

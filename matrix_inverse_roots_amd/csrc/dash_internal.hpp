@@ -265,7 +265,7 @@ size_t evd_workspace_bytes(int64_t N, int B);
 // Stack / unstack n weights: the ceil(rows/B) x ceil(cols/B) tiles of each, in order, into
 // consecutive blocks of `stack` (to_stack) or back out of it; the part of an edge tile outside the
 // weight is zero in the stack and not written back.  One launch per COPY_GROUP weights.
-constexpr int COPY_GROUP = 32;
+constexpr int COPY_GROUP = 80;  // (of 48 bytes each: kernel arguments hold 4 KiB)
 struct CopyGroup {
   float* ptr[COPY_GROUP];
   int64_t ld[COPY_GROUP];

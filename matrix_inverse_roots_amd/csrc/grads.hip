@@ -253,7 +253,7 @@ Share share_out(const dash_tensor* g, int n, bool write) {
   const int64_t step = 256 * (write ? WRITE_DEPTH : READ_DEPTH), least = write ? step : 2 * step;
   const int64_t even = (all / (write ? 1 << 22 : 1 << 16) + step - 1) / step * step;
   s.per_wg = even > least ? even : least;
-  s.past = all > LARGE_BYTES / 16;
+  s.past = all * (write ? 32 : 16) > LARGE_BYTES;
   s.small = n <= 64 && most <= SMALL_PIECES;
   s.wgs = 0;
   for (int i = 0; i < n; ++i) s.wgs += Shape(g[i]).workgroups(s.per_wg);

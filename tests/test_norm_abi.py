@@ -151,6 +151,19 @@ def test_gradient_norm_refusals():
     assert f(P[10]) == WS and f(P[9], ws=P[0]) == WS
 
 
+def test_the_norm_s_workspace_does_not_go_by_addresses():
+    size = ctypes.c_size_t()
+    for rows, cols, ld in ((1, 5, 5), (1, 4096, 4096), (1, 1 << 20, 1 << 20), (300, 257, 300), (3000, 64, 80), (1, 1 << 33,
+                           1 << 33)):
+        for dtype, step in ((FP32, 4), (BF16, 2)):
+            got = set()
+            for off in range(0, 16, step):
+                arr = tensors((P[0] + off, rows, cols, ld, dtype), (P[1] + off, 1, 77, 77, dtype))
+                assert dash.library().dash_grad_norm_workspace(arr, 2, ctypes.byref(size)) == 0
+                got.add(size.value)
+            assert len(got) == 1
+
+
 def test_clip_refusals():
     lib = dash.library()
     arr = tensors(GOOD)
