@@ -62,9 +62,12 @@ __device__ __forceinline__ float gain_at(const void* gain, dash_prec type, int64
 // `shared` holds a value per wave.
 template <typename S>
 __device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
-  for (int o = 1; o < 64 && o < lanes; o *= 2) v += __shfl_xor(v, o, 64);
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2)
+    if (o < lanes) v += of_lane_xor(v, o);
   if (lanes > 64) {
-    const int wave = threadIdx.x >> 6, waves = lanes >> 6, first = wave / waves * waves;
+    const int wave = threadIdx.x >> 6, waves = lanes >> 6;
+    const int first = waves == (int)(blockDim.x >> 6) ? 0 : wave / waves * waves;
     __syncthreads();  // (the last row's values have been read)
     if ((threadIdx.x & 63) == 0) shared[wave] = v;
     __syncthreads();
@@ -81,7 +84,7 @@ __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int6
 #pragma unroll
   for (int q = 0; q < E; ++q) top = umax(top, mag_bits(y[q]));
 #pragma unroll
-  for (int o = 1; o < GROUP / E; o *= 2) top = umax(top, __shfl_xor(top, o, 64));
+  for (int o = 1; o < GROUP / E; o *= 2) top = umax(top, of_lane_xor(top, o));
   const unsigned byte = scale_byte<F>(top);
   typedef typename Codes<F>::raw4 raw4;
   typedef raw4 raw_t __attribute__((ext_vector_type(E / 4)));
@@ -332,6 +335,7 @@ __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lan
     const int64_t c = (int64_t)E * (lane + k * a.lanes);
     dy[k] = load_piece<PAST>((const T*)a.dy + row * a.lddy, c, n);
     h[k] = load_piece<PAST>((const T*)a.h + row * a.ldh, c, n);
+    dh[k] = minus_zeros<T>();
     if (a.dh) dh[k] = load_piece<PAST>((const T*)a.dh + row * a.lddh, c, n);
   }
   const float rstd = row < a.T ? a.rstd[row] : 0.f;
@@ -355,7 +359,7 @@ __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lan
 #pragma unroll
     for (int q = 0; q < E; ++q) {
       const float xhat = (float)h[k][q] * rstd;
-      dx[q] = fmaf(rstd, fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]), a.dh ? (float)dh[k][q] : 0.f);
+      dx[q] = fmaf(rstd, fmaf(-xhat, mean, (float)dy[k][q] * g[k][q]), (float)dh[k][q]);
     }
     store_piece<PAST>((T*)a.dx + row * a.lddx, c, n, dx);
   }

@@ -57,6 +57,13 @@ __device__ __forceinline__ auto load_elements(const T* row, int64_t c, int64_t n
   }
   return v;
 }
+// A piece of -0, which changes nothing that it is added to
+template <typename T>
+__device__ __forceinline__ vec_of<T> minus_zeros() {
+  typedef unsigned words_t __attribute__((ext_vector_type(4)));
+  const unsigned w = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
+  return __builtin_bit_cast(vec_of<T>, words_t{w, w, w, w});
+}
 // Elements c .. c + EACH - 1 of a row of n, zero beyond it; n >= EACH, or 0
 template <bool PAST = false, typename T>
 __device__ __forceinline__ vec_of<T> load_piece(const T* row, int64_t c, int64_t n) {
@@ -106,18 +113,41 @@ __device__ __forceinline__ void store_piece(T* row, int64_t c, int64_t n, const 
   }
 }
 
+// v of the lane whose number differs in the bits `o`; one instruction a word (__shfl_xor checks the number, too)
+template <typename S>
+__device__ __forceinline__ S of_lane_xor(S v, int o) {
+  const int from = (int)(((threadIdx.x & 63) ^ (unsigned)o) << 2);
+  if constexpr (sizeof(S) == 8) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)w);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)(w >> 32));
+    return __builtin_bit_cast(S, (uint64_t)hi << 32 | lo);
+  } else {
+    return __builtin_bit_cast(S, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, v)));
+  }
+}
+
 // x_0^2 + ... + x_{E-1}^2 in 64 bits.  Formed in 32 bits where neither the sum leaves their range nor a term
-// that matters falls below it (the sum is then off by at most E roundings of 2^-24 of it); else, a sum of
-// zeros too, term by term in 64.
+// that matters falls below it (the sum is then off by at most E roundings of 2^-24 of it); else term by term in
+// 64, on a branch that a wave takes only if a lane needs it (as a choice of two values it would always pay).
 template <int E>
 __device__ __forceinline__ double sum_squares(const float* x) {
   float s = x[0] * x[0];
 #pragma unroll
   for (int q = 1; q < E; ++q) s = fmaf(x[q], x[q], s);
-  if (s >= 0x1p-96f && s <= 0x1p126f) return (double)s;
-  double d = 0.;
+  const bool out = !(s >= 0x1p-96f && s <= 0x1p126f);
+  double d = (double)s;
+  if (__ballot(out)) {
+    unsigned any = 0;
 #pragma unroll
-  for (int q = 0; q < E; ++q) d = fma((double)x[q], (double)x[q], d);
+    for (int q = 0; q < E; ++q) any |= __builtin_bit_cast(unsigned, x[q]) << 1;
+    if (__ballot(out && any != 0)) {
+      double t = 0.;
+#pragma unroll
+      for (int q = 0; q < E; ++q) t = fma((double)x[q], (double)x[q], t);
+      if (out) d = t;
+    }
+  }
   return d;
 }
 
