@@ -77,6 +77,21 @@ __device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
   return v;
 }
 
+// rstd in two fp32 parts that add up to it, and h rstd g rounded once from them: the codes' own rounding then meets
+// next to no values that lie on the other side of a border than h rstd g does.
+struct Root {
+  float rstd, rest;
+  __device__ __forceinline__ Root(double square) {
+    const double r = rsqrt(square);
+    rstd = (float)r;
+    rest = (float)(r - (double)rstd);
+  }
+  __device__ __forceinline__ float times(float h, float g) const {
+    const float t = h * rstd, e = fmaf(h, rest, fmaf(h, rstd, -t));
+    return fmaf(t, g, e * g);
+  }
+};
+
 // One piece of y as codes; the scale byte from the first lane of its group
 template <int F, int E, bool PAST>
 __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int64_t c, uint8_t* codes, uint8_t* scales) {
@@ -132,8 +147,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   }
   s = row_sum(s, a.lanes, shared);
   if (!live) return;
-  const float rstd = (float)rsqrt(fma(s, a.over_n, a.eps));
-  if (a.rstd && lane == 0) a.rstd[row] = rstd;
+  const Root root(fma(s, a.over_n, a.eps));
+  if (a.rstd && lane == 0) a.rstd[row] = root.rstd;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int64_t c = (int64_t)E * (lane + k * a.lanes);
@@ -141,7 +156,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
     if (a.h) store_piece<PAST>((T*)a.h + row * a.ldh, c, a.n, h[k]);
     float y[E];
 #pragma unroll
-    for (int q = 0; q < E; ++q) y[q] = h[k][q] * rstd * g[k][q];
+    for (int q = 0; q < E; ++q) y[q] = root.times(h[k][q], g[k][q]);
     if (a.y) store_piece<PAST>((T*)a.y + row * a.ldy, c, a.n, y);
     if (a.codes) store_codes<F, E, PAST>(y, row * groups, c, a.codes, a.scales);
   }
@@ -170,8 +185,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
     s += sum_squares<E>(h);
   }
   s = row_sum(s, 1024, shared);
-  const float rstd = (float)rsqrt(fma(s, a.over_n, a.eps));
-  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  const Root root(fma(s, a.over_n, a.eps));
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = root.rstd;
   for (int64_t c = (int64_t)E * threadIdx.x; c < groups * GROUP; c += E * 1024) {
     const vec_of<T> vx = load_piece(x, c, a.n);
     float h[E], g[E], y[E];
@@ -185,7 +200,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
     }
     if (a.h) store_piece((T*)a.h + row * a.ldh, c, a.n, h);
 #pragma unroll
-    for (int q = 0; q < E; ++q) y[q] = h[q] * rstd * g[q];
+    for (int q = 0; q < E; ++q) y[q] = root.times(h[q], g[q]);
     if (a.y) store_piece((T*)a.y + row * a.ldy, c, a.n, y);
     if (a.codes) store_codes<F, E, false>(y, row * groups, c, a.codes, a.scales);
   }
@@ -206,14 +221,14 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
     if (a.res && q < n) h[q] += (float)((const T*)a.res)[row * a.ldr + q];
     s = fma((double)h[q], (double)h[q], s);
   }
-  const float rstd = (float)rsqrt(fma(s, a.over_n, a.eps));
-  if (a.rstd) a.rstd[row] = rstd;
+  const Root root(fma(s, a.over_n, a.eps));
+  if (a.rstd) a.rstd[row] = root.rstd;
   unsigned top = 0;
 #pragma unroll
   for (int q = 0; q < GROUP; ++q) {
     y[q] = 0.f;
     if (q < TINY && q < n) {
-      y[q] = h[q] * rstd * gain_at(a.gain, a.gain_type, q);
+      y[q] = root.times(h[q], gain_at(a.gain, a.gain_type, q));
       if (a.h) ((T*)a.h)[row * a.ldh + q] = (T)h[q];
       if (a.y) ((T*)a.y)[row * a.ldy + q] = (T)y[q];
     }
