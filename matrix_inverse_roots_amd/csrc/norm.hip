@@ -272,8 +272,8 @@ int row_lanes(int64_t pieces, int k) {
 // Pieces of a thread, where at most `threads` share a row.  One, so that many waves have loads under way (8192 x
 // 2048 bfloat16 with 1 / 2 / 4: 30.7 / 36.0 / 37.3 us; its gradient 31.1 / 33.4); but two where the last
 // one of a row is cut, which the wave that holds it pays for (50001 x 263: 39.6 / 35.4, gradient 50 / 42).
-int row_pieces(int64_t pieces, bool whole, int threads) {
-  int k = whole ? 1 : 2;
+int row_pieces(int64_t pieces, bool whole, int threads, int least = 1) {
+  int k = whole || least > 1 ? least : 2;
   while (pieces > (int64_t)threads * k) k *= 2;
   return k;
 }
@@ -284,9 +284,15 @@ hipError_t rmsnorm(NormArgs& a, hipStream_t stream) {
   const int64_t pieces = (a.n + GROUP - 1) / GROUP * (GROUP / E);
   if (a.n < TINY) return launch_rows(rmsnorm_tiny_kernel<T, F>, (a.T + 255) / 256, 256, a, stream);
   if (pieces > 1024 * (32 / E)) return launch_rows(rmsnorm_long_kernel<T, F>, a.T, 1024, a, stream);
-  // (fp32, with half as many elements a thread, from 512 threads on: 16384 x 4096 with 512 / 1024 198 / 206 us,
-  // 32768 x 8192 without y 604 / 619)
-  const int k = row_pieces(pieces, a.n % E == 0, E == 4 && pieces <= 2048 ? 512 : 1024);
+  // Threads of a row at most: 1024; fp32, with half as many elements each, sooner takes more of them (16384 x 4096 with
+  // 512 / 1024 threads 198 / 206 us; codes alone of 4096 x 12288 with 384 / 768 80 / 58, 4096 x 16384 with 512 / 1024
+  // 81 / 100).
+  const int most = E == 8 || pieces > 6144 ? 1024 : pieces > 2048 ? 768 : 512;
+  // Without a residual a piece is one load and not two, and needs more of them a thread: with codes alone 16 elements
+  // (65536 x 4096 bfloat16 with 1 / 2 pieces 254 / 205 us, fp32 with 2 / 4 298 / 252), with y from 512 pieces on two
+  // (287 / 249 us; 8192 x 2048 19.1 / 19.9).
+  const int least = a.res ? 1 : !a.y && !a.h ? 16 / E : pieces >= 512 ? 2 : 1;
+  const int k = row_pieces(pieces, a.n % E == 0, most, least);
   a.lanes = row_lanes(pieces, k);
   if (a.lanes < GROUP / E) a.lanes = GROUP / E;
   a.per = a.lanes < 256 ? 256 / a.lanes : 1;
