@@ -558,8 +558,9 @@ dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, das
  *   rstd:  NULL, or [T] in fp32, which dash_rmsnorm_backward takes.
  * At least one output is given; apart from h they share no memory with the inputs or with each other.
  * h enters the norm, and y its codes, in fp32 before they are rounded; the sum of squares is kept in 64 bits
- * (no row of finite elements overflows it).  eps >= 0.  A row of zeros with eps = 0 has rstd = Inf and y = NaN;
- * a NaN in a row makes its rstd and y NaN, an Inf rstd = 0, its own y NaN and the rest 0. */
+ * (no row of finite elements overflows it).  eps >= 0.  A row whose rstd passes fp32's largest number (eps = 0 and
+ * zeros, or elements all below 2.9e-39) has rstd = Inf and y = NaN; a NaN in a row makes its rstd and y NaN, an Inf
+ * rstd = 0, its own y NaN and the rest 0. */
 dash_status dash_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, dash_prec type, const void* gain,
                          dash_prec gain_type, int64_t T, int64_t n, float eps, void* h, int64_t ldh, void* y,
                          int64_t ldy, dash_mx_fmt fmt, void* codes, void* scales, float* rstd, void* stream);
@@ -594,13 +595,14 @@ dash_status dash_grad_norm(const dash_tensor* grads, int32_t n, float* norm, flo
 dash_status dash_grad_norm_workspace(const dash_tensor* grads, int32_t n, size_t* bytes);
 
 /* g_i <- g_i min(1, max_norm / norm[0]) in place for the n >= 0 gradients, which share no memory (slices of one
- * buffer with the same pitch may interleave).  max_norm >= 0.  The product is formed in fp32 and rounded once.
- * norm[0] <= max_norm leaves the gradients unread; norm[0] = Inf makes finite elements 0 and the others NaN (any
- * finite max_norm), norm[0] = NaN makes all NaN. */
+ * buffer with the same pitch may interleave).  max_norm >= 0.  The factor is rounded to fp32, the product once to
+ * the type.  norm[0] <= max_norm leaves the gradients unread; norm[0] = Inf makes finite elements 0 and the others
+ * NaN (any finite max_norm), norm[0] = NaN makes all NaN. */
 dash_status dash_grad_clip(const dash_tensor* grads, int32_t n, const float* norm, float max_norm, void* stream);
 
 /* dash_stack of clipped gradients: the tiles of g_i min(1, max_norm / norm[0]), the gradients left as they are.
- * Arguments, tiles and errors as dash_stack, norm and max_norm as dash_grad_clip. */
+ * Arguments, tiles and errors as dash_stack, norm and max_norm as dash_grad_clip; G_stack shares no memory with
+ * the gradients or norm. */
 dash_status dash_stack_clip(const dash_mat* grads, int32_t n, int32_t B, const float* norm, float max_norm,
                             float* G_stack, void* stream);
 

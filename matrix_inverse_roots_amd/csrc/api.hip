@@ -2049,7 +2049,10 @@ dash_status dash_stack_clip(const dash_mat* grads, int32_t n, int32_t B, const f
   if (st == DASH_OK) st = clip_args_check(norm, max_norm);
   if (st != DASH_OK) return st;
   if (!G_stack || !aligned(G_stack, 16)) return DASH_ERR_INVALID_ARG;
-  if (overlap(region(G_stack, tiles * B * B * 4), region(norm, 4))) return DASH_ERR_INVALID_ARG;
+  const Region out = region(G_stack, tiles * B * B * 4);
+  if (overlap(out, region(norm, 4))) return DASH_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (overlap(out, region(grads[i].ptr, grads[i].rows, grads[i].cols, grads[i].ld, 4))) return DASH_ERR_INVALID_ARG;
   TRY(launch_tile_copy(grads, n, B, G_stack, true, as_stream(stream), norm, max_norm));
   return DASH_OK;
 }

@@ -192,6 +192,9 @@ def test_clip_refusals():
     assert g(norm=P[9] + 1) == INVALID and g(most=-0.5) == INVALID and g(most=NAN) == INVALID
     assert g(ld=66) == INVALID and g(B=100) == SHAPE and g(norm=P[5] + 64 * 64 * 4 - 4) == INVALID
     assert lib.dash_stack_clip(None, 1, 64, P[9], 1.0, P[5], None) == INVALID
+    # the stack over a gradient: at its last element, behind its first, and the other way round
+    for G, ld in ((P[4] + 7 * 64 * 4 + 240, 64), (P[4] - 64 * 64 * 4 + 16, 64), (P[4], 64), (P[4] + 64 * 4, 128)):
+        assert g(grads=P[4], G=G, ld=ld) == INVALID, (G - P[4], ld)
 
 
 def test_host_tensors_and_other_types_are_refused():
