@@ -100,6 +100,7 @@ struct Codes<DASH_MX_E2M1> {
 __device__ __forceinline__ unsigned mag_bits(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
 
 __device__ __forceinline__ unsigned umax(unsigned a, unsigned b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned umin(unsigned a, unsigned b) { return a < b ? a : b; }
 
 }  // namespace
 }  // namespace dash

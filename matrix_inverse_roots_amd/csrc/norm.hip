@@ -77,8 +77,7 @@ __device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
   return v;
 }
 
-// rstd in two fp32 parts that add up to it, and h rstd g rounded once from them: the codes' own rounding then meets
-// next to no values that lie on the other side of a border than h rstd g does.
+// rstd in two fp32 parts that add up to it (48 bits)
 struct Root {
   float rstd, rest;
   __device__ __forceinline__ Root(double square) {
@@ -86,9 +85,19 @@ struct Root {
     rstd = (float)r;
     rest = (float)(r - (double)rstd);
   }
-  __device__ __forceinline__ float times(float h, float g) const {
-    const float t = h * rstd, e = fmaf(h, rest, fmaf(h, rstd, -t));
-    return fmaf(t, g, e * g);
+  // y = h rstd g, off by at most four roundings (of h, of rstd and of two products)
+  __device__ __forceinline__ float times(float h, float g) const { return h * rstd * g; }
+  // The same as the fp32 number that rounds to the code that h rstd g itself rounds to: cut off, and made odd if
+  // anything was lost, so that it is on y's side of each border of codes and of scales (they end in 19 zeros).
+  // more: what h lacks.
+  __device__ __forceinline__ float odd_times(float h, float more, float g) const {
+    const float t = h * rstd, e = fmaf(more, rstd, fmaf(h, rest, fmaf(h, rstd, -t)));
+    const float y = fmaf(t, g, e * g);
+    const float lost = fmaf(t, g, -y) + e * g;
+    unsigned bits = __builtin_bit_cast(unsigned, y);
+    if (lost == 0.f || (bits & 0x7fffffffu) >= 0x7f800000u) return y;
+    bits -= (bits ^ __builtin_bit_cast(unsigned, lost)) >> 31;
+    return __builtin_bit_cast(float, bits | 1u);
   }
 };
 
@@ -114,6 +123,58 @@ __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int6
   if (c % GROUP == 0) scales[group0 + c / GROUP] = (uint8_t)byte;
 }
 
+// x + res - h, exactly (h is their rounded sum; of 16-bit elements it is next to never rounded)
+__device__ __forceinline__ float rest_of_sum(float x, float res, float h) {
+  const float part = h - x;
+  return (x - (h - part)) + (res - part);
+}
+
+// A piece of y made ready for its codes.  Four roundings move an element across a border only if its last 19 bits are
+// next to zeros: once in a hundred waves, which form the piece again, one element after the other (the registers are
+// few).  The sum x + res of fp32 elements is rounded as often as not; of 16-bit ones next to never.
+template <typename T>
+__device__ __forceinline__ void settle(const NormArgs& a, int64_t row, int64_t c, float* y, const float* h,
+                                       const float* g, const Root& root) {
+  constexpr int E = EACH<T>;
+  constexpr unsigned NEAR = 4;
+  const auto border = [](float v) { return (__builtin_bit_cast(unsigned, v) + NEAR) << 13; };
+  unsigned least = ~0u;
+#pragma unroll
+  for (int q = 0; q < E; ++q) least = umin(least, border(y[q]));
+  if (__builtin_expect(!__ballot(least <= 2 * NEAR << 13), 1)) return;
+#pragma unroll
+  for (int q = 0; q < E; ++q) {
+    const bool near = border(y[q]) <= 2 * NEAR << 13 && y[q] != 0.f;  // (zeros are where they belong)
+    if (__builtin_expect(!__ballot(near), 1)) continue;
+    float hq = h[q], more = 0.f;
+    asm volatile("" : "+v"(hq));
+    if (sizeof(T) == 4 && a.res && near && c + q < a.n) {
+      asm volatile("" : "+v"(row));
+      more = rest_of_sum(((const float*)a.x)[row * a.ldx + c + q], ((const float*)a.res)[row * a.ldr + c + q], hq);
+    }
+    y[q] = root.odd_times(hq, more, g[q]);
+  }
+}
+
+// One piece of h = x + res; what its squares lack of those of the fp32 sums themselves, 2 sum h rest, is added to `more`
+template <typename T, int K>
+__device__ __forceinline__ void add_up(const vec_of<T>& x, const vec_of<T>& res, bool sum, float* h, float* more) {
+#pragma unroll
+  for (int q = 0; q < EACH<T>; ++q) h[q] = sum ? (float)x[q] + (float)res[q] : (float)x[q];
+  if (sizeof(T) == 2 || !sum) return;
+#pragma unroll
+  for (int q = 0; q < EACH<T>; ++q) *more = fmaf(2.f * h[q], rest_of_sum((float)x[q], (float)res[q], h[q]), *more);
+  if (K >= 4) asm volatile("" : "+v"(*more));  // (here, and not with x and res in registers until the gain is there)
+}
+template <int E>
+__device__ __forceinline__ double squares64(const float* h) {
+  double s = 0.;
+#pragma unroll
+  for (int q = 0; q < E; ++q) s = fma((double)h[q], (double)h[q], s);
+  asm volatile("" : "+v"(s));  // (one piece at a time in 64 bits: the registers are few)
+  return s;
+}
+
 template <typename T, int F, int K, bool PAST>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   constexpr int E = EACH<T>;
@@ -124,26 +185,24 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   const int64_t groups = (a.n + GROUP - 1) / GROUP;
   const T* x = (const T*)a.x + row * a.ldx;
   const T* res = (const T*)a.res + row * a.ldr;
-  float h[K][E];
+  float h[K][E], g[K][E];
+  float more = 0.f;
   {
     vec_of<T> vx[K], vr[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int64_t c = (int64_t)E * (lane + k * a.lanes);
+      const unsigned c = (unsigned)E * (lane + k * a.lanes);
       vx[k] = load_piece(x, c, live ? a.n : 0);
       if (a.res) vr[k] = load_piece(res, c, live ? a.n : 0);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int q = 0; q < E; ++q) h[k][q] = a.res ? (float)vx[k][q] + (float)vr[k][q] : (float)vx[k][q];
+    for (int k = 0; k < K; ++k) add_up<T, K>(vx[k], vr[k], a.res != nullptr, h[k], &more);
   }
-  float g[K][E];
-  double s = 0.;
+  double s = isfinite(more) ? (double)more : 0.;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k) {  // (the gain on its way before the sums: 8192 x 2048 bfloat16 36 -> 32 us)
     load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
-    s += sum_squares<E>(h[k]);
+    s += squares64<E>(h[k]);
   }
   s = row_sum(s, a.lanes, shared);
   if (!live) return;
@@ -151,14 +210,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   if (a.rstd && lane == 0) a.rstd[row] = root.rstd;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int64_t c = (int64_t)E * (lane + k * a.lanes);
+    const unsigned c = (unsigned)E * (lane + k * a.lanes);
     if (c >= groups * GROUP) break;  // (the lanes of a group together)
-    if (a.h) store_piece<PAST>((T*)a.h + row * a.ldh, c, a.n, h[k]);
     float y[E];
 #pragma unroll
     for (int q = 0; q < E; ++q) y[q] = root.times(h[k][q], g[k][q]);
     if (a.y) store_piece<PAST>((T*)a.y + row * a.ldy, c, a.n, y);
-    if (a.codes) store_codes<F, E, PAST>(y, row * groups, c, a.codes, a.scales);
+    if (a.codes) {
+      settle<T>(a, row, c, y, h[k], g[k], root);
+      store_codes<F, E, PAST>(y, row * groups, c, a.codes, a.scales);
+    }
+    if (a.h) store_piece<PAST>((T*)a.h + row * a.ldh, c, a.n, h[k]);  // (last: it may take the place of x or res)
   }
 }
 
@@ -174,15 +236,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
   double s = 0.;
   for (int64_t c = (int64_t)E * threadIdx.x; c < a.n; c += E * 1024) {
     const vec_of<T> vx = load_piece(x, c, a.n);
+    vec_of<T> vr;
+    if (a.res) vr = load_piece(res, c, a.n);
     float h[E];
-#pragma unroll
-    for (int q = 0; q < E; ++q) h[q] = (float)vx[q];
-    if (a.res) {
-      const vec_of<T> vr = load_piece(res, c, a.n);
-#pragma unroll
-      for (int q = 0; q < E; ++q) h[q] += (float)vr[q];
-    }
-    s += sum_squares<E>(h);
+    float more = 0.f;
+    add_up<T, 1>(vx, vr, a.res != nullptr, h, &more);
+    s += squares64<E>(h) + (isfinite(more) ? (double)more : 0.);
   }
   s = row_sum(s, 1024, shared);
   const Root root(fma(s, a.over_n, a.eps));
@@ -198,11 +257,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
 #pragma unroll
       for (int q = 0; q < E; ++q) h[q] += (float)vr[q];
     }
-    if (a.h) store_piece((T*)a.h + row * a.ldh, c, a.n, h);
 #pragma unroll
     for (int q = 0; q < E; ++q) y[q] = root.times(h[q], g[q]);
     if (a.y) store_piece((T*)a.y + row * a.ldy, c, a.n, y);
-    if (a.codes) store_codes<F, E, false>(y, row * groups, c, a.codes, a.scales);
+    if (a.codes) {
+      settle<T>(a, row, c, y, h, g, root);
+      store_codes<F, E, false>(y, row * groups, c, a.codes, a.scales);
+    }
+    if (a.h) store_piece((T*)a.h + row * a.ldh, c, a.n, h);
   }
 }
 
@@ -213,13 +275,15 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
   const int64_t row = (a.first_wg + blockIdx.x) * 256 + threadIdx.x;
   if (row >= a.T) return;
   const int n = (int)a.n;
-  float h[TINY], y[GROUP];
+  float h[TINY], more[TINY], y[GROUP];
   double s = 0.;
 #pragma unroll
   for (int q = 0; q < TINY; ++q) {
-    h[q] = q < n ? (float)((const T*)a.x)[row * a.ldx + q] : 0.f;
-    if (a.res && q < n) h[q] += (float)((const T*)a.res)[row * a.ldr + q];
-    s = fma((double)h[q], (double)h[q], s);
+    const double x = q < n ? (double)(float)((const T*)a.x)[row * a.ldx + q] : 0.;
+    const double r = a.res && q < n ? (double)(float)((const T*)a.res)[row * a.ldr + q] : 0.;
+    h[q] = (float)(x + r);
+    more[q] = isfinite(h[q]) ? (float)(x + r - (double)h[q]) : 0.f;
+    s = fma(x + r, x + r, s);
   }
   const Root root(fma(s, a.over_n, a.eps));
   if (a.rstd) a.rstd[row] = root.rstd;
@@ -228,9 +292,10 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
   for (int q = 0; q < GROUP; ++q) {
     y[q] = 0.f;
     if (q < TINY && q < n) {
-      y[q] = root.times(h[q], gain_at(a.gain, a.gain_type, q));
+      const float g = gain_at(a.gain, a.gain_type, q);
+      y[q] = root.odd_times(h[q], more[q], g);
       if (a.h) ((T*)a.h)[row * a.ldh + q] = (T)h[q];
-      if (a.y) ((T*)a.y)[row * a.ldy + q] = (T)y[q];
+      if (a.y) ((T*)a.y)[row * a.ldy + q] = (T)root.times(h[q], g);
     }
     top = umax(top, mag_bits(y[q]));
   }

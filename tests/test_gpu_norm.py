@@ -133,14 +133,42 @@ def test_h_in_the_place_of_an_input(T, n, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=IDS)
-@pytest.mark.parametrize("T,n", [(5, 6), (9, 263), (700, 1024), (2, 40000)])
-def test_codes_are_the_quantised_y(T, n, fmt):
-    """In fp32 y is what the codes are made from: dash_mx_quantize of it gives the same bytes."""
-    x, gain = randn(40, T, n, scale=5), 1 + randn(41, n, scale=0.3)
-    _, y, codes, scales, _ = norm(x, None, gain, fmt)
-    c, s = dash.mx_buffers(1, T, n, fmt, device=DEV)
-    dash.dash_mx_quantize(y, 1, T, n, fmt, c, s)
-    assert torch.equal(c, codes) and torch.equal(s, scales)
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("T,n", [(5, 6), (9, 263), (300, 1024), (2, 40000)])
+def test_codes_are_those_of_64_bits(T, n, dtype, fmt):
+    """Every byte is the definition's: y is rounded once.  (The call's y is within 2^-44 of it, at fewer than 2^19
+    elements of which one in 2^20 a step of 2^-24 lies next to a border: 2^-20 of them on the other side.)"""
+    for res in (False, True):
+        x, gain = randn(40, T, n, scale=5, dtype=dtype), 1 + randn(41, n, scale=0.3)
+        r = randn(42, T, n, dtype=dtype) if res else None
+        _, _, codes, scales, _ = norm(x, r, gain, fmt)
+        want, byte = ref.quantize(definition(x, r, gain)[2].cpu().numpy(), fmt)
+        assert np.array_equal(codes.cpu().numpy()[0], ref.pack(want, fmt))
+        assert np.array_equal(scales.cpu().numpy()[0], byte)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=IDS)
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("n", [7, 64, 1024, 8208, 33024])
+def test_codes_next_to_borders(n, dtype, fmt):
+    """Rows of one magnitude (of any size), for which y = +-gain, and gains one step of 2^-24 to either side of the
+    borders between codes (and of scales, in groups of their own)."""
+    t = ref.grid(fmt)
+    mid = (t[1:] + t[:-1]) / 2
+    rng = np.random.default_rng(7)
+    g = rng.choice(mid[len(mid) // 3:], n) / 4
+    g[32::64] = ref.TOP[fmt] / 8  # (the groups' largest elements: some are borders of scales)
+    gain = np.nextafter(g.astype(np.float32), (2 * rng.integers(0, 2, n) * g.max()).astype(np.float32))
+    assert gain.dtype == np.float32 and np.all(gain != g)
+    T = 40
+    size = torch.tensor(rng.uniform(0.1, 100, T), device=DEV)[:, None].to(dtype)
+    sign = torch.tensor(rng.choice([-1.0, 1.0], (T, n)), device=DEV).to(dtype)
+    x = size * sign
+    for res in (None, (size * 0.377).to(dtype) * sign):
+        got = norm(x, res, torch.tensor(gain, device=DEV), fmt, eps=0.0, y=False)
+        want, byte = ref.quantize(sign.double().cpu().numpy() * gain.astype(np.float64), fmt)
+        assert np.array_equal(got[2].cpu().numpy()[0], ref.pack(want, fmt)), res is None
+        assert np.array_equal(got[3].cpu().numpy()[0], byte)
 
 
 def test_each_output_alone():
