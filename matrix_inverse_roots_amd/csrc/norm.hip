@@ -175,6 +175,10 @@ __device__ __forceinline__ double squares64(const float* h) {
   return s;
 }
 
+// Rows side by side in a workgroup, each in the registers of its `lanes` threads from its only read on.  HBM bounds it:
+// 8192 x 2048 bfloat16 with residual, y and codes 30.6 us (152 MB, 5.0 TB/s), 65536 x 4096 390 us (6.2 TB/s), 32768 x
+// 8192 fp32 without y 599 us (5.8 TB/s).  Codes alone, where more instructions come to a byte: 65536 x 4096 bfloat16
+// 208 us (3.9 TB/s).
 template <typename T, int F, int K, bool PAST>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   constexpr int E = EACH<T>;
@@ -198,7 +202,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < K; ++k) add_up<T, K>(vx[k], vr[k], a.res != nullptr, h[k], &more);
   }
-  double s = isfinite(more) ? (double)more : 0.;
+  double s = isfinite(more) ? (double)more : 0.;  // (h beyond 1e22 may overflow it)
 #pragma unroll
   for (int k = 0; k < K; ++k) {  // (the gain on its way before the sums: 8192 x 2048 bfloat16 36 -> 32 us)
     load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
@@ -224,7 +228,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   }
 }
 
-// Rows that the registers of a workgroup do not hold: x and res are read twice
+// Rows that the registers of a workgroup do not hold: x and res are read twice, the second time from the caches (2000
+// x 40000 bfloat16 with residual, y and codes 172 us; 723 MB at the rate of a copy 153)
 template <typename T, int F>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
   constexpr int E = EACH<T>;
@@ -268,7 +273,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
   }
 }
 
-// Rows of fewer than 8 elements, which no 16-byte piece fits: a thread each
+// Rows of fewer than 8 elements, which no 16-byte piece fits: a thread each.  A wave's access is not one run, and a group
+// of codes is mostly padding: 2^21 x 4 fp32 with residual, y and codes 65 us (212 MB at the rate of a copy 45).
 constexpr int TINY = 8;
 template <typename T, int F>
 __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
@@ -322,7 +328,8 @@ hipError_t launch_rows(K kernel, int64_t grid, int block, A& a, hipStream_t stre
 
 template <typename T, int F, int K>
 hipError_t rmsnorm_rows(NormArgs& a, hipStream_t stream) {
-  return launch_rows(a.past ? rmsnorm_kernel<T, F, K, true> : rmsnorm_kernel<T, F, K, false>, (a.T + a.per - 1) / a.per, a.per * a.lanes, a, stream);
+  return launch_rows(a.past ? rmsnorm_kernel<T, F, K, true> : rmsnorm_kernel<T, F, K, false>,
+                     (a.T + a.per - 1) / a.per, a.per * a.lanes, a, stream);
 }
 
 // Threads for a row of `pieces`, k each: whole waves, or within one a power of two
@@ -454,7 +461,8 @@ __device__ __forceinline__ void back_row(const BackArgs& a, int64_t row, int lan
 // `per` rows side by side, then the next ones a grid further (the workgroups together read one run of rows:
 // 32768 x 8192 bfloat16 417 -> 395 us over a run of rows for each).  Every thread keeps the sums dy xhat of
 // its columns in registers, and the workgroup stores one row of them at the end: equal calls add in the same
-// order.
+// order.  HBM bounds it: that case now takes 375 us (2.15 GB, 5.7 TB/s); 50001 x 263 fp32, whose rows start on 4
+// bytes, 50 us (211 MB, 4.2 TB/s).
 template <typename T, int K, bool PAST>
 __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
@@ -497,7 +505,8 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_kernel(BackArgs a) {
 }
 
 // Few rows, dy not replaced: the first row_wgs workgroups take `per` rows each, and the others 16 pieces of columns
-// each, whose sums they form from dy and h themselves (the caches hold them): no second launch.
+// each, whose sums they form from dy and h themselves (the caches hold them): no second launch.  The launch and one
+// row's latency bound it: 16 x 2048 bfloat16 4.0 us, 9.4 with the call around it (13.4 with a launch for the join).
 template <typename T, int K>
 __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_few_kernel(BackArgs a, int row_wgs) {
   constexpr int E = EACH<T>, WIDE = 16, SHARES = BACK_BLOCK / WIDE;
@@ -538,7 +547,8 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_few_kernel(BackArgs a
 }
 
 // Rows that the registers of a workgroup do not hold: each is read twice, and the sums stay in the workgroup's
-// row of `part`
+// row of `part`, which is read and written for every row (2000 x 40000 bfloat16 266 us; 640 MB at the rate of a copy
+// 135)
 template <typename T>
 __global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
@@ -587,7 +597,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
   }
 }
 
-// Rows of fewer than 8 elements: a thread each, whose sums a workgroup joins in order
+// Rows of fewer than 8 elements: a thread each, whose sums a workgroup joins in order (2^21 x 4 fp32 63 us; 143 MB at
+// the rate of a copy 30)
 template <typename T>
 __global__ __launch_bounds__(256) void rmsnorm_back_tiny_kernel(BackArgs a) {
   __shared__ float sums[TINY][256];
@@ -626,7 +637,7 @@ __global__ __launch_bounds__(256) void rmsnorm_back_tiny_kernel(BackArgs a) {
 }
 
 // dgain (+)= the sum of the workgroups' rows: 32 columns x 32 threads with a share of the rows each, which are
-// joined across a wave.
+// joined across a wave (512 rows of 263 4.4 us, 256 rows of 8192 4.8: latency).
 __global__ __launch_bounds__(1024) void rmsnorm_join_kernel(const float* part, int parts, int64_t n, float* dgain,
                                                             bool accumulate) {
   __shared__ double sums[32][33];
