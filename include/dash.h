@@ -558,9 +558,10 @@ dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, das
  *   rstd:  NULL, or [T] in fp32, which dash_rmsnorm_backward takes.
  * At least one output is given; apart from h they share no memory with the inputs or with each other.
  * h enters y in fp32 before it is rounded to the type; the sum of squares is kept in 64 bits (no row of finite
- * elements overflows it).  Each code and scale is that of y as defined, rounded once.  eps >= 0.  A row whose rstd
- * passes fp32's largest number (eps = 0 and zeros, or elements all below 2.9e-39) has rstd = Inf and no finite y; a
- * NaN in a row makes its rstd and y NaN, an Inf rstd = 0, its own y NaN and the rest 0. */
+ * elements overflows it).  Each code and scale is that of y as defined, rounded once (where rstd and y are normal
+ * fp32 numbers; sums of 16-bit x and res as fp32 takes them).  eps >= 0.  A row whose rstd passes fp32's largest
+ * number (eps = 0 and zeros, or elements all below 2.9e-39) has rstd = Inf and no finite y; a NaN in a row makes its
+ * rstd and y NaN, an Inf rstd = 0, its own y NaN and the rest 0. */
 dash_status dash_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, dash_prec type, const void* gain,
                          dash_prec gain_type, int64_t T, int64_t n, float eps, void* h, int64_t ldh, void* y,
                          int64_t ldy, dash_mx_fmt fmt, void* codes, void* scales, float* rstd, void* stream);
