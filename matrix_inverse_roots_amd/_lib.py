@@ -274,6 +274,7 @@ class _Args:
         """dash_tensor descriptors of GPU gradients: contiguous ones of any shape, or matrices with unit column
         stride, of float32, float16 or bfloat16; a GradList's own."""
         if isinstance(ts, GradList):
+            ts.check(self.call, name)
             if ts.index is not None:
                 if self.index not in (None, ts.index):
                     raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, ts.device,
@@ -321,25 +322,39 @@ class _Args:
 
 class GradList:
     """The gradients of a model, described once for many calls (dash_grad_norm, dash_grad_clip, dash_stack_clip).
-    It holds the tensors themselves, so what it describes stays where it is; a gradient that gets another
-    tensor needs a new list."""
+    It stands for the memory that the tensors have when it is made, and keeps that memory.  A call raises ValueError
+    once one of the tensors lies elsewhere (another .data, set_, a storage that was resized), dash_stack_clip also
+    once one has another shape or pitch; they need a new list then, as does a gradient that gets another tensor."""
 
-    __slots__ = ("tensors", "array", "device", "index", "_mats")
+    __slots__ = ("tensors", "array", "device", "index", "_held", "_at", "_mats")
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
         a = _Args("grad_list")
         self.array = a.tensors(self.tensors, "tensors")
         self.device, self.index = a.device, a.index
+        self._held = tuple(t.detach() for t in self.tensors)  # (which no change of a tensor's own memory reaches)
+        self._at = [t.data_ptr() for t in self._held]
         self._mats = None
 
     def __len__(self):
         return len(self.tensors)
 
+    def check(self, call, name):
+        # (1000 tensors 35 us, which a call's kernels hide; their shapes and strides would be 100 more)
+        if self._at and list(map(_Tensor.data_ptr, self.tensors)) != self._at:
+            i = [t.data_ptr() == at for t, at in zip(self.tensors, self._at)].index(False)
+            raise ValueError("%s: %s[%d] has other memory than when the list was made" % (call, name, i))
+
     def mats(self, call):
+        """(dash_mat descriptors, shapes)"""
+        now, then = ([(t.shape, t.stride()) for t in ts] for ts in (self.tensors, self._held))
+        if now != then:
+            i = [a == b for a, b in zip(now, then)].index(False)
+            raise ValueError("%s: grads[%d] has another shape or pitch than when the list was made" % (call, i))
         if self._mats is None:
-            self._mats = _Args(call).mats(self.tensors, "grads")
-        return self._mats
+            self._mats = _Args(call).mats(self._held, "grads")
+        return self._mats, [shape for shape, _ in then]
 
 
 def _check(name, status):
@@ -861,7 +876,7 @@ def dash_stack_clip(grads, B: int, norm, max_norm: float, G_stack, stream=None):
     a = _Args("dash_stack_clip")
     if isinstance(grads, GradList):
         a.tensors(grads, "grads")  # (the call's device)
-        arr, shapes = grads.mats(a.call), [t.shape for t in grads.tensors]
+        arr, shapes = grads.mats(a.call)
     else:
         arr, shapes = a.mats(grads, "grads"), [t.shape for t in grads]
     n = _tiles(shapes, B) * B * B
