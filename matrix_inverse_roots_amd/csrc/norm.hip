@@ -123,10 +123,9 @@ __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int6
   if (c % GROUP == 0) scales[group0 + c / GROUP] = (uint8_t)byte;
 }
 
-// x + res - h, exactly (h is their rounded sum; of 16-bit elements it is next to never rounded)
-__device__ __forceinline__ float rest_of_sum(float x, float res, float h) {
-  const float part = h - x;
-  return (x - (h - part)) + (res - part);
+// x + res - h (h is their rounded sum; of 16-bit elements it is next to never rounded)
+__device__ __forceinline__ double rest_of_sum(float x, float res, float h) {
+  return ((double)x + (double)res) - (double)h;
 }
 
 // A piece of y made ready for its codes.  Four roundings move an element across a border only if its last 19 bits are
@@ -150,20 +149,24 @@ __device__ __forceinline__ void settle(const NormArgs& a, int64_t row, int64_t c
     asm volatile("" : "+v"(hq));
     if (sizeof(T) == 4 && a.res && near && c + q < a.n) {
       asm volatile("" : "+v"(row));
-      more = rest_of_sum(((const float*)a.x)[row * a.ldx + c + q], ((const float*)a.res)[row * a.ldr + c + q], hq);
+      more = (float)rest_of_sum(((const float*)a.x)[row * a.ldx + c + q], ((const float*)a.res)[row * a.ldr + c + q], hq);
     }
     y[q] = root.odd_times(hq, more, g[q]);
   }
 }
 
 // One piece of h = x + res; what its squares lack of those of the fp32 sums themselves, 2 sum h rest, is added to `more`
+// (in 64 bits: its terms lie 2^-24 below squares that may be anywhere in their range)
 template <typename T, int K>
-__device__ __forceinline__ void add_up(const vec_of<T>& x, const vec_of<T>& res, bool sum, float* h, float* more) {
+__device__ __forceinline__ void add_up(const vec_of<T>& x, const vec_of<T>& res, bool sum, float* h, double* more) {
 #pragma unroll
   for (int q = 0; q < EACH<T>; ++q) h[q] = sum ? (float)x[q] + (float)res[q] : (float)x[q];
   if (sizeof(T) == 2 || !sum) return;
 #pragma unroll
-  for (int q = 0; q < EACH<T>; ++q) *more = fmaf(2.f * h[q], rest_of_sum((float)x[q], (float)res[q], h[q]), *more);
+  for (int q = 0; q < EACH<T>; ++q) {
+    const double twice = 2. * (double)h[q];
+    *more = fma(twice, rest_of_sum((float)x[q], (float)res[q], h[q]), *more);
+  }
   if (K >= 4) asm volatile("" : "+v"(*more));  // (here, and not with x and res in registers until the gain is there)
 }
 template <int E>
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
   const T* x = (const T*)a.x + row * a.ldx;
   const T* res = (const T*)a.res + row * a.ldr;
   float h[K][E], g[K][E];
-  float more = 0.f;
+  double more = 0.;
   {
     vec_of<T> vx[K], vr[K];
 #pragma unroll
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < K; ++k) add_up<T, K>(vx[k], vr[k], a.res != nullptr, h[k], &more);
   }
-  double s = isfinite(more) ? (double)more : 0.;  // (h beyond 1e22 may overflow it)
+  double s = isfinite(more) ? more : 0.;  // (an h that is not finite makes the sum what it is)
 #pragma unroll
   for (int k = 0; k < K; ++k) {  // (the gain on its way before the sums: 8192 x 2048 bfloat16 36 -> 32 us)
     load_gain<E>(a.gain, a.gain_type, (int64_t)E * (lane + k * a.lanes), a.n, g[k]);
@@ -244,9 +247,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
     vec_of<T> vr;
     if (a.res) vr = load_piece(res, c, a.n);
     float h[E];
-    float more = 0.f;
+    double more = 0.;
     add_up<T, 1>(vx, vr, a.res != nullptr, h, &more);
-    s += squares64<E>(h) + (isfinite(more) ? (double)more : 0.);
+    s += squares64<E>(h) + (isfinite(more) ? more : 0.);
   }
   s = row_sum(s, 1024, shared);
   const Root root(fma(s, a.over_n, a.eps));
