@@ -274,7 +274,9 @@ class _Args:
         """dash_tensor descriptors of GPU gradients: contiguous ones of any shape, or matrices with unit column
         stride, of float32, float16 or bfloat16; a GradList's own."""
         if isinstance(ts, GradList):
-            ts.check(self.call, name)
+            # (1000 tensors 35 us, which a call's kernels hide; shapes and strides as well would be 100 more)
+            if ts._at and list(map(_Tensor.data_ptr, ts.tensors)) != ts._at:
+                ts._differs(ts._at, _Tensor.data_ptr, self.call, "memory")
             if ts.index is not None:
                 if self.index not in (None, ts.index):
                     raise ValueError("%s: %s is on %s, the call's other tensors on %s" % (self.call, name, ts.device,
@@ -322,11 +324,12 @@ class _Args:
 
 class GradList:
     """The gradients of a model, described once for many calls (dash_grad_norm, dash_grad_clip, dash_stack_clip).
-    It stands for the memory that the tensors have when it is made, and keeps that memory.  A call raises ValueError
-    once one of the tensors lies elsewhere (another .data, set_, a storage that was resized), dash_stack_clip also
-    once one has another shape or pitch; they need a new list then, as does a gradient that gets another tensor."""
+    It stands for the tensors as they are when it is made, and keeps their memory.  A call raises ValueError once one of
+    them lies elsewhere (another .data, set_, a storage that was resized), dash_stack_clip also once one has more or
+    fewer elements; they need a new list then, as does a gradient that gets another tensor.  Other changes of shape
+    within the same memory are not looked for: the list goes on standing for what it was made of."""
 
-    __slots__ = ("tensors", "array", "device", "index", "_held", "_at", "_mats")
+    __slots__ = ("tensors", "array", "device", "index", "_held", "_at", "_sizes", "_mats", "_tiles")
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
@@ -335,26 +338,26 @@ class GradList:
         self.device, self.index = a.device, a.index
         self._held = tuple(t.detach() for t in self.tensors)  # (which no change of a tensor's own memory reaches)
         self._at = [t.data_ptr() for t in self._held]
+        self._sizes = [t.numel() for t in self._held]
         self._mats = None
+        self._tiles = (0, 0)  # a block size, and the tiles of that size
 
     def __len__(self):
         return len(self.tensors)
 
-    def check(self, call, name):
-        # (1000 tensors 35 us, which a call's kernels hide; their shapes and strides would be 100 more)
-        if self._at and list(map(_Tensor.data_ptr, self.tensors)) != self._at:
-            i = [t.data_ptr() == at for t, at in zip(self.tensors, self._at)].index(False)
-            raise ValueError("%s: %s[%d] has other memory than when the list was made" % (call, name, i))
+    def _differs(self, then, now, call, what):
+        i = [now(t) == s for t, s in zip(self.tensors, then)].index(False)
+        raise ValueError("%s: grads[%d] has other %s than when the list was made" % (call, i, what))
 
-    def mats(self, call):
-        """(dash_mat descriptors, shapes)"""
-        now, then = ([(t.shape, t.stride()) for t in ts] for ts in (self.tensors, self._held))
-        if now != then:
-            i = [a == b for a, b in zip(now, then)].index(False)
-            raise ValueError("%s: grads[%d] has another shape or pitch than when the list was made" % (call, i))
+    def mats(self, call, B):
+        """(dash_mat descriptors, tiles of B x B)"""
+        if self._at and list(map(_Tensor.numel, self.tensors)) != self._sizes:
+            self._differs(self._sizes, _Tensor.numel, call, "sizes")
         if self._mats is None:
             self._mats = _Args(call).mats(self._held, "grads")
-        return self._mats, [shape for shape, _ in then]
+        if self._tiles[0] != B:  # (300 weights 25 us)
+            self._tiles = (B, _tiles([t.shape for t in self._held], B))
+        return self._mats, self._tiles[1]
 
 
 def _check(name, status):
@@ -876,9 +879,9 @@ def dash_stack_clip(grads, B: int, norm, max_norm: float, G_stack, stream=None):
     a = _Args("dash_stack_clip")
     if isinstance(grads, GradList):
         a.tensors(grads, "grads")  # (the call's device)
-        arr, shapes = grads.mats(a.call)
+        arr, tiles = grads.mats(a.call, B)
     else:
-        arr, shapes = a.mats(grads, "grads"), [t.shape for t in grads]
-    n = _tiles(shapes, B) * B * B
+        arr, tiles = a.mats(grads, "grads"), _tiles([t.shape for t in grads], B)
+    n = tiles * B * B
     a.run(library().dash_stack_clip, arr, len(grads), B, a.ptr(norm, "norm", numel=1), max_norm,
           a.ptr(G_stack, "G_stack", numel=n), a.stream(stream))

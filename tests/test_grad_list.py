@@ -97,19 +97,33 @@ def test_the_memory_stays(calls):
         dash.dash_grad_clip(lst, NORM, 1.0, stream=0)
 
 
-def test_another_shape_in_the_same_memory(calls):
-    """Tiles go by shapes: refused, whether the list has been used for tiles before or not.  Norm and clipping
-    take what the list was made of."""
+def test_other_sizes_in_the_same_memory(calls):
+    """Tiles are refused, whether the list has been used for tiles before or not.  Norm and clipping take what the list
+    was made of."""
     for used in (False, True):
-        for change in (lambda t: t.resize_(8, 4), lambda t: t.t_(), lambda t: t.unsqueeze_(0)):
+        for change in (lambda t: t.resize_(8, 4), lambda t: t.resize_(64, 256), lambda t: t.resize_(255, 256)):
             ts = [torch.zeros(64, 64), torch.zeros(256, 256)]
             lst = dash.grad_list(ts)
             if used:
                 dash.dash_stack_clip(lst, 64, NORM, 1.0, STACK, stream=0)
             change(ts[1])
-            G = torch.zeros(2, 64, 64)  # (enough for what is left of it, not for what is described)
-            for out in (G, STACK):
-                with pytest.raises(ValueError):
-                    dash.dash_stack_clip(lst, 64, NORM, 1.0, out, stream=0)
+            with pytest.raises(ValueError, match="other sizes"):
+                dash.dash_stack_clip(lst, 64, NORM, 1.0, STACK, stream=0)
             dash.dash_grad_clip(lst, NORM, 1.0, stream=0)
             assert calls.last == [(ts[0].data_ptr(), 1, 4096, 4096), (ts[1].data_ptr(), 1, 65536, 65536)]
+
+
+def test_tiles_are_those_of_the_description(calls):
+    """A weight that is transposed in place, after or before the list's first tiles: the stack has to hold the tiles that
+    are launched."""
+    for used in (False, True):
+        t = torch.zeros(64, 250)
+        lst = dash.grad_list([t])
+        if used:
+            dash.dash_stack_clip(lst, 192, NORM, 1.0, STACK, stream=0)
+        t.t_()
+        for B, tiles in ((192, 2), (64, 4), (192, 2)):
+            with pytest.raises(ValueError, match="G_stack"):
+                dash.dash_stack_clip(lst, B, NORM, 1.0, torch.zeros(tiles * B * B - 1), stream=0)
+            dash.dash_stack_clip(lst, B, NORM, 1.0, torch.zeros(tiles * B * B), stream=0)
+            assert calls.last == [(t.data_ptr(), 64, 250, 250)]
