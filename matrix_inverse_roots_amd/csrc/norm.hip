@@ -77,27 +77,25 @@ __device__ __forceinline__ S row_sum(S v, int lanes, S* shared) {
   return v;
 }
 
-// rstd in two fp32 parts that add up to it (48 bits)
+// rstd, and what its rounding lost times 2^24, so that the two hold 47 bits of it down to fp32's least normal number
 struct Root {
   float rstd, rest;
   __device__ __forceinline__ Root(double square) {
     const double r = rsqrt(square);
     rstd = (float)r;
-    rest = (float)(r - (double)rstd);
+    rest = (float)(0x1p24 * (r - (double)rstd));
   }
   // y = h rstd g, off by at most four roundings (of h, of rstd and of two products)
   __device__ __forceinline__ float times(float h, float g) const { return h * rstd * g; }
-  // The same as the fp32 number that rounds to the code that h rstd g itself rounds to: cut off, and made odd if
-  // anything was lost, so that it is on y's side of each border of codes and of scales (they end in 19 zeros).
-  // more: what h lacks.
-  __device__ __forceinline__ float odd_times(float h, float more, float g) const {
-    const float t = h * rstd, e = fmaf(more, rstd, fmaf(h, rest, fmaf(h, rstd, -t)));
-    const float y = fmaf(t, g, e * g);
-    const float lost = fmaf(t, g, -y) + e * g;
-    unsigned bits = __builtin_bit_cast(unsigned, y);
-    if (lost == 0.f || (bits & 0x7fffffffu) >= 0x7f800000u) return y;
-    bits -= (bits ^ __builtin_bit_cast(unsigned, lost)) >> 31;
-    return __builtin_bit_cast(float, bits | 1u);
+  // The same as the fp32 number that rounds to the code that h rstd g itself rounds to: formed in 64 bits, cut off, and
+  // made odd if anything was lost, so that it is on y's side of each border of codes and of scales (they end in 19
+  // zeros).  h: the sum before its rounding.
+  __device__ __forceinline__ float odd_times(double h, float g) const {
+    const double root = fma((double)rest, 0x1p-24, (double)rstd);
+    uint64_t y = __builtin_bit_cast(uint64_t, h * root * (double)g);
+    const unsigned low = (1u << 29) - 1;  // (what fp32 does not hold)
+    if ((unsigned)y & low) y = (y & ~(uint64_t)low) | (low + 1);
+    return (float)__builtin_bit_cast(double, y);
   }
 };
 
@@ -123,11 +121,6 @@ __device__ __forceinline__ void store_codes(const float* y, int64_t group0, int6
   if (c % GROUP == 0) scales[group0 + c / GROUP] = (uint8_t)byte;
 }
 
-// x + res - h (h is their rounded sum; of 16-bit elements it is next to never rounded)
-__device__ __forceinline__ double rest_of_sum(float x, float res, float h) {
-  return ((double)x + (double)res) - (double)h;
-}
-
 // A piece of y made ready for its codes.  Four roundings move an element across a border only if its last 19 bits are
 // next to zeros: once in a hundred waves, which form the piece again, one element after the other (the registers are
 // few).  The sum x + res of fp32 elements is rounded as often as not; of 16-bit ones next to never.
@@ -143,15 +136,18 @@ __device__ __forceinline__ void settle(const NormArgs& a, int64_t row, int64_t c
   if (__builtin_expect(!__ballot(least <= 2 * NEAR << 13), 1)) return;
 #pragma unroll
   for (int q = 0; q < E; ++q) {
-    const bool near = border(y[q]) <= 2 * NEAR << 13 && y[q] != 0.f;  // (zeros are where they belong)
+    // (zeros, Inf and NaN are where they belong)
+    const bool near = border(y[q]) <= 2 * NEAR << 13 && y[q] != 0.f && isfinite(y[q]);
     if (__builtin_expect(!__ballot(near), 1)) continue;
-    float hq = h[q], more = 0.f;
+    float hq = h[q];
     asm volatile("" : "+v"(hq));
+    double sum = hq;
     if (sizeof(T) == 4 && a.res && near && c + q < a.n) {
       asm volatile("" : "+v"(row));
-      more = (float)rest_of_sum(((const float*)a.x)[row * a.ldx + c + q], ((const float*)a.res)[row * a.ldr + c + q], hq);
+      sum = (double)((const float*)a.x)[row * a.ldx + c + q] + (double)((const float*)a.res)[row * a.ldr + c + q];
     }
-    y[q] = root.odd_times(hq, more, g[q]);
+    const float odd = root.odd_times(sum, g[q]);
+    if (near) y[q] = odd;
   }
 }
 
@@ -164,8 +160,8 @@ __device__ __forceinline__ void add_up(const vec_of<T>& x, const vec_of<T>& res,
   if (sizeof(T) == 2 || !sum) return;
 #pragma unroll
   for (int q = 0; q < EACH<T>; ++q) {
-    const double twice = 2. * (double)h[q];
-    *more = fma(twice, rest_of_sum((float)x[q], (float)res[q], h[q]), *more);
+    const double rest = ((double)(float)x[q] + (double)(float)res[q]) - (double)h[q];
+    *more = fma(2. * (double)h[q], rest, *more);
   }
   if (K >= 4) asm volatile("" : "+v"(*more));  // (here, and not with x and res in registers until the gain is there)
 }
@@ -284,15 +280,14 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
   const int64_t row = (a.first_wg + blockIdx.x) * 256 + threadIdx.x;
   if (row >= a.T) return;
   const int n = (int)a.n;
-  float h[TINY], more[TINY], y[GROUP];
+  double h[TINY];
+  float y[GROUP];
   double s = 0.;
 #pragma unroll
   for (int q = 0; q < TINY; ++q) {
-    const double x = q < n ? (double)(float)((const T*)a.x)[row * a.ldx + q] : 0.;
-    const double r = a.res && q < n ? (double)(float)((const T*)a.res)[row * a.ldr + q] : 0.;
-    h[q] = (float)(x + r);
-    more[q] = isfinite(h[q]) ? (float)(x + r - (double)h[q]) : 0.f;
-    s = fma(x + r, x + r, s);
+    h[q] = q < n ? (double)(float)((const T*)a.x)[row * a.ldx + q] : 0.;
+    if (a.res && q < n) h[q] += (double)(float)((const T*)a.res)[row * a.ldr + q];
+    s = fma(h[q], h[q], s);
   }
   const Root root(fma(s, a.over_n, a.eps));
   if (a.rstd) a.rstd[row] = root.rstd;
@@ -302,9 +297,10 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
     y[q] = 0.f;
     if (q < TINY && q < n) {
       const float g = gain_at(a.gain, a.gain_type, q);
-      y[q] = root.odd_times(h[q], more[q], g);
-      if (a.h) ((T*)a.h)[row * a.ldh + q] = (T)h[q];
-      if (a.y) ((T*)a.y)[row * a.ldy + q] = (T)root.times(h[q], g);
+      const float rounded = (float)h[q], plain = root.times(rounded, g), odd = root.odd_times(h[q], g);
+      y[q] = isfinite(plain) ? odd : plain;
+      if (a.h) ((T*)a.h)[row * a.ldh + q] = (T)rounded;
+      if (a.y) ((T*)a.y)[row * a.ldy + q] = (T)plain;
     }
     top = umax(top, mag_bits(y[q]));
   }

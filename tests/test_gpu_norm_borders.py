@@ -51,3 +51,13 @@ def test_what_a_sum_of_fp32_elements_loses(n, fmt):
     """x + res rounded to fp32 is off by up to 2^-24; rstd is that of the sums themselves."""
     for i, size in enumerate((1e-36, 1e-30, 1e-21, 1e-19, 1e-10, 1.0, 1e10, 1e23, 1e28)):
         check(n, size, fmt, torch.float32, True, 100 * n + i)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=NAMES.get)
+@pytest.mark.parametrize("fmt", FMTS, ids=IDS)
+@pytest.mark.parametrize("n", [7, 1000, 4096, 8208, 33024])
+def test_rows_of_any_size(n, fmt, dtype):
+    """rstd down to fp32's least normal numbers."""
+    for i, size in enumerate((1e-36, 1e-20, 1.0, 1e20, 2.0**105, 2.0**112, 2.0**118, 2.0**122, 2.0**124)):
+        for with_res in (False, True):
+            check(n, size, fmt, dtype, with_res, 100 * n + 20 + i)
