@@ -558,8 +558,10 @@ dash_status dash_grad_stack_mx_workspace(int64_t T, int64_t out, int64_t in, das
  *   rstd:  NULL, or [T] in fp32, which dash_rmsnorm_backward takes.
  * At least one output is given; apart from h they share no memory with the inputs or with each other.
  * h enters y in fp32 before it is rounded to the type; the sum of squares is kept in 64 bits (no row of finite
- * elements overflows it).  Each code and scale is that of y as defined, rounded once (where rstd and y are normal
- * fp32 numbers; sums of 16-bit x and res as fp32 takes them).  eps >= 0.  A row whose rstd passes fp32's largest
+ * elements overflows it).  Each code and scale is that of y as defined, rounded once (where rstd, h rstd and y are
+ * normal fp32 numbers; sums of 16-bit x and res as fp32 takes them): y is known to 2^-47 of itself (in rows of more
+ * than 32768 to what a sum of n squares in 64 bits leaves), and within 2^-46 of a border between codes it counts as
+ * on it, where the even code is the nearest.  eps >= 0.  A row whose rstd passes fp32's largest
  * number (eps = 0 and zeros, or elements all below 2.9e-39) has rstd = Inf and no finite y; a NaN in a row makes its
  * rstd and y NaN, an Inf rstd = 0, its own y NaN and the rest 0. */
 dash_status dash_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldr, dash_prec type, const void* gain,

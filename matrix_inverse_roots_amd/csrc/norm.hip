@@ -89,12 +89,14 @@ struct Root {
   __device__ __forceinline__ float times(float h, float g) const { return h * rstd * g; }
   // The same as the fp32 number that rounds to the code that h rstd g itself rounds to: formed in 64 bits, cut off, and
   // made odd if anything was lost, so that it is on y's side of each border of codes and of scales (they end in 19
-  // zeros).  h: the sum before its rounding.
+  // zeros).  y carries up to 2^-47 of itself (the sum of up to 32 squares a thread and its joins 2^-48.6, what is left
+  // of rstd 2^-49, a few roundings): if it is within 64 steps of 2^-53 to 2^-52 of an fp32 number, it is that one, as where
+  // the row's elements have one magnitude.  h: the sum before its rounding.
   __device__ __forceinline__ float odd_times(double h, float g) const {
     const double root = fma((double)rest, 0x1p-24, (double)rstd);
     uint64_t y = __builtin_bit_cast(uint64_t, h * root * (double)g);
-    const unsigned low = (1u << 29) - 1;  // (what fp32 does not hold)
-    if ((unsigned)y & low) y = (y & ~(uint64_t)low) | (low + 1);
+    const unsigned low = (1u << 29) - 1, within = 64;  // (what fp32 does not hold)
+    if ((((unsigned)y + within) & low) > 2 * within) y = (y & ~(uint64_t)low) | (low + 1);
     return (float)__builtin_bit_cast(double, y);
   }
 };

@@ -61,3 +61,26 @@ def test_rows_of_any_size(n, fmt, dtype):
     for i, size in enumerate((1e-36, 1e-20, 1.0, 1e20, 2.0**105, 2.0**112, 2.0**118, 2.0**122, 2.0**124)):
         for with_res in (False, True):
             check(n, size, fmt, dtype, with_res, 100 * n + 20 + i)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=NAMES.get)
+@pytest.mark.parametrize("fmt", FMTS, ids=IDS)
+@pytest.mark.parametrize("n", [1, 3, 7, 49, 1000, 4096, 8208, 33024])
+def test_elements_on_borders(n, fmt, dtype):
+    """Rows of one magnitude, for which y = +-gain, and gains on the borders between codes: to the even code."""
+    table = ref.grid(fmt)
+    mid = (table[1:] + table[:-1]) / 2
+    rng = np.random.default_rng(n)
+    T = 50
+    gain = rng.choice(mid, n)
+    gain[::32] = mid[-1]
+    size = torch.tensor(rng.choice((1e-30, 0.1, 1.0, 77.0, 1e20), T) * rng.uniform(0.5, 2, T))[:, None].to(dtype)
+    sign = torch.tensor(rng.choice([-1.0, 1.0], (T, n))).to(dtype)
+    want, byte = ref.quantize(sign.double().numpy() * gain, fmt)
+    for res in (None, size * sign * 0.375):
+        x = (size * sign).to(DEV)
+        _, _, codes, scales, _ = norm(x, None if res is None else res.to(DEV), torch.tensor(gain).float().to(DEV), fmt,
+                                      eps=0.0)
+        assert np.array_equal(scales.cpu().numpy()[0], byte)
+        wrong = ref.unpack(codes.cpu().numpy()[0], fmt) != want
+        assert not wrong.any(), (res is None, int(wrong.sum()))
