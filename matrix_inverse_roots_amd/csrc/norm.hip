@@ -289,6 +289,7 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
   for (int q = 0; q < TINY; ++q) {
     h[q] = q < n ? (double)(float)((const T*)a.x)[row * a.ldx + q] : 0.;
     if (a.res && q < n) h[q] += (double)(float)((const T*)a.res)[row * a.ldr + q];
+    if (!isfinite((float)h[q])) h[q] = (double)(float)h[q];  // (h is fp32's: an Inf, and so is the sum)
     s = fma(h[q], h[q], s);
   }
   const Root root(fma(s, a.over_n, a.eps));
