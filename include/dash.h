@@ -575,8 +575,9 @@ dash_status dash_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ld
  * dx may be dy or dh itself (with its pitch) and shares no memory with the rest.
  *   dgain: NULL, or [n] in fp32; accumulate = 1 adds to what it holds, 0 overwrites it.  A 1-D gradient
  *          (dash_stack_vec).  Equal calls give equal bits.
- * Sums are fp32 (dgain's over the workgroups' shares 64 bits), dx is rounded once; where m is a multiple of
- * xhat the terms of dx cancel and what is left is their rounding.  T = 0: empty sums (only dgain is used).
+ * Sums are fp32 (c's of rows of more than 16384 64 bits from pieces of 16 bytes on, dgain's over the workgroups'
+ * shares 64 bits), dx is rounded once; where m is a multiple of xhat the terms of dx cancel and what is left is
+ * their rounding.  T = 0: empty sums (only dgain is used).
  * ws: dash_rmsnorm_backward_workspace bytes, 256-byte aligned (NULL without dgain); the size for one T serves
  * any smaller one. */
 dash_status dash_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,

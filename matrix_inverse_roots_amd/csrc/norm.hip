@@ -548,27 +548,28 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_few_kernel(BackArgs a
   a.dgain[out] = (float)all;
 }
 
-// Rows that the registers of a workgroup do not hold: each is read twice, and the sums stay in the workgroup's
-// row of `part`, which is read and written for every row (2000 x 40000 bfloat16 266 us; 640 MB at the rate of a copy
-// 135)
+// Rows that the registers of a workgroup do not hold: each is read twice, its mean summed in 64 bits from pieces on (a
+// thread may have thousands of them), and the column sums stay in the workgroup's row of `part`, which is read and
+// written for every row (2000 x 40000 bfloat16 266 us; 640 MB at the rate of a copy 135)
 template <typename T>
 __global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
-  __shared__ float shared[16];
+  __shared__ double shared[16];
   float* part = a.part + blockIdx.x * a.n;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const T* dy = (const T*)a.dy + row * a.lddy;
     const T* h = (const T*)a.h + row * a.ldh;
     const float rstd = a.rstd[row];
-    float dot = 0.f;
+    double dot = 0.;
     for (int64_t c = (int64_t)E * threadIdx.x; c < a.n; c += E * 1024) {
       const vec_of<T> vd = load_piece(dy, c, a.n), vh = load_piece(h, c, a.n);
-      float g[E];
+      float g[E], sum = 0.f;
       load_gain<E>(a.gain, a.gain_type, c, a.n, g);
 #pragma unroll
-      for (int q = 0; q < E; ++q) dot = fmaf((float)vd[q] * g[q], (float)vh[q] * rstd, dot);
+      for (int q = 0; q < E; ++q) sum = fmaf((float)vd[q] * g[q], (float)vh[q] * rstd, sum);
+      dot += (double)sum;
     }
-    const float mean = row_sum(dot, 1024, shared) * a.over_n;
+    const float mean = (float)(row_sum(dot, 1024, shared) * (double)a.over_n);
     for (int64_t c = (int64_t)E * threadIdx.x; c < a.n; c += E * 1024) {
       const vec_of<T> vd = load_piece(dy, c, a.n), vh = load_piece(h, c, a.n);
       float g[E], dx[E];
