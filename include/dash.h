@@ -606,7 +606,8 @@ dash_status dash_grad_clip(const dash_tensor* grads, int32_t n, const float* nor
 
 /* dash_stack of clipped gradients: the tiles of g_i min(1, max_norm / norm[0]), the gradients left as they are.
  * Arguments, tiles and errors as dash_stack, norm and max_norm as dash_grad_clip; G_stack shares no memory with
- * the gradients or norm. */
+ * the gradients or norm.  The padding of edge tiles is 0, but for norm[0] = NaN, which makes every element of every
+ * tile NaN. */
 dash_status dash_stack_clip(const dash_mat* grads, int32_t n, int32_t B, const float* norm, float max_norm,
                             float* G_stack, void* stream);
 

@@ -261,7 +261,7 @@ __global__ void freeze_update_kernel(const float* monitor, int mon_stride, int c
 constexpr int COPY_VEC = 4;
 
 // CLIP (to the stack): times min(1, most / norm), which the copy hides (384 tiles of 1024, 3.2 GB in two launches, 504
-// us: 6.4 TB/s).
+// us: 6.4 TB/s); the padding's zeros, too, so that a NaN factor leaves nothing finite.
 template <bool TO_STACK, bool CLIP>
 __global__ __launch_bounds__(256) void tile_copy_kernel(CopyGroup g, int B, float* stack, const float* norm, float most) {
   const float factor = CLIP ? clip_factor(norm, most) : 1.f;

@@ -67,3 +67,19 @@ def test_launches_that_end_by_size(first):
     B = 64
     big = randn(1, first[0], first[1] + -first[1] % 4)[:, :first[1]]
     check([big] + ragged(75, B, 2) + [big[:9000]] + ragged(30, B, 3), B)
+
+
+@pytest.mark.parametrize("B", [64, 192])
+def test_norms_that_are_not_finite(B):
+    """An infinite norm makes finite elements 0 and others NaN, and the padding stays 0; a NaN norm makes every element
+    of every tile NaN, the padding's too."""
+    weights = ragged(20, B, 4)
+    weights[3][0, 0] = float("inf")
+    n = sum(-(-w.shape[0] // B) * -(-w.shape[1] // B) for w in weights)
+    G = torch.full((n, B, B), 7.0, device=DEV)
+    dash.dash_stack_clip(weights, B, torch.full((1,), float("inf"), device=DEV), 1.0, G)
+    want = torch.cat([tiles(w * 0.0, B) for w in weights])
+    assert torch.equal(G.isnan(), want.isnan()) and int(G.isnan().sum()) == 1
+    assert not bool(G[~G.isnan()].any())
+    dash.dash_stack_clip(weights, B, torch.full((1,), float("nan"), device=DEV), 1.0, G)
+    assert bool(G.isnan().all())
