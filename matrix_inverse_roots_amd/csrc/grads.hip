@@ -241,13 +241,16 @@ struct Shape {
 };
 
 // How a list is shared out: pieces of a workgroup, and workgroups in all.  Clipping takes one pass of every thread (0.8
-// GB of bfloat16 257 us; 16384 workgroups that loop 300), up to 2^22 workgroups.  The norm takes two passes, up to
+// GB of bfloat16 257 us; 16384 workgroups that loop 300), up to 2^22 workgroups; where nothing is clipped they read the
+// norm and leave (0.8 GB 23 us, 6.4 GB of fp32 168).  The norm takes two passes, up to
 // 65536 workgroups, whose sums one more launch adds (6.4 GB: 923 us, with 16384 of them 935, with 393216 1159).
 struct Share {
   int64_t per_wg, wgs;
   bool small;  // for grad_norm_small_kernel
   bool past;   // the caches: they hold no part of it until the next pass
 };
+// One workgroup or two launches (tensors x bfloat16 elements, us): 9 x 512 3.1 / 5.2, 9 x 4096 4.5 / 5.1, 32 x 512 4.5 /
+// 5.2, 32 x 4096 7.7 / 5.1, 64 x 512 7.3 / 5.3, 64 x 4096 13.8 / 5.2: at the rule's end the other way is the shorter one.
 constexpr int64_t SMALL_PIECES = 512;
 Share share_out(const dash_tensor* g, int n, bool write) {
   int64_t all = 0, most = 0;

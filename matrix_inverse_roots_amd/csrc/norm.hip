@@ -345,7 +345,9 @@ int row_lanes(int64_t pieces, int k) {
 
 // Pieces of a thread, where at most `threads` share a row.  One, so that many waves have loads under way (8192 x
 // 2048 bfloat16 with 1 / 2 / 4: 30.7 / 36.0 / 37.3 us; its gradient 31.1 / 33.4); but two where the last
-// one of a row is cut, which the wave that holds it pays for (50001 x 263: 39.6 / 35.4, gradient 50 / 42).
+// one of a row is cut, which the wave that holds it pays for (one / two: 50001 x 263 binary16 34.3 / 30.7, gradient 34.4
+// / 30.2; 12001 x 1001 bfloat16 23.3 / 21.4, 26.5 / 24.3; 12001 x 2047 40 / 39, 46 / 41; 50001 x 263 fp32 51 / 46, 56 / 44;
+// 12001 x 3001 fp32 the same).
 int row_pieces(int64_t pieces, bool whole, int threads, int least = 1) {
   int k = whole || least > 1 ? least : 2;
   while (pieces > (int64_t)threads * k) k *= 2;
@@ -550,7 +552,7 @@ __global__ __launch_bounds__(BACK_BLOCK) void rmsnorm_back_few_kernel(BackArgs a
 
 // Rows that the registers of a workgroup do not hold: each is read twice, its mean summed in 64 bits from pieces on (a
 // thread may have thousands of them), and the column sums stay in the workgroup's row of `part`, which is read and
-// written for every row (2000 x 40000 bfloat16 266 us; 640 MB at the rate of a copy 135)
+// written for every row (2000 x 40000 bfloat16 267 us; 640 MB at the rate of a copy 135)
 template <typename T>
 __global__ __launch_bounds__(1024) void rmsnorm_back_long_kernel(BackArgs a) {
   constexpr int E = EACH<T>;
@@ -666,6 +668,8 @@ struct BackPlan {
   int64_t wgs;
   bool few = false;  // rmsnorm_back_few_kernel
 };
+// Rows whose gradient is one launch, though their columns' workgroups read dy and h once more: 16 x 2048 bfloat16 3.0 us
+// (in two launches 5.9), 512 x 64 4.8 (6.7), 512 x 2048 5.7 (9.2), 512 x 16384 16.5 (22.1), in fp32 31.8 (30.2).
 constexpr int64_t FEW_ROWS = 512;
 BackPlan back_plan(int64_t T, int64_t n, int E) {
   BackPlan p;
