@@ -90,8 +90,8 @@ struct Root {
   // The same as the fp32 number that rounds to the code that h rstd g itself rounds to: formed in 64 bits, cut off, and
   // made odd if anything was lost, so that it is on y's side of each border of codes and of scales (they end in 19
   // zeros).  y carries up to 2^-47 of itself (the sum of up to 32 squares a thread and its joins 2^-48.6, what is left
-  // of rstd 2^-49, a few roundings): if it is within 64 steps of 2^-53 to 2^-52 of an fp32 number, it is that one, as where
-  // the row's elements have one magnitude.  h: the sum before its rounding.
+  // of rstd 2^-49, a few roundings): if it is within 64 steps of 2^-53 to 2^-52 of an fp32 number, it is that one, as
+  // where the row's elements have one magnitude.  h: the sum before its rounding.
   __device__ __forceinline__ float odd_times(double h, float g) const {
     const double root = fma((double)rest, 0x1p-24, (double)rstd);
     uint64_t y = __builtin_bit_cast(uint64_t, h * root * (double)g);
@@ -289,7 +289,8 @@ __global__ __launch_bounds__(256) void rmsnorm_tiny_kernel(NormArgs a) {
   for (int q = 0; q < TINY; ++q) {
     h[q] = q < n ? (double)(float)((const T*)a.x)[row * a.ldx + q] : 0.;
     if (a.res && q < n) h[q] += (double)(float)((const T*)a.res)[row * a.ldr + q];
-    if (!isfinite((float)h[q])) h[q] = (double)(float)h[q];  // (h is fp32's: an Inf, and so is the sum)
+    // (h is fp32's sum: of 16-bit elements as longer rows take it, and beyond fp32 an Inf)
+    if (sizeof(T) == 2 || !isfinite((float)h[q])) h[q] = (double)(float)h[q];
     s = fma(h[q], h[q], s);
   }
   const Root root(fma(s, a.over_n, a.eps));
@@ -346,8 +347,8 @@ int row_lanes(int64_t pieces, int k) {
 // Pieces of a thread, where at most `threads` share a row.  One, so that many waves have loads under way (8192 x
 // 2048 bfloat16 with 1 / 2 / 4: 30.7 / 36.0 / 37.3 us; its gradient 31.1 / 33.4); but two where the last
 // one of a row is cut, which the wave that holds it pays for (one / two: 50001 x 263 binary16 34.3 / 30.7, gradient 34.4
-// / 30.2; 12001 x 1001 bfloat16 23.3 / 21.4, 26.5 / 24.3; 12001 x 2047 40 / 39, 46 / 41; 50001 x 263 fp32 51 / 46, 56 / 44;
-// 12001 x 3001 fp32 the same).
+// / 30.2; 12001 x 1001 bfloat16 23.3 / 21.4, 26.5 / 24.3; 12001 x 2047 40 / 39, 46 / 41; 50001 x 263 fp32 51 / 46, 56 /
+// 44; 12001 x 3001 fp32 the same).
 int row_pieces(int64_t pieces, bool whole, int threads, int least = 1) {
   int k = whole || least > 1 ? least : 2;
   while (pieces > (int64_t)threads * k) k *= 2;
@@ -668,8 +669,8 @@ struct BackPlan {
   int64_t wgs;
   bool few = false;  // rmsnorm_back_few_kernel
 };
-// Rows whose gradient is one launch, though their columns' workgroups read dy and h once more: 16 x 2048 bfloat16 3.0 us
-// (in two launches 5.9), 512 x 64 4.8 (6.7), 512 x 2048 5.7 (9.2), 512 x 16384 16.5 (22.1), in fp32 31.8 (30.2).
+// Rows whose gradient is one launch, though their columns' workgroups read dy and h once more: 16 x 2048 bfloat16 3.0
+// us (in two launches 5.9), 512 x 64 4.8 (6.7), 512 x 2048 5.7 (9.2), 512 x 16384 16.5 (22.1), in fp32 31.8 (30.2).
 constexpr int64_t FEW_ROWS = 512;
 BackPlan back_plan(int64_t T, int64_t n, int E) {
   BackPlan p;

@@ -84,3 +84,19 @@ def test_elements_on_borders(n, fmt, dtype):
         assert np.array_equal(scales.cpu().numpy()[0], byte)
         wrong = ref.unpack(codes.cpu().numpy()[0], fmt) != want
         assert not wrong.any(), (res is None, int(wrong.sum()))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=IDS)
+@pytest.mark.parametrize("n", [2, 7, 8, 263, 33000])
+def test_sums_of_16_bit_elements(n, fmt):
+    """1 + 2^-30 is 1 in fp32, so that y = +-gain lies on its border in rows of any length."""
+    table = ref.grid(fmt)
+    mid = (table[1:] + table[:-1]) / 2
+    rng = np.random.default_rng(n)
+    gain, sign = rng.choice(mid, n), torch.tensor(rng.choice([-1.0, 1.0], (20, n)))
+    gain[::32] = mid[-1]
+    res = (2.0**-30 * torch.tensor(rng.choice([-1.0, 0.0, 1.0], (20, n)))).to(DEV, torch.bfloat16)
+    want, byte = ref.quantize(sign.numpy() * gain, fmt)
+    _, _, codes, scales, _ = norm(sign.to(DEV, torch.bfloat16), res, torch.tensor(gain).float().to(DEV), fmt, eps=0.0)
+    assert np.array_equal(scales.cpu().numpy()[0], byte)
+    assert np.array_equal(ref.unpack(codes.cpu().numpy()[0], fmt), want)
